@@ -50,6 +50,8 @@ typedef enum { IDX_ROPE_NONE = 0, IDX_ROPE_NEOX = 1, IDX_ROPE_INTERLEAVED = 2 } 
 #define IDX_STATUS_BAD_PAGE 0x4     /* page-table entry outside [0, num_pages): tile skipped */
 #define IDX_STATUS_TIMEOUT 0x8      /* a bounded wait ran out: the CTA stopped early */
 #define IDX_STATUS_BAD_LEN 0x10     /* a sequence's key or query count broke its bound: skipped */
+#define IDX_STATUS_NO_PAGE 0x20     /* the free pages did not suffice for a request's new tokens */
+#define IDX_STATUS_BAD_VALUE 0x40   /* a NaN among the values to store: stored as 0 */
 
 /*
  * Page layout of the paged indexer K cache. This library owns it: callers learn it only
@@ -373,6 +375,131 @@ int idx_debug_mma_rate(int32_t dtype, int32_t iters, int32_t* dev_status, double
  * and returns; the context stays usable. *dev_status: a device int32 (required).
  */
 int idx_debug_wait_timeout(int32_t limit_us, int32_t* dev_status, cudaStream_t stream);
+
+/*
+ * Page tables, slot map, positions and lengths of a step, from the requests' lengths, on the
+ * GPU: the inputs of idx_k_store / idx_qk_prep / idx_kv_store, the scorers, the top-k and
+ * idx_attn_paged, so that a step needs no host round trip and can be replayed as a graph.
+ *   ctx_lens, q_lens: int32 [B]; request b has ctx_lens[b] tokens in the cache and gets
+ *     q_lens[b] new ones (0: none this step).
+ *   page_table: int32 [B][pt_stride]; entries 0 .. ceil(ctx/P) - 1 hold the request's pages.
+ *     In place, the call appends the pages that ctx + q tokens need: entries ceil(ctx/P) ..
+ *     ceil((ctx+q)/P) - 1. Nothing else of it is written, and the appended entries are not read.
+ *   free_pages: int32 [free_cap], page ids; free_span: int32 [2], the free ones are entries
+ *     free_span[0] .. free_span[1] - 1. Requests take theirs from the front in request order;
+ *     *free_next becomes the first entry not taken (the next step's free_span[0]).
+ *   Outputs: cu_seqlens_q int32 [B+1] (prefix sums of q_lens, at most T_cap); seq_lens_k int32
+ *     [B] = ctx + q; for each row t < T_cap: positions[t] (int32) = ctx + i and
+ *     slot_mapping[t] (int64) = page * P + position % P for the i-th new token of its request.
+ *     Rows behind the last request get position 0 and slot -1 (the stores skip them).
+ * A request whose lengths are negative or whose ctx + q is above max_seq_len_k, or whose rows
+ *   do not all fit below T_cap, sets IDX_STATUS_BAD_LEN; one whose pages the free list cannot
+ *   give (a request takes all of its pages or none, and none are given out behind the first
+ *   refusal) sets IDX_STATUS_NO_PAGE. Such a request gets no page, seq_lens_k 0, and its
+ *   rows get position 0 and slot -1; its rows below T_cap still count in cu_seqlens_q (a
+ *   negative q_len counts 0). A page id outside [0, num_pages) sets IDX_STATUS_BAD_PAGE and
+ *   gives slot -1; so does a free_span outside [0, free_cap], which is taken as empty.
+ * max_seq_len_k <= pt_stride * P. B <= 16384 (IDX_EUNSUPPORTED above). B = 0 or T_cap = 0 is
+ *   allowed. The outputs may not overlap the inputs or one another (IDX_EINVAL where the
+ *   base addresses are equal). Two launches: the second, empty one orders the step's following
+ *   calls, which read lengths and page tables before they wait for their predecessor, behind
+ *   the first.
+ */
+int idx_step_meta(const int32_t* ctx_lens, const int32_t* q_lens, int32_t B, int32_t* page_table,
+                  int32_t pt_stride, int32_t page_size, int32_t max_seq_len_k,
+                  const int32_t* free_pages, int32_t free_cap, const int32_t* free_span,
+                  int64_t num_pages, int32_t* cu_seqlens_q, int32_t* seq_lens_k,
+                  int32_t* positions, int64_t* slot_mapping, int64_t T_cap, int32_t* free_next,
+                  int32_t* dev_status, cudaStream_t stream);
+
+/*
+ * The 8-bit paged KV cache that idx_attn_paged reads and idx_kv_store fills (beside the
+ * indexer's own K cache; the two may share page tables and slots). D = 64 or 128, page size
+ * P = 64 or 128. A page holds its kv heads back to back, head_bytes = 2*P*D + 16 each:
+ *   token s of the head: its D K codes (e4m3) at s*2*D, its D V codes at s*2*D + D;
+ *   scale bytes at 2*P*D: byte 2*i is the K scale, byte 2*i + 1 the V scale of the head's
+ *   tokens 16*i .. 16*i + 15; a scale byte e stands for 2^(e - 127), e in 95 .. 175 (others,
+ *   which idx_kv_store never writes, are read as the nearest of these).
+ * A value is code * 2^(e - 127).
+ */
+typedef struct {
+    int64_t page_bytes;     /* kv_heads * head_bytes */
+    int64_t head_bytes;     /* 2*P*D + 16 */
+    int64_t scale_offset;   /* of the scale bytes in a head's part: 2*P*D */
+    int32_t scale_block;    /* tokens that share a scale: 16 */
+    int32_t page_size, kv_heads, head_dim;
+} idx_kv_layout_t;
+
+typedef enum { IDX_BF16 = 0, IDX_FP16 = 1 } idx_ftype; /* element type of q, k, v and out */
+
+int idx_kv_layout(int32_t kv_heads, int32_t head_dim, int32_t page_size, idx_kv_layout_t* out);
+
+/*
+ * K and V rows into the 8-bit paged cache. Row r < n_rows, head h < kv_heads: D values at
+ * k + r*k_row_stride + h*k_head_stride (elements; v alike), 16-byte aligned, strides >= 0 and
+ * multiples of 8. slot_mapping int64 [n_rows]: slot = page * P + in-page token, < 0 skips the row, one
+ * past the pool sets IDX_STATUS_BAD_SLOT and skips it.
+ * Scale of a 16-token block, per head and side (K, V): 2^E with the least E in [-32, 48] for
+ *   which the block's largest finite magnitude is <= 448 * 2^E (zeros alone: E = -32). Code =
+ *   value * 2^-E rounded to nearest-even e4m3, saturating at 448. An infinity is stored as the
+ *   largest code; a NaN is stored as 0 and sets IDX_STATUS_BAD_VALUE.
+ * Appending: tokens of a block below the lowest slot that the call writes in it are kept. When
+ *   the new rows need a larger E, the kept codes are rescaled by the power of two and rounded
+ *   again (exact but for values that become subnormal). A block whose first token the call
+ *   writes starts afresh: its old scale does not count. Tokens above the lowest slot that the
+ *   call does not write are no longer defined, so rolling back and writing again is allowed.
+ * Rows of one block have to be adjacent in slot_mapping, in increasing slot order, as
+ *   idx_step_meta gives them. A row whose predecessor is in its block at a slot that is not
+ *   lower sets IDX_STATUS_BAD_SLOT and it and the block's rows behind it are skipped; if rows of one block are
+ *   apart, that block's contents are unspecified.
+ */
+int idx_kv_store(const void* k, const void* v, int32_t ftype, int64_t n_rows, int32_t kv_heads,
+                 int32_t head_dim, int64_t k_row_stride, int64_t k_head_stride,
+                 int64_t v_row_stride, int64_t v_head_stride, const int64_t* slot_mapping,
+                 void* pool, int64_t num_pages, int32_t page_size, int64_t page_stride,
+                 int32_t* dev_status, cudaStream_t stream);
+
+/*
+ * Softmax attention over the 8-bit paged KV cache, for decode, chunked and whole prefill, over
+ * every visible key or over the keys that the indexer selected:
+ *   s_j = softmax_scale * q[t,h] . k_j;  out[t,h] = sum_j softmax(s)_j v_j;
+ *   lse[t,h] = ln sum_j exp(s_j)
+ * over the keys j that query t sees (visible rule, cu_seqlens_q, seq_lens_k, page_table, causal,
+ * max_q_len and max_seq_len_k as in idx_mqa_logits_paged) and, when sel_idx is given, that
+ * sel_idx[t*sel_stride .. + n_sel - 1] lists (int32 key positions in the sequence, any order:
+ * the output of idx_topk, idx_mqa_topk_paged or idx_mqa_topk_cand_paged). Entries that are
+ * negative or not visible are ignored; a position listed twice counts twice.
+ *   q: [T][Hq][D] at q + t*q_row_stride + h*q_head_stride; out alike with its own strides (elements; 16-byte
+ *     aligned, strides multiples of 8; out strides >= D); both of type ftype. Query head h reads kv
+ *     head h / (Hq / kv_heads); Hq is a multiple of kv_heads. lse: fp32 [T][Hq], may be NULL.
+ *   softmax_scale: finite, > 0.
+ * A row that sees no key gets out 0 and lse -inf. Rows of no sequence (behind cu_seqlens_q[B]) are
+ *   left as they were, and so are the rows of a sequence that breaks its length bounds
+ *   (IDX_STATUS_BAD_LEN). Keys of a page outside the pool are skipped (IDX_STATUS_BAD_PAGE). A query
+ *   row that holds an infinity or a NaN gives NaN in that row. What the cache holds in slots that a row
+ *   does not see (NaN codes too) does not reach it.
+ * Arithmetic: q is scaled by a power of two per row and held in fp16 (exact for fp16 and, but for
+ *   values below 2^-28 of the row's largest, for bf16), products and sums in fp32; the softmax
+ *   weights are rounded to fp16 (2^-11 relative, half a step) for the product with v.
+ * workspace: optional device memory, 256-byte aligned, no starting value needed: partial results of a key axis
+ *   that is split over CTAs when the rows alone do not fill the GPU. idx_attn_workspace_bytes
+ *   gives the size that the splitting would like; with less (or NULL) it splits less. One
+ *   workspace serves one call at a time. The split, and so the order of sums, depends on the
+ *   arguments' sizes alone: same call, same bits.
+ */
+int idx_attn_workspace_bytes(int64_t T, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t B,
+                             int32_t max_q_len, int32_t max_seq_len_k, int32_t n_sel,
+                             size_t* bytes);
+
+int idx_attn_paged(const void* q, int32_t ftype, int64_t T, int32_t q_heads, int32_t kv_heads,
+                   int32_t head_dim, int64_t q_row_stride, int64_t q_head_stride, const void* pool,
+                   int64_t num_pages, int32_t page_size, int64_t page_stride,
+                   const int32_t* page_table, int32_t pt_stride, const int32_t* seq_lens_k,
+                   const int32_t* cu_seqlens_q, int32_t B, int32_t causal, int32_t max_q_len,
+                   int32_t max_seq_len_k, const int32_t* sel_idx, int64_t sel_stride,
+                   int32_t n_sel, float softmax_scale, void* out, int64_t out_row_stride,
+                   int64_t out_head_stride, float* lse, void* workspace, size_t workspace_bytes,
+                   int32_t* dev_status, cudaStream_t stream);
 
 /* Human-readable name of an idx_status value (static string). */
 const char* idx_status_string(int status);

@@ -18,6 +18,8 @@ IDX_MXFP4, IDX_FP8 = 0, 1
 IDX_ROPE_NONE, IDX_ROPE_NEOX, IDX_ROPE_INTERLEAVED = 0, 1, 2
 IDX_STATUS_BAD_SLOT, IDX_STATUS_BAD_POS, IDX_STATUS_BAD_PAGE = 0x1, 0x2, 0x4
 IDX_STATUS_TIMEOUT, IDX_STATUS_BAD_LEN = 0x8, 0x10
+IDX_STATUS_NO_PAGE, IDX_STATUS_BAD_VALUE = 0x20, 0x40
+IDX_BF16, IDX_FP16 = 0, 1
 
 HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include",
                       "idx.h")
@@ -37,6 +39,12 @@ class IdxLayout(C.Structure):
                 ("code_bytes", C.c_int64), ("scale_offset", C.c_int64),
                 ("scale_bytes", C.c_int64), ("bytes_per_token", C.c_int32),
                 ("page_size", C.c_int32)]
+
+
+class IdxKvLayout(C.Structure):
+    _fields_ = [("page_bytes", C.c_int64), ("head_bytes", C.c_int64), ("scale_offset", C.c_int64),
+                ("scale_block", C.c_int32), ("page_size", C.c_int32), ("kv_heads", C.c_int32),
+                ("head_dim", C.c_int32)]
 
 
 def library_path() -> str:
@@ -93,11 +101,21 @@ def _declare(L):
     L.idx_debug_wait_timeout.argtypes = [i32, vp, vp]
     L.idx_compress_k_store.argtypes = [vp, vp, i64, i64, vp, vp, i64, i32, vp, vp, vp, i32, i32, i32,
                                        vp, vp, f32, i32, vp, i64, i32, i64, vp, vp]
+    L.idx_step_meta.argtypes = [vp, vp, i32, vp, i32, i32, i32, vp, i32, vp, i64, vp, vp, vp, vp, i64,
+                                vp, vp, vp]
+    L.idx_kv_layout.argtypes = [i32, i32, i32, C.POINTER(IdxKvLayout)]
+    L.idx_kv_store.argtypes = [vp, vp, i32, i64, i32, i32, i64, i64, i64, i64, vp, vp, i64, i32, i64, vp,
+                               vp]
+    L.idx_attn_workspace_bytes.argtypes = [i64, i32, i32, i32, i32, i32, i32, i32, C.POINTER(C.c_size_t)]
+    L.idx_attn_paged.argtypes = [vp, i32, i64, i32, i32, i32, i64, i64, vp, i64, i32, i64, vp, i32, vp, vp,
+                                 i32, i32, i32, i32, vp, i64, i32, f32, vp, i64, i64, vp, vp, C.c_size_t,
+                                 vp, vp]
     for n in ("idx_cache_layout", "idx_k_store", "idx_q_quant", "idx_qk_prep", "idx_mqa_logits_paged",
               "idx_topk", "idx_debug_encode", "idx_mqa_topk_workspace_bytes", "idx_mqa_topk_paged",
               "idx_debug_mma_rate", "idx_mqa_topk_paged_noalloc", "idx_compress_k_store",
               "idx_mqa_topk_cand_workspace_bytes", "idx_mqa_topk_cand_paged",
-              "idx_mqa_logits_workspace_bytes", "idx_debug_wait_timeout"):
+              "idx_mqa_logits_workspace_bytes", "idx_debug_wait_timeout", "idx_step_meta", "idx_kv_layout",
+              "idx_kv_store", "idx_attn_workspace_bytes", "idx_attn_paged"):
         getattr(L, n).restype = C.c_int
 
 
@@ -281,3 +299,116 @@ def idx_mqa_topk_paged_noalloc(q_codes, q_scales, w, dtype, pool, num_pages, pag
         page_stride, _ptr(page_table), page_table.shape[1], _ptr(seq_lens_k), _ptr(cu_seqlens_q),
         seq_lens_k.shape[0], int(causal), max_q_len, max_seq_len_k, k, _ptr(out_idx),
         _ptr(dev_status), _stream(stream)))
+
+
+def _need(fn, name, x, dtype, ndim=None, contiguous=True):
+    """Refuse a tensor whose type or layout the pointer alone would not tell the library, or that
+    lies on another device than the current one (where the call is launched)."""
+    import torch
+    if x.dtype != dtype or (ndim is not None and x.dim() != ndim) or (contiguous and not x.is_contiguous()):
+        raise ValueError(f"{fn}: {name} has to be {dtype}"
+                         f"{'' if ndim is None else f' with {ndim} dimensions'}"
+                         f"{', contiguous' if contiguous else ''}; got {x.dtype}, shape "
+                         f"{tuple(x.shape)}, strides {x.stride()}")
+    if not x.is_cuda or x.device.index != torch.cuda.current_device():
+        raise ValueError(f"{fn}: {name} is on {x.device}, not on the current CUDA device")
+
+
+def _ftype(fn, x):
+    import torch
+    if x.dtype == torch.bfloat16:
+        return IDX_BF16
+    if x.dtype == torch.float16:
+        return IDX_FP16
+    raise ValueError(f"{fn}: {x.dtype} is neither bfloat16 nor float16")
+
+
+def idx_step_meta(ctx_lens, q_lens, page_table, page_size, max_seq_len_k, free_pages, free_span, num_pages,
+                  cu_seqlens_q, seq_lens_k, positions, slot_mapping, free_next, dev_status=None,
+                  stream=None):
+    """Page tables, slot map, positions and lengths of a step; T_cap = len(slot_mapping)."""
+    import torch
+    i32, fn = torch.int32, "idx_step_meta"
+    B, T = ctx_lens.shape[0], slot_mapping.shape[0]
+    for name, x, d in (("ctx_lens", ctx_lens, 1), ("q_lens", q_lens, 1), ("page_table", page_table, 2),
+                       ("free_pages", free_pages, 1), ("free_span", free_span, 1), ("cu_seqlens_q", cu_seqlens_q, 1),
+                       ("seq_lens_k", seq_lens_k, 1), ("positions", positions, 1), ("free_next", free_next, 1)):
+        _need(fn, name, x, i32, d)
+    _need(fn, "slot_mapping", slot_mapping, torch.int64, 1)
+    if (q_lens.shape[0] != B or page_table.shape[0] != B or seq_lens_k.shape[0] != B or cu_seqlens_q.shape[0] != B + 1
+            or positions.shape[0] != T or free_span.shape[0] != 2 or free_next.shape[0] != 1):
+        raise ValueError(f"{fn}: shapes do not belong to {B} requests and {T} rows")
+    _check(fn, load().idx_step_meta(
+        _ptr(ctx_lens), _ptr(q_lens), B, _ptr(page_table), page_table.shape[1], page_size, max_seq_len_k,
+        _ptr(free_pages), free_pages.shape[0], _ptr(free_span), num_pages, _ptr(cu_seqlens_q), _ptr(seq_lens_k),
+        _ptr(positions), _ptr(slot_mapping), T, _ptr(free_next), _ptr(dev_status), _stream(stream)))
+
+
+def idx_kv_layout(kv_heads: int, head_dim: int, page_size: int) -> IdxKvLayout:
+    out = IdxKvLayout()
+    _check("idx_kv_layout", load().idx_kv_layout(kv_heads, head_dim, page_size, C.byref(out)))
+    return out
+
+
+def idx_kv_store(k, v, slot_mapping, pool, num_pages, page_size, page_stride, dev_status=None, stream=None):
+    """k, v: bf16 or fp16 [rows, kv_heads, head_dim], last dimension dense, the others strided."""
+    import torch
+    fn = "idx_kv_store"
+    ft = _ftype(fn, k)
+    _need(fn, "k", k, k.dtype, 3, False)
+    _need(fn, "v", v, k.dtype, 3, False)
+    _need(fn, "slot_mapping", slot_mapping, torch.int64, 1)
+    n, H, D = k.shape
+    if v.shape != k.shape or slot_mapping.shape[0] != n:
+        raise ValueError(f"{fn}: k {tuple(k.shape)}, v {tuple(v.shape)} and {slot_mapping.shape[0]} slots do not match")
+    if n > 0 and (k.stride(2) != 1 or v.stride(2) != 1):
+        raise ValueError(f"{fn}: the last dimension of k and v has to be dense")
+    _check(fn, load().idx_kv_store(
+        _ptr(k), _ptr(v), ft, n, H, D, k.stride(0), k.stride(1), v.stride(0), v.stride(1), _ptr(slot_mapping),
+        _ptr(pool), num_pages, page_size, page_stride, _ptr(dev_status), _stream(stream)))
+
+
+def idx_attn_workspace_bytes(T, q_heads, kv_heads, head_dim, B, max_q_len, max_seq_len_k, n_sel=0) -> int:
+    n = C.c_size_t(0)
+    _check("idx_attn_workspace_bytes", load().idx_attn_workspace_bytes(
+        T, q_heads, kv_heads, head_dim, B, max_q_len, max_seq_len_k, n_sel, C.byref(n)))
+    return int(n.value)
+
+
+def idx_attn_paged(q, pool, num_pages, page_size, page_stride, kv_heads, page_table, seq_lens_k, cu_seqlens_q,
+                   causal, max_q_len, max_seq_len_k, softmax_scale, out, lse=None, sel_idx=None, workspace=None,
+                   dev_status=None, stream=None):
+    """q, out: bf16 or fp16 [T, q_heads, head_dim], last dimension dense, the others strided;
+    sel_idx: int32 [T, n_sel], rows strided (the top-k's output), or None for every visible key."""
+    import torch
+    fn, i32 = "idx_attn_paged", torch.int32
+    ft = _ftype(fn, q)
+    _need(fn, "q", q, q.dtype, 3, False)
+    _need(fn, "out", out, q.dtype, 3, False)
+    _need(fn, "page_table", page_table, i32, 2)
+    _need(fn, "seq_lens_k", seq_lens_k, i32, 1)
+    _need(fn, "cu_seqlens_q", cu_seqlens_q, i32, 1)
+    T, H, D = q.shape
+    B = seq_lens_k.shape[0]
+    if out.shape != q.shape or page_table.shape[0] != B or cu_seqlens_q.shape[0] != B + 1:
+        raise ValueError(f"{fn}: q {tuple(q.shape)}, out {tuple(out.shape)}, page_table {tuple(page_table.shape)}, "
+                         f"seq_lens_k {B} and cu_seqlens_q {cu_seqlens_q.shape[0]} do not match")
+    if T > 0 and (q.stride(2) != 1 or out.stride(2) != 1):
+        raise ValueError(f"{fn}: the last dimension of q and out has to be dense")
+    sel_stride = n_sel = 0
+    if lse is not None:
+        _need(fn, "lse", lse, torch.float32, 2)
+        if lse.shape != (T, H):
+            raise ValueError(f"{fn}: lse is {tuple(lse.shape)}, not {(T, H)}")
+    if sel_idx is not None:
+        _need(fn, "sel_idx", sel_idx, i32, 2, False)
+        n_sel, sel_stride = sel_idx.shape[1], max(sel_idx.stride(0), sel_idx.shape[1])
+        if sel_idx.shape[0] != T or (T > 0 and n_sel > 1 and sel_idx.stride(1) != 1) or \
+                (T > 1 and sel_idx.stride(0) < n_sel):
+            raise ValueError(f"{fn}: sel_idx {tuple(sel_idx.shape)} with strides {sel_idx.stride()}")
+    wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(fn, load().idx_attn_paged(
+        _ptr(q), ft, T, H, kv_heads, D, q.stride(0), q.stride(1), _ptr(pool), num_pages, page_size, page_stride,
+        _ptr(page_table), page_table.shape[1], _ptr(seq_lens_k), _ptr(cu_seqlens_q), B, int(causal), max_q_len,
+        max_seq_len_k, _ptr(sel_idx), sel_stride, n_sel, softmax_scale, _ptr(out), out.stride(0), out.stride(1),
+        _ptr(lse), _ptr(workspace), wsb, _ptr(dev_status), _stream(stream)))

@@ -3,28 +3,17 @@
 #include <algorithm>
 #include <cmath>
 
-#include <nvtx3/nvToolsExt.h>
-
 #include "../../include/idx.h"
+#include "api_util.h"
 #include "kernels.h"
 
 namespace {
 
-// One NVTX range per entry point call (visible in Nsight timelines; near free otherwise).
-struct Range {
-    explicit Range(const char* name) { nvtxRangePushA(name); }
-    ~Range() { nvtxRangePop(); }
-    Range(const Range&) = delete;
-    Range& operator=(const Range&) = delete;
-};
-
-inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 inline bool valid_dtype(int32_t d) { return d == IDX_MXFP4 || d == IDX_FP8; }
 inline bool valid_rope(int32_t r) {
     return r == IDX_ROPE_NONE || r == IDX_ROPE_NEOX || r == IDX_ROPE_INTERLEAVED;
 }
 inline int64_t page_bytes(int32_t dtype, int32_t P) { return (dtype == IDX_MXFP4 ? 68 : 132) * (int64_t)P; }
-inline int cuda_status(cudaError_t e) { return e == cudaSuccess ? IDX_OK : IDX_ECUDA; }
 constexpr size_t kLogitsWorkspaceBytes = 256;  // the decode schedule's two counters, padded
 
 // common pool checks: page size, stride, alignment

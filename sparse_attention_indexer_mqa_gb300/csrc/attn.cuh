@@ -1,0 +1,89 @@
+// attn.cuh -- what the attention kernels over the 8-bit paged KV cache share: the row rules, the
+// numbers of the running softmax and the output writes.
+//
+// The softmax that every kernel keeps. With s = q . k_code (fp32 sum), c = softmax_scale * log2(e)
+// * (q's power of two) * 2^Ek and Ev the exponent of the key's V block,
+//     u = s * c + Ev,   p' = 2^(u - m + kShift),   O += p' * v_code,   l += p' * 2^-Ev:
+// V's scale is part of the weight, so both products run on bare codes and nothing has to be
+// scaled element by element. m follows the largest u; it is raised only when a u passes it by more than
+// kLazy, since raising it means rescaling O and l. p' <= 2^(kShift + kLazy) = 2^15 stays in fp16's
+// range, and weights down to 2^-26 of the largest keep fp16's full 11 bits.
+//     out = O / l,   lse = ln 2 * (m - kShift + log2 l).
+// |Ev| <= 48, so that p' and p' * 2^-Ev can only underflow where the weight is below 2^-46 of
+// the row's largest.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "kernels.h"
+#include "kv.cuh"
+
+namespace idx {
+
+constexpr float kShift = 12.0f, kLazy = 3.0f;
+constexpr float kLn2 = 0.693147180559945309f, kLog2e = 1.44269504088896341f;
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
+
+__device__ __forceinline__ float lse_of(float m, float l) {
+    return l == 0.0f ? neg_inf() : kLn2 * (m - kShift + log2f(l));
+}
+
+// A block's two scale bytes (K low, V high; 127 + E): 2^Ek, and Ev. Bytes that the store does not write
+// are taken as the nearest that it does.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t e) {
+    return min(max(e & 255u, 127u + kKvEMin), 127u + kKvEMax);
+}
+__device__ __forceinline__ float k_scale(uint32_t two) { return __uint_as_float(scale_byte(two) << 23); }
+__device__ __forceinline__ float v_exponent(uint32_t two) { return (float)((int)scale_byte(two >> 8) - 127); }
+
+// A sequence's rows: its first query row and how many, or nq = -1 if it breaks its bounds.
+struct SeqRows {
+    int64_t t0;
+    int32_t nq, len;
+};
+__device__ __forceinline__ SeqRows seq_rows(const AttnArgs& a, int b) {
+    SeqRows s;
+    const int32_t c0 = a.cu_seqlens_q[b], c1 = a.cu_seqlens_q[b + 1];
+    s.len = a.seq_lens_k[b];
+    s.t0 = c0;
+    s.nq = c1 - c0;
+    if (c0 < 0 || c1 < c0 || c1 > a.T || s.nq > a.max_q_len || s.len < 0 || s.len > a.max_seq_len_k) s.nq = -1;
+    return s;
+}
+
+// Power of two that brings a row of q with the given largest magnitude into fp16's range (its
+// largest value to [2^14, 2^15)), and the exponent it takes away. fp16 rows stay as they are.
+template <bool kHalf>
+__device__ __forceinline__ int q_exponent(float amax) {
+    if constexpr (kHalf) return 0;
+    const int e = (int)(__float_as_uint(amax) >> 23) - 127;
+    return amax > 0.0f ? max(e, -100) - 14 : 0;
+}
+
+template <bool kHalf>
+__device__ __forceinline__ float2 load_pair(uint32_t w) {
+    if constexpr (kHalf) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+    return make_float2(bf16_lo(w), bf16_hi(w));
+}
+template <bool kHalf>
+__device__ __forceinline__ uint32_t store_pair(float x, float y) {
+    if constexpr (kHalf) {
+        const __half2 h = __floats2half2_rn(x, y);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t half2_bits(float x, float y) {
+    const __half2 h = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+}  // namespace idx

@@ -144,6 +144,78 @@ cudaError_t launch_scorer_prefill_select(const ScoreArgs& a, cudaStream_t st);
 int prefill_queries_per_block(int32_t H);
 int device_sm_count();
 
+// Step metadata (idx_step_meta).
+struct MetaArgs {
+    const int32_t* ctx_lens;
+    const int32_t* q_lens;
+    int32_t B;
+    int32_t* page_table;
+    int32_t pt_stride, page_size, max_seq_len_k;
+    const int32_t* free_pages;
+    int32_t free_cap;
+    const int32_t* free_span;
+    int64_t num_pages;
+    int32_t* cu_seqlens_q;
+    int32_t* seq_lens_k;
+    int32_t* positions;
+    int64_t* slot_mapping;
+    int64_t T_cap;
+    int32_t* free_next;
+    int32_t* dev_status;
+};
+cudaError_t launch_step_meta(const MetaArgs& a, cudaStream_t st);
+
+// K and V rows into the 8-bit paged KV cache (idx_kv_store); strides in elements.
+struct KvStoreArgs {
+    const uint16_t* k;
+    const uint16_t* v;
+    int32_t ftype;
+    int64_t n_rows;
+    int32_t kv_heads, head_dim;
+    int64_t k_row_stride, k_head_stride, v_row_stride, v_head_stride;
+    const int64_t* slot_mapping;
+    uint8_t* pool;
+    int64_t num_pages;
+    int32_t page_size;
+    int64_t page_stride;
+    int32_t* dev_status;
+};
+cudaError_t launch_kv_store(const KvStoreArgs& a, cudaStream_t st);
+
+// Attention over that cache (idx_attn_paged); strides in elements.
+struct AttnArgs {
+    const uint16_t* q;
+    int32_t ftype;
+    int64_t T;
+    int32_t q_heads, kv_heads, head_dim, group;  // group = q_heads / kv_heads
+    int64_t q_row_stride, q_head_stride;
+    const uint8_t* pool;
+    int64_t num_pages;
+    int32_t page_size;
+    int64_t page_stride;
+    const int32_t* page_table;
+    int32_t pt_stride;
+    const int32_t* seq_lens_k;
+    const int32_t* cu_seqlens_q;
+    int32_t B, causal, max_q_len, max_seq_len_k;
+    const int32_t* sel;
+    int64_t sel_stride;
+    int32_t n_sel;
+    float scale;
+    uint16_t* out;
+    int64_t out_row_stride, out_head_stride;
+    float* lse;
+    int32_t* dev_status;
+    // key axis split: split z takes keys (or list entries) z * chunk .. ; with n_split > 1 the
+    // kernels write O and (m, l) of each split there and the combine kernel joins them
+    int32_t n_split, chunk;
+    float* part_o;    // [n_split][T][q_heads][head_dim]
+    float2* part_ml;  // [n_split][T][q_heads]
+};
+// Fills n_split and chunk for at most `bytes` of workspace (0: none); bytes the split wants.
+int64_t attn_plan(AttnArgs& a, int64_t bytes);
+cudaError_t launch_attn(const AttnArgs& a, cudaStream_t st);
+
 // Bounded-wait test hook (idx_debug_wait_timeout).
 cudaError_t launch_wait_timeout(int32_t limit_us, int32_t* status, cudaStream_t st);
 
