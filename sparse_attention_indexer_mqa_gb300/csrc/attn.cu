@@ -485,6 +485,11 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a) {
     if (a.lse && lane == 0) a.lse[row] = lse_of(M, L);
 }
 
+// Rows that share their keys: those of a sequence and a kv head, or with a list those of a query's group.
+int64_t shared_rows(const AttnArgs& a) { return a.n_sel ? a.group : (int64_t)a.max_q_len * a.group; }
+// More rows than one mma.sync tile: the tensor-memory kernel.
+bool use_tile(const AttnArgs& a) { return shared_rows(a) > 16; }
+
 template <int D, bool kHalf, bool kSel>
 cudaError_t launch_rows(const AttnArgs& a, cudaStream_t st) {
     constexpr int smem = Ring<D, kSel>::kBytes;
@@ -499,7 +504,9 @@ cudaError_t launch_rows(const AttnArgs& a, cudaStream_t st) {
 
 template <int D, bool kHalf>
 cudaError_t launch_d(const AttnArgs& a, cudaStream_t st) {
-    cudaError_t e = a.sel ? launch_rows<D, kHalf, true>(a, st) : launch_rows<D, kHalf, false>(a, st);
+    cudaError_t e = use_tile(a) ? launch_attn_tile(a, st)
+                    : a.sel     ? launch_rows<D, kHalf, true>(a, st)
+                                : launch_rows<D, kHalf, false>(a, st);
     if (e != cudaSuccess || a.n_split <= 1) return e;
     const int64_t rows = a.T * a.q_heads;
     return launch_pdl(attn_join_kernel<D, kHalf>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, st, a);
@@ -508,26 +515,28 @@ cudaError_t launch_d(const AttnArgs& a, cudaStream_t st) {
 }  // namespace
 
 int64_t attn_plan(AttnArgs& a, int64_t bytes) {
-    // Units without a split, against three resident CTAs on each SM, two rounds of them.
     const int sms = device_sm_count();
     if (sms <= 0) return -1;
-    const int64_t units = (a.n_sel ? a.T * ((a.group + 15) / 16) : a.B * (((int64_t)a.max_q_len * a.group + 15) / 16)) *
-                          a.kv_heads;
+    const bool tile = use_tile(a);
+    const int64_t per_unit = tile ? 128 : 16;
+    const int64_t units = (a.n_sel ? a.T : a.B) * ((shared_rows(a) + per_unit - 1) / per_unit) * a.kv_heads;
     const int64_t keys = a.n_sel ? a.n_sel : a.max_seq_len_k;
     const int64_t per_split = a.T * a.q_heads * (a.head_dim + 2) * 4;
-    int64_t want = units > 0 ? (6ll * sms + units - 1) / units : 1;
-    want = want < (keys + 255) / 256 ? want : (keys + 255) / 256;  // 4 steps of 64 keys at least
+    // two rounds of resident CTAs (three or two to an SM), four steps of keys to a CTA at least
+    const int64_t slots = 2ll * sms * (tile ? 2 : 3), least = tile ? 512 : 256;
+    int64_t want = units > 0 ? (slots + units - 1) / units : 1;
+    want = want < (keys + least - 1) / least ? want : (keys + least - 1) / least;
     want = want > 64 ? 64 : want;
     if (want < 1) want = 1;
     const int64_t fits = per_split > 0 ? bytes / per_split : 1;
     int64_t n = want < fits ? want : fits;
     if (n < 1) n = 1;
-    int64_t chunk = ((keys + n - 1) / n + 63) / 64 * 64;
-    if (chunk < 64) chunk = 64;
+    int64_t chunk = ((keys + n - 1) / n + 127) / 128 * 128;  // whole steps and pages
+    if (chunk < 128) chunk = 128;
     n = (keys + chunk - 1) / chunk;
     if (n < 1) n = 1;
     a.n_split = (int32_t)n;
-    a.chunk = (int32_t)(chunk > INT32_MAX - 64 ? INT32_MAX - 63 : chunk);
+    a.chunk = (int32_t)chunk;
     return want > 1 ? want * per_split : 0;
 }
 

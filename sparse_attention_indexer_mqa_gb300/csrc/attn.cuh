@@ -38,7 +38,7 @@ __device__ __forceinline__ float lse_of(float m, float l) {
 // A block's two scale bytes (K low, V high; 127 + E): 2^Ek, and Ev. Bytes that the store does not write
 // are taken as the nearest that it does.
 __device__ __forceinline__ uint32_t scale_byte(uint32_t e) {
-    return min(max(e & 255u, 127u + kKvEMin), 127u + kKvEMax);
+    return min(max(e & 255u, (uint32_t)(127 + kKvEMin)), (uint32_t)(127 + kKvEMax));
 }
 __device__ __forceinline__ float k_scale(uint32_t two) { return __uint_as_float(scale_byte(two) << 23); }
 __device__ __forceinline__ float v_exponent(uint32_t two) { return (float)((int)scale_byte(two >> 8) - 127); }

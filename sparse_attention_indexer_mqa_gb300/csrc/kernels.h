@@ -215,6 +215,7 @@ struct AttnArgs {
 // Fills n_split and chunk for at most `bytes` of workspace (0: none); bytes the split wants.
 int64_t attn_plan(AttnArgs& a, int64_t bytes);
 cudaError_t launch_attn(const AttnArgs& a, cudaStream_t st);
+cudaError_t launch_attn_tile(const AttnArgs& a, cudaStream_t st);  // many rows per kv head (attn_tc.cu)
 
 // Bounded-wait test hook (idx_debug_wait_timeout).
 cudaError_t launch_wait_timeout(int32_t limit_us, int32_t* status, cudaStream_t st);
