@@ -54,6 +54,8 @@ def library_path() -> str:
 def load(build_if_missing: bool = True):
     """Load (building first if needed) the CUDA library; raises if that is impossible."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.LIB
@@ -134,9 +136,23 @@ def _ptr(x):
     return x.data_ptr()
 
 
+_torch = None       # the module, once something needs it
+_raw_stream = None  # torch's current stream of a device as a handle, without a Stream object
+
+
+def _load_torch():
+    global _torch, _raw_stream
+    import torch
+    _torch = torch
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return torch
+
+
 def _stream(stream):
     if stream is None:
-        import torch
+        torch = _torch or _load_torch()
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -301,24 +317,28 @@ def idx_mqa_topk_paged_noalloc(q_codes, q_scales, w, dtype, pool, num_pages, pag
         _ptr(dev_status), _stream(stream)))
 
 
-def _need(fn, name, x, dtype, ndim=None, contiguous=True):
-    """Refuse a tensor whose type or layout the pointer alone would not tell the library, or that
-    lies on another device than the current one (where the call is launched)."""
-    import torch
-    if x.dtype != dtype or (ndim is not None and x.dim() != ndim) or (contiguous and not x.is_contiguous()):
-        raise ValueError(f"{fn}: {name} has to be {dtype}"
-                         f"{'' if ndim is None else f' with {ndim} dimensions'}"
-                         f"{', contiguous' if contiguous else ''}; got {x.dtype}, shape "
-                         f"{tuple(x.shape)}, strides {x.stride()}")
-    if not x.is_cuda or x.device.index != torch.cuda.current_device():
-        raise ValueError(f"{fn}: {name} is on {x.device}, not on the current CUDA device")
+def _device():
+    torch = _torch or _load_torch()
+    try:
+        return torch.cuda.current_device()
+    except (RuntimeError, AssertionError):  # no CUDA device: no tensor is on it
+        return -2
 
+
+def _refuse(fn, name, x, dtype, ndim, dense):
+    raise ValueError(f"{fn}: {name} has to be {dtype} with {ndim} dimensions{', contiguous' if dense else ''}, on the "
+                     f"current CUDA device; got {x.dtype}, shape {tuple(x.shape)}, strides {x.stride()}, {x.device}")
+
+
+# The checks of a tensor's type, rank, layout and device that its pointer does not tell the library
+# (calls are launched on the current device) are written out in each function: a helper per tensor would
+# double the host's share of a small call.
 
 def _ftype(fn, x):
-    import torch
-    if x.dtype == torch.bfloat16:
+    torch = _torch or _load_torch()
+    if x.dtype is torch.bfloat16:
         return IDX_BF16
-    if x.dtype == torch.float16:
+    if x.dtype is torch.float16:
         return IDX_FP16
     raise ValueError(f"{fn}: {x.dtype} is neither bfloat16 nor float16")
 
@@ -327,21 +347,29 @@ def idx_step_meta(ctx_lens, q_lens, page_table, page_size, max_seq_len_k, free_p
                   cu_seqlens_q, seq_lens_k, positions, slot_mapping, free_next, dev_status=None,
                   stream=None):
     """Page tables, slot map, positions and lengths of a step; T_cap = len(slot_mapping)."""
-    import torch
-    i32, fn = torch.int32, "idx_step_meta"
-    B, T = ctx_lens.shape[0], slot_mapping.shape[0]
-    for name, x, d in (("ctx_lens", ctx_lens, 1), ("q_lens", q_lens, 1), ("page_table", page_table, 2),
-                       ("free_pages", free_pages, 1), ("free_span", free_span, 1), ("cu_seqlens_q", cu_seqlens_q, 1),
-                       ("seq_lens_k", seq_lens_k, 1), ("positions", positions, 1), ("free_next", free_next, 1)):
-        _need(fn, name, x, i32, d)
-    _need(fn, "slot_mapping", slot_mapping, torch.int64, 1)
-    if (q_lens.shape[0] != B or page_table.shape[0] != B or seq_lens_k.shape[0] != B or cu_seqlens_q.shape[0] != B + 1
-            or positions.shape[0] != T or free_span.shape[0] != 2 or free_next.shape[0] != 1):
+    fn, dev = "idx_step_meta", _device()
+    i32 = _torch.int32
+    for x in (ctx_lens, q_lens, free_pages, free_span, cu_seqlens_q, seq_lens_k, positions, free_next):
+        if x.dtype is not i32 or x.dim() != 1 or x.get_device() != dev or not x.is_contiguous():
+            _refuse(fn, "every list of lengths, pages or positions", x, i32, 1, True)
+    if page_table.dtype is not i32 or page_table.dim() != 2 or page_table.get_device() != dev or \
+            not page_table.is_contiguous():
+        _refuse(fn, "page_table", page_table, i32, 2, True)
+    if slot_mapping.dtype is not _torch.int64 or slot_mapping.dim() != 1 or slot_mapping.get_device() != dev or \
+            not slot_mapping.is_contiguous():
+        _refuse(fn, "slot_mapping", slot_mapping, _torch.int64, 1, True)
+    B, T = len(ctx_lens), len(slot_mapping)
+    rows, width = page_table.shape
+    if (len(q_lens) != B or rows != B or len(seq_lens_k) != B or len(cu_seqlens_q) != B + 1 or len(positions) != T
+            or len(free_span) != 2 or len(free_next) != 1):
         raise ValueError(f"{fn}: shapes do not belong to {B} requests and {T} rows")
-    _check(fn, load().idx_step_meta(
-        _ptr(ctx_lens), _ptr(q_lens), B, _ptr(page_table), page_table.shape[1], page_size, max_seq_len_k,
-        _ptr(free_pages), free_pages.shape[0], _ptr(free_span), num_pages, _ptr(cu_seqlens_q), _ptr(seq_lens_k),
-        _ptr(positions), _ptr(slot_mapping), T, _ptr(free_next), _ptr(dev_status), _stream(stream)))
+    st = (_lib or load()).idx_step_meta(
+        ctx_lens.data_ptr(), q_lens.data_ptr(), B, page_table.data_ptr(), width, page_size, max_seq_len_k,
+        free_pages.data_ptr(), len(free_pages), free_span.data_ptr(), num_pages, cu_seqlens_q.data_ptr(),
+        seq_lens_k.data_ptr(), positions.data_ptr(), slot_mapping.data_ptr(), T, free_next.data_ptr(),
+        _ptr(dev_status), _stream(stream))
+    if st:
+        _check(fn, st)
 
 
 def idx_kv_layout(kv_heads: int, head_dim: int, page_size: int) -> IdxKvLayout:
@@ -350,22 +378,41 @@ def idx_kv_layout(kv_heads: int, head_dim: int, page_size: int) -> IdxKvLayout:
     return out
 
 
+def _pool_bytes(fn, pool, num_pages, page_stride, page_bytes, dev):
+    """The pool holds its pages: the library only sees a pointer."""
+    if pool.get_device() != dev or (num_pages > 0 and
+                                    pool.numel() * pool.element_size() < (num_pages - 1) * page_stride + page_bytes):
+        raise ValueError(f"{fn}: the pool ({tuple(pool.shape)}, {pool.dtype}, {pool.device}) does not hold {num_pages} pages "
+                         f"{page_stride} bytes apart on the current CUDA device")
+
+
 def idx_kv_store(k, v, slot_mapping, pool, num_pages, page_size, page_stride, dev_status=None, stream=None):
     """k, v: bf16 or fp16 [rows, kv_heads, head_dim], last dimension dense, the others strided."""
-    import torch
-    fn = "idx_kv_store"
+    fn, dev = "idx_kv_store", _device()
     ft = _ftype(fn, k)
-    _need(fn, "k", k, k.dtype, 3, False)
-    _need(fn, "v", v, k.dtype, 3, False)
-    _need(fn, "slot_mapping", slot_mapping, torch.int64, 1)
+    if k.dim() != 3 or k.get_device() != dev:
+        _refuse(fn, "k", k, k.dtype, 3, False)
+    if v.dtype is not k.dtype or v.get_device() != dev:
+        _refuse(fn, "v", v, k.dtype, 3, False)
+    if slot_mapping.dtype is not _torch.int64 or slot_mapping.dim() != 1 or slot_mapping.get_device() != dev or \
+            not slot_mapping.is_contiguous():
+        _refuse(fn, "slot_mapping", slot_mapping, _torch.int64, 1, True)
     n, H, D = k.shape
-    if v.shape != k.shape or slot_mapping.shape[0] != n:
-        raise ValueError(f"{fn}: k {tuple(k.shape)}, v {tuple(v.shape)} and {slot_mapping.shape[0]} slots do not match")
-    if n > 0 and (k.stride(2) != 1 or v.stride(2) != 1):
+    if v.shape != k.shape or len(slot_mapping) != n:
+        raise ValueError(f"{fn}: k {tuple(k.shape)}, v {tuple(v.shape)} and {len(slot_mapping)} slots do not match")
+    kr, kh, kd = k.stride()
+    vr, vh, vd = v.stride()
+    if n > 0 and (kd != 1 or vd != 1):
         raise ValueError(f"{fn}: the last dimension of k and v has to be dense")
-    _check(fn, load().idx_kv_store(
-        _ptr(k), _ptr(v), ft, n, H, D, k.stride(0), k.stride(1), v.stride(0), v.stride(1), _ptr(slot_mapping),
-        _ptr(pool), num_pages, page_size, page_stride, _ptr(dev_status), _stream(stream)))
+    if n <= 1 or H <= 1:  # the stride of a dimension of one is arbitrary
+        kr, vr = (0, 0) if n <= 1 else (kr, vr)
+        kh, vh = (0, 0) if H <= 1 else (kh, vh)
+    _pool_bytes(fn, pool, num_pages, page_stride, H * (2 * page_size * D + 16), dev)
+    st = (_lib or load()).idx_kv_store(
+        k.data_ptr(), v.data_ptr(), ft, n, H, D, kr, kh, vr, vh, slot_mapping.data_ptr(), pool.data_ptr(), num_pages,
+        page_size, page_stride, _ptr(dev_status), _stream(stream))
+    if st:
+        _check(fn, st)
 
 
 def idx_attn_workspace_bytes(T, q_heads, kv_heads, head_dim, B, max_q_len, max_seq_len_k, n_sel=0) -> int:
@@ -380,35 +427,56 @@ def idx_attn_paged(q, pool, num_pages, page_size, page_stride, kv_heads, page_ta
                    dev_status=None, stream=None):
     """q, out: bf16 or fp16 [T, q_heads, head_dim], last dimension dense, the others strided;
     sel_idx: int32 [T, n_sel], rows strided (the top-k's output), or None for every visible key."""
-    import torch
-    fn, i32 = "idx_attn_paged", torch.int32
+    fn, dev = "idx_attn_paged", _device()
+    i32 = _torch.int32
     ft = _ftype(fn, q)
-    _need(fn, "q", q, q.dtype, 3, False)
-    _need(fn, "out", out, q.dtype, 3, False)
-    _need(fn, "page_table", page_table, i32, 2)
-    _need(fn, "seq_lens_k", seq_lens_k, i32, 1)
-    _need(fn, "cu_seqlens_q", cu_seqlens_q, i32, 1)
+    if q.dim() != 3 or q.get_device() != dev:
+        _refuse(fn, "q", q, q.dtype, 3, False)
+    if out.dtype is not q.dtype or out.get_device() != dev:
+        _refuse(fn, "out", out, q.dtype, 3, False)
+    if page_table.dtype is not i32 or page_table.dim() != 2 or page_table.get_device() != dev or \
+            not page_table.is_contiguous():
+        _refuse(fn, "page_table", page_table, i32, 2, True)
+    for x in (seq_lens_k, cu_seqlens_q):
+        if x.dtype is not i32 or x.dim() != 1 or x.get_device() != dev or not x.is_contiguous():
+            _refuse(fn, "seq_lens_k and cu_seqlens_q", x, i32, 1, True)
     T, H, D = q.shape
-    B = seq_lens_k.shape[0]
-    if out.shape != q.shape or page_table.shape[0] != B or cu_seqlens_q.shape[0] != B + 1:
+    B = len(seq_lens_k)
+    rows, width = page_table.shape
+    if out.shape != q.shape or rows != B or len(cu_seqlens_q) != B + 1:
         raise ValueError(f"{fn}: q {tuple(q.shape)}, out {tuple(out.shape)}, page_table {tuple(page_table.shape)}, "
-                         f"seq_lens_k {B} and cu_seqlens_q {cu_seqlens_q.shape[0]} do not match")
-    if T > 0 and (q.stride(2) != 1 or out.stride(2) != 1):
+                         f"seq_lens_k {B} and cu_seqlens_q {len(cu_seqlens_q)} do not match")
+    qr, qh, qd = q.stride()
+    orow, oh, od = out.stride()
+    if T > 0 and (qd != 1 or od != 1):
         raise ValueError(f"{fn}: the last dimension of q and out has to be dense")
-    sel_stride = n_sel = 0
+    if T <= 1 or H <= 1:  # the stride of a dimension of one is arbitrary
+        qr, orow = (0, 0) if T <= 1 else (qr, orow)
+        qh, oh = (0, 0) if H <= 1 else (qh, oh)
+    _pool_bytes(fn, pool, num_pages, page_stride, kv_heads * (2 * page_size * D + 16), dev)
+    sel_stride = n_sel = wsb = 0
+    lse_p = sel_p = ws_p = None
     if lse is not None:
-        _need(fn, "lse", lse, torch.float32, 2)
-        if lse.shape != (T, H):
-            raise ValueError(f"{fn}: lse is {tuple(lse.shape)}, not {(T, H)}")
+        if lse.dtype is not _torch.float32 or lse.shape != (T, H) or lse.get_device() != dev or not lse.is_contiguous():
+            _refuse(fn, f"lse (of {T} rows and {H} heads)", lse, _torch.float32, 2, True)
+        lse_p = lse.data_ptr()
     if sel_idx is not None:
-        _need(fn, "sel_idx", sel_idx, i32, 2, False)
-        n_sel, sel_stride = sel_idx.shape[1], max(sel_idx.stride(0), sel_idx.shape[1])
-        if sel_idx.shape[0] != T or (T > 0 and n_sel > 1 and sel_idx.stride(1) != 1) or \
-                (T > 1 and sel_idx.stride(0) < n_sel):
+        if sel_idx.dtype is not i32 or sel_idx.dim() != 2 or sel_idx.get_device() != dev:
+            _refuse(fn, "sel_idx", sel_idx, i32, 2, False)
+        n, n_sel = sel_idx.shape
+        s0, s1 = sel_idx.stride()
+        sel_stride = max(s0, n_sel)
+        if n != T or (T > 0 and n_sel > 1 and s1 != 1) or (T > 1 and s0 < n_sel):
             raise ValueError(f"{fn}: sel_idx {tuple(sel_idx.shape)} with strides {sel_idx.stride()}")
-    wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(fn, load().idx_attn_paged(
-        _ptr(q), ft, T, H, kv_heads, D, q.stride(0), q.stride(1), _ptr(pool), num_pages, page_size, page_stride,
-        _ptr(page_table), page_table.shape[1], _ptr(seq_lens_k), _ptr(cu_seqlens_q), B, int(causal), max_q_len,
-        max_seq_len_k, _ptr(sel_idx), sel_stride, n_sel, softmax_scale, _ptr(out), out.stride(0), out.stride(1),
-        _ptr(lse), _ptr(workspace), wsb, _ptr(dev_status), _stream(stream)))
+        sel_p = sel_idx.data_ptr()
+    if workspace is not None:
+        if workspace.get_device() != dev:
+            raise ValueError(f"{fn}: the workspace is on {workspace.device}, not on the current CUDA device")
+        wsb, ws_p = workspace.numel() * workspace.element_size(), workspace.data_ptr()
+    st = (_lib or load()).idx_attn_paged(
+        q.data_ptr(), ft, T, H, kv_heads, D, qr, qh, pool.data_ptr(), num_pages, page_size, page_stride,
+        page_table.data_ptr(), width, seq_lens_k.data_ptr(), cu_seqlens_q.data_ptr(), B, 1 if causal else 0, max_q_len,
+        max_seq_len_k, sel_p, sel_stride, n_sel, softmax_scale, out.data_ptr(), orow, oh, lse_p, ws_p, wsb,
+        _ptr(dev_status), _stream(stream))
+    if st:
+        _check(fn, st)

@@ -494,7 +494,8 @@ template <int D, bool kHalf, bool kSel>
 cudaError_t launch_rows(const AttnArgs& a, cudaStream_t st) {
     constexpr int smem = Ring<D, kSel>::kBytes;
     auto* kernel = attn_rows_kernel<D, kHalf, kSel>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e = allow_smem(allowed, kernel, smem);
     if (e != cudaSuccess) return e;
     const int64_t units = kSel ? a.T * ((a.group + 15) / 16)
                                : a.B * (((int64_t)a.max_q_len * a.group + 15) / 16);

@@ -6,8 +6,10 @@
 //     u = s * c + Ev,   p' = 2^(u - m + kShift),   O += p' * v_code,   l += p' * 2^-Ev:
 // V's scale is part of the weight, so both products run on bare codes and nothing has to be
 // scaled element by element. m follows the largest u; it is raised only when a u passes it by more than
-// kLazy, since raising it means rescaling O and l. p' <= 2^(kShift + kLazy) = 2^15 stays in fp16's
-// range, and weights down to 2^-26 of the largest keep fp16's full 11 bits.
+// kLazy, since raising it means rescaling O and l (of 128-key steps with 32 rows in a warp every
+// second one raised some row with 3, one in twenty with 8: 8192-token prefill XXX us). p' <=
+// 2^(kShift + kLazy) = 2^15 stays in fp16's range; weights down to 2^-21 of the largest keep fp16's full
+// 11 bits, and below that an absolute 2^-32 of it.
 //     out = O / l,   lse = ln 2 * (m - kShift + log2 l).
 // |Ev| <= 48, so that p' and p' * 2^-Ev can only underflow where the weight is below 2^-46 of
 // the row's largest.
@@ -16,18 +18,37 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "kernels.h"
 #include "kv.cuh"
 
 namespace idx {
 
-constexpr float kShift = 12.0f, kLazy = 3.0f;
+constexpr float kShift = 7.0f, kLazy = 8.0f;
 constexpr float kLn2 = 0.693147180559945309f, kLog2e = 1.44269504088896341f;
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+// two fp32 operations in one instruction, each rounded as by itself
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+        " fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n"
+        " add.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
 }
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
 

@@ -5,14 +5,15 @@
 // group; with a list of keys, the group's heads of one token) against a range of keys, 128 at a
 // time: S = Q K^T (M = 128 rows, N = 128 keys), the running softmax of attn.cuh, O += P V (N = D). S and
 // O live in tensor memory (128 + D columns), P overwrites S as fp16 and is the second product's A
-// operand from there. Roles of a CTA's eight warps:
-//   0-3  softmax: thread = row. Q to shared memory at the start, S -> P per tile, O out at the end;
-//   4-7  converters: e4m3 from memory to fp16 operand tiles in shared memory (exact). The loads of
-//        a tile go out one tile ahead into registers, so any row order costs the same: pages
-//        and lists of keys need no gather pass. V is transposed on the way (8 keys x 16 dims per
-//        thread, bytes paired by prmt), which makes both products K-major;
-//   7    one of its threads issues the MMAs between its own conversions (a ninth warp would cost
-//        every thread a quarter of its registers).
+// operand from there. Roles of a CTA's two warpgroups:
+//   0  softmax: thread = row. Q to shared memory at the start, S -> P per tile, O out at the end; one
+//      thread of warp 0 issues the MMAs, which its warp would wait for anyway (in a converter warp
+//      each step waited for that warp's other work, and a warp of its own costs every thread a
+//      quarter of its registers);
+//   1  converters: e4m3 from memory to fp16 operand tiles in shared memory (exact). The loads of a
+//      tile go out one tile ahead into registers, so any row order costs the same: pages and
+//      lists of keys need no gather pass. V is transposed on the way (8 keys x 16 dims per
+//      thread, bytes paired by prmt), which makes both products K-major.
 // fp16 runs at half the 8-bit rate, but 8-bit operands would leave q and the weights 4 bits; two
 // 8-bit halves each would cost the same tensor time and more conversion. Two CTAs share an SM
 // (tensor memory 2 x 256 columns, shared memory 2 x 103 KB): one's products run under the other's
@@ -27,6 +28,19 @@ namespace {
 constexpr int kRowsT = 128;   // rows of a tile
 constexpr int kKeysT = 128;   // keys of a step
 constexpr int kThreadsT = 256;
+#ifndef NSI
+#define NSI 0
+#define NSS 20
+#define NSC 40
+#endif
+constexpr int kNsIssue = NSI, kNsSoft = NSS, kNsConv = NSC;
+
+// Where 8 consecutive dims (chunk i) of q and k lie in the operand tiles: any order serves, and this one
+// lets 8 lanes that convert one key's consecutive 16-byte pieces write 8 different chunks.
+template <int D>
+__device__ __forceinline__ constexpr int dims_sub(int i) { return D == 128 ? i & 1 : 0; }
+template <int D>
+__device__ __forceinline__ constexpr int dims_chunk(int i) { return D == 128 ? i >> 1 : (i >> 1) + 4 * (i & 1); }
 
 template <int D>
 struct SmemT {
@@ -51,8 +65,9 @@ __device__ __forceinline__ bool conv_all(bool v) {
     return r != 0;
 }
 // Bounded wait of a whole warp: every lane gets the same answer.
+template <int kNs>
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
-    return __all_sync(kFull, tc::mbar_wait(bar, parity));
+    return __all_sync(kFull, tc::mbar_spin<kNs>(bar, parity));
 }
 
 template <int D, bool kHalf, bool kSel>
@@ -67,16 +82,6 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
     float4* scales = reinterpret_cast<float4*>(sm + S::kScale);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
-    if (tid == 0) {
-        tc::mbar_init(q_full, kRowsT);
-        tc::mbar_init(k_full, 128);
-        tc::mbar_init(v_full, 128);
-        tc::mbar_init(s_full, 1);
-        tc::mbar_init(p_full, kRowsT);
-        tc::mbar_init(o_done, 1);
-        tc::mbar_init(drain, 1);
-        tc::fence_mbar_init();
-    }
     pdl_wait();
 
     // ---- the unit ------------------------------------------------------------------------------
@@ -112,7 +117,18 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
         pdl_launch_dependents();
         return;
     }
-    if (warp == 7) {
+    if (tid == 0) {
+        tc::mbar_init(q_full, kRowsT);
+        tc::mbar_init(k_full, 128);
+        tc::mbar_init(v_full, 128);
+        tc::mbar_init(s_full, 1);
+        tc::mbar_init(p_full, (rows + 31) / 32);  // a warp without rows takes no part
+        tc::mbar_init(o_done, 1);
+        tc::mbar_init(drain, 1);
+        tc::fence_mbar_init();
+    }
+    __syncwarp();
+    if (warp == 0) {
         tc::tmem_alloc(&tmem_slot, 256);
         tc::tmem_relinquish();
     }
@@ -135,13 +151,12 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
         float rc = 0.0f;
         {
             const uint4* q = reinterpret_cast<const uint4*>(a.q + tok * a.q_row_stride + (int64_t)hq * a.q_head_stride);
-            uint4 w[D / 8];
             float amax = 0.0f;
             bool odd = false;
-#pragma unroll
+#pragma unroll 4
             for (int i = 0; i < D / 8; ++i) {
-                w[i] = real ? q[i] : make_uint4(0, 0, 0, 0);
-                const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+                const uint4 w = real ? q[i] : make_uint4(0, 0, 0, 0);
+                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     const float2 f = load_pair<kHalf>(u[x]);
@@ -152,9 +167,10 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
             const int e = odd ? 0 : q_exponent<kHalf>(amax);
             const float up = pow2f(-e);
             rc = odd ? __int_as_float(0x7fc00000) : a.scale * kLog2e * pow2f(e);
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-                uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll 4
+            for (int i = 0; i < D / 8; ++i) {  // again, from L1
+                const uint4 w = real ? q[i] : make_uint4(0, 0, 0, 0);
+                uint32_t u[4] = {w.x, w.y, w.z, w.w};
                 if constexpr (!kHalf) {
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
@@ -162,8 +178,8 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
                         u[x] = half2_bits(f.x * up, f.y * up);
                     }
                 }
-                *reinterpret_cast<uint4*>(sm + S::kQ + (i / 8) * (kRowsT * 128) + tid * 128 +
-                                          (((i & 7) ^ (tid & 7)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
+                *reinterpret_cast<uint4*>(sm + S::kQ + dims_sub<D>(i) * (kRowsT * 128) + tid * 128 +
+                                          ((dims_chunk<D>(i) ^ (tid & 7)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
             }
             tc::fence_proxy_async();
             tc::mbar_arrive(q_full);
@@ -171,141 +187,201 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
         const uint32_t lanes = (uint32_t)(warp * 32) << 16;
         const bool idle = 32 * warp >= rows;  // no row of this warp exists
         float m = neg_inf(), l = 0.0f;
-        for (int j = 0; j < n && ok; ++j) {
-            ok = warp_wait(s_full, j & 1);
-            if (!ok) break;
-            if (!idle) {
-                tc::tc_fence_after();
-                const float4* sc = scales + (j & 1) * kKeysT;
-                const int kt = k0 + j * kKeysT;
-                const bool cut = !kSel && __any_sync(kFull, kt + kKeysT > vis);
-                float mx = neg_inf();
+        // One step of the running softmax: S to P, with the rows' visibility tested key by key
+        // (kCut, the tiles that some row of the warp does not see whole) or not.
+        auto step = [&](int j, auto cut_tag) {
+            constexpr bool kCut = decltype(cut_tag)::value;
+            const float4* sc = scales + (j & 1) * kKeysT;
+            const int left = vis - (k0 + j * kKeysT);  // keys of this step that the row sees
+            float mx = neg_inf();
+#pragma unroll 1
+            for (int c = 0; c < 4; c += 2) {
+                uint32_t r[2][32];
+                __syncwarp();
+                tc::tmem_ld32(tm_s + lanes + 32 * c, r[0]);
+                tc::tmem_ld32(tm_s + lanes + 32 * c + 32, r[1]);
+                tc::tmem_ld_wait();
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t r[32];
-                    __syncwarp();
-                    tc::tmem_ld32(tm_s + lanes + 32 * c, r);
-                    tc::tmem_ld_wait();
+                for (int h = 0; h < 4; ++h) {
+                    const uint32_t* x = &r[h >> 1][16 * (h & 1)];
+                    const int at = 32 * c + 16 * h;
                     if constexpr (kSel) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const float4 k = sc[32 * c + i];
-                            mx = fmaxf(mx, fmaf(__uint_as_float(r[i]), rc * k.x, k.y));
+                        for (int i = 0; i < 16; ++i) {
+                            const float4 k = sc[at + i];
+                            mx = fmaxf(mx, fmaf(__uint_as_float(x[i]), rc * k.x, k.y));
                         }
                     } else {
+                        const float4 k = sc[at / 16];
+                        float bm = neg_inf();
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const float4 k = sc[2 * c + h];
-                            float bm = neg_inf();
-                            if (cut) {
-#pragma unroll
-                                for (int i = 0; i < 16; ++i)
-                                    if (kt + 32 * c + 16 * h + i < vis) bm = fmaxf(bm, __uint_as_float(r[16 * h + i]));
-                            } else {
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) bm = fmaxf(bm, __uint_as_float(r[16 * h + i]));
-                            }
-                            // nothing visible: bm is -inf, and so is the sum whatever the factor's sign of zero
-                            if (bm > neg_inf()) mx = fmaxf(mx, fmaf(bm, rc * k.x, k.y));
-                        }
+                        for (int i = 0; i < 16; ++i)
+                            bm = fmaxf(bm, !kCut || at + i < left ? __uint_as_float(x[i]) : neg_inf());
+                        // nothing visible: bm is -inf whatever the factor
+                        const float u = fmaf(bm, rc * k.x, k.y);
+                        mx = fmaxf(mx, kCut && bm == neg_inf() ? bm : u);
                     }
                 }
-                float f = 1.0f;
-                const bool raise = mx > m + kLazy;
-                if (raise) {
-                    f = ex2(m - mx);
-                    m = mx;
-                    l *= f;
-                }
-                if (j > 0 && __any_sync(kFull, raise)) {
-                    // s_full is committed behind the previous O += P V, so O is complete
+            }
+            float f = 1.0f;
+            const bool raise = mx > m + kLazy;
+            if (raise) {
+                f = ex2(m - mx);
+                m = mx;
+                l *= f;
+            }
+            if (j > 0 && __any_sync(kFull, raise)) {
+                // the scores were issued behind the completed O += P V of the step before
 #pragma unroll 1
-                    for (int c = 0; c < D / 16; ++c) {
-                        uint32_t r[16];
-                        __syncwarp();
-                        tc::tmem_ld16(tm_o + lanes + 16 * c, r);
-                        tc::tmem_ld_wait();
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
-                        tc::tmem_st16(tm_o + lanes + 16 * c, r);
-                    }
-                }
-                const float top = m == neg_inf() ? 0.0f : kShift - m;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t r[32], p2[16];
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t r[2][16];
                     __syncwarp();
-                    tc::tmem_ld32(tm_s + lanes + 32 * c, r);
+                    tc::tmem_ld16(tm_o + lanes + 32 * c, r[0]);
+                    tc::tmem_ld16(tm_o + lanes + 32 * c + 16, r[1]);
                     tc::tmem_ld_wait();
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float cc = 0.0f, sub = 0.0f, inv = 0.0f, sum = 0.0f;
-                        if constexpr (!kSel) {
-                            const float4 k = sc[2 * c + h];
-                            cc = rc * k.x;
-                            sub = k.y + top;
-                            inv = k.z;
-                        }
-#pragma unroll
-                        for (int i = 0; i < 16; i += 2) {
-                            float p[2];
-#pragma unroll
-                            for (int y = 0; y < 2; ++y) {
-                                const int at = 16 * h + i + y;
-                                if constexpr (kSel) {
-                                    const float4 k = sc[32 * c + at];
-                                    p[y] = ex2(fmaf(__uint_as_float(r[at]), rc * k.x, k.y + top));
-                                    l = fmaf(p[y], k.z, l);
-                                } else {
-                                    float u = fmaf(__uint_as_float(r[at]), cc, sub);
-                                    if (cut) u = kt + 32 * c + at < vis ? u : neg_inf();
-                                    p[y] = ex2(u);
-                                    sum += p[y];
-                                }
-                            }
-                            p2[8 * h + i / 2] = half2_bits(p[0], p[1]);
-                        }
-                        if constexpr (!kSel) l = fmaf(sum, inv, l);
+                    for (int i = 0; i < 16; ++i) {
+                        r[0][i] = __float_as_uint(__uint_as_float(r[0][i]) * f);
+                        r[1][i] = __float_as_uint(__uint_as_float(r[1][i]) * f);
                     }
-                    // columns 16c .. 16c+15 held scores that were read in step c or before
-                    tc::tmem_st16(tm_s + lanes + 16 * c, p2);
+                    tc::tmem_st16(tm_o + lanes + 32 * c, r[0]);
+                    tc::tmem_st16(tm_o + lanes + 32 * c + 16, r[1]);
                 }
-                tc::tmem_st_wait();
-                tc::tc_fence_before();
             }
-            tc::mbar_arrive(p_full);
+            const float top = m == neg_inf() ? 0.0f : kShift - m;
+#pragma unroll 1
+            for (int c = 0; c < 4; c += 2) {
+                uint32_t r[2][32];
+                __syncwarp();
+                tc::tmem_ld32(tm_s + lanes + 32 * c, r[0]);
+                tc::tmem_ld32(tm_s + lanes + 32 * c + 32, r[1]);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    uint32_t p2[16];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t* x = &r[g][16 * h];
+                        const int at = 32 * (c + g) + 16 * h;
+                        if constexpr (kSel) {
+#pragma unroll
+                            for (int i = 0; i < 16; i += 2) {
+                                const float4 ka = sc[at + i], kb = sc[at + i + 1];
+                                const float pa = ex2(fmaf(__uint_as_float(x[i]), rc * ka.x, ka.y + top));
+                                const float pb = ex2(fmaf(__uint_as_float(x[i + 1]), rc * kb.x, kb.y + top));
+                                l = fmaf(pa, ka.z, l);
+                                l = fmaf(pb, kb.z, l);
+                                p2[8 * h + i / 2] = half2_bits(pa, pb);
+                            }
+                        } else {
+                            const float4 k = sc[at / 16];
+                            const float cc = rc * k.x, sub = k.y + top;
+                            float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+                            for (int i = 0; i < 16; i += 2) {
+                                float2 u = fma2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])),
+                                                make_float2(cc, cc), make_float2(sub, sub));
+                                if constexpr (kCut) {
+                                    u.x = at + i < left ? u.x : neg_inf();
+                                    u.y = at + i + 1 < left ? u.y : neg_inf();
+                                }
+                                const float2 p = make_float2(ex2(u.x), ex2(u.y));
+                                sum = add2(sum, p);
+                                p2[8 * h + i / 2] = half2_bits(p.x, p.y);
+                            }
+                            l = fmaf(sum.x + sum.y, k.z, l);
+                        }
+                    }
+                    // columns 16(c+g) .. +15 held scores that have been read
+                    tc::tmem_st16(tm_s + lanes + 16 * (c + g), p2);
+                }
+            }
+            tc::tmem_st_wait();
+            tc::tc_fence_before();
+        };
+        // The MMAs of a step, by one thread of warp 0, which has nothing else to do meanwhile.
+        const uint32_t base = tc::smem_u32(sm);
+        auto issue_s = [&]() {
+            tc::tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                const uint32_t at = (k / 4) * (128 * 128) + (k % 4) * 32;
+                tc::mma_f16(tm_s, tc::smem_desc_sw128(base + S::kQ + at), tc::smem_desc_sw128(base + S::kK + at),
+                            tc::idesc_f16(kRowsT, kKeysT), k > 0);
+            }
+            tc::mma_commit(s_full);
+        };
+        auto issue_o = [&](bool accumulate) {
+            tc::tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < kKeysT / 16; ++k)
+                tc::mma_f16_ta(tm_o, tm_s + 8 * k,
+                               tc::smem_desc_sw128(base + S::kV + (k / 4) * (D * 128) + (k % 4) * 32),
+                               tc::idesc_f16(kRowsT, D), accumulate || k > 0);
+            tc::mma_commit(o_done);
+        };
+        // Round j: O += P V of step j and S of step j + 1, then the softmax of step j + 1.
+        for (int j = -1; j < n && !idle; ++j) {
+            if (tid == 0) {
+                if (j >= 0) {
+                    ok = tc::mbar_spin<kNsIssue>(v_full, j & 1) && tc::mbar_spin<kNsIssue>(p_full, j & 1);
+                    if (ok) issue_o(j > 0);
+                }
+                if (ok && j + 1 < n) {
+                    // P of step j lies where the next S goes: its product has to be done
+                    ok = tc::mbar_spin<kNsIssue>(k_full, (j + 1) & 1) && tc::mbar_spin<kNsIssue>(j < 0 ? q_full : o_done, j < 0 ? 0 : j & 1);
+                    if (ok) issue_s();
+                }
+            }
+            ok = __all_sync(kFull, ok);
+            if (!ok || j + 1 >= n) break;
+            ok = warp_wait<kNsSoft>(s_full, (j + 1) & 1);
+            if (!ok) break;
+            tc::tc_fence_after();
+            if (!kSel && __any_sync(kFull, k0 + (j + 2) * kKeysT > vis))
+                step(j + 1, std::true_type{});
+            else
+                step(j + 1, std::false_type{});
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(p_full);
         }
+        if (tid == 0) {  // what was issued has to finish before the tensor memory is given back
+            tc::mma_commit(drain);
+            if (!tc::mbar_spin<kNsIssue>(drain, 0)) ok = false;
+        }
+        ok = __all_sync(kFull, ok);
         // ---- the row's result -------------------------------------------------------------------------
-        if (ok && n > 0) ok = warp_wait(o_done, (n - 1) & 1);
+        if (ok && n > 0 && !idle) ok = warp_wait<kNsSoft>(o_done, (n - 1) & 1);
         if (ok && !idle) {
             tc::tc_fence_after();
             const float g = a.n_split > 1 ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
             const int64_t pr = ((int64_t)z * a.T + tok) * a.q_heads + hq;
             uint16_t* out = a.out + tok * a.out_row_stride + (int64_t)hq * a.out_head_stride;
+            // column 8y + dg of O is dim (D/8) * dg + y: 32 columns are 4 dims of each dg
 #pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
-                uint32_t r[16];
-                float v[16];
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t r[32];
                 __syncwarp();
                 if (n > 0) {
-                    tc::tmem_ld16(tm_o + lanes + 16 * c, r);
+                    tc::tmem_ld32(tm_o + lanes + 32 * c, r);
                     tc::tmem_ld_wait();
                 }
+                if (!(n > 0 && l != 0.0f)) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] = (n > 0 && l != 0.0f) ? __uint_as_float(r[i]) * g : 0.0f;
-                if (real && a.n_split > 1) {
-                    if (l != 0.0f) {
-                        float4* dst = reinterpret_cast<float4*>(a.part_o + pr * D + 16 * c);
+                    for (int i = 0; i < 32; ++i) r[i] = 0;
+                }
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                for (int x = 0; x < 8; ++x) {
+                    float v[4];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) v[y] = __uint_as_float(r[8 * y + x]) * g;
+                    const int dim = D / 8 * x + 4 * c;
+                    if (real && a.n_split > 1) {
+                        if (l != 0.0f)
+                            *reinterpret_cast<float4*>(a.part_o + pr * D + dim) = make_float4(v[0], v[1], v[2], v[3]);
+                    } else if (real) {
+                        *reinterpret_cast<uint2*>(out + dim) = make_uint2(store_pair<kHalf>(v[0], v[1]), store_pair<kHalf>(v[2], v[3]));
                     }
-                } else if (real) {
-                    uint4* dst = reinterpret_cast<uint4*>(out + 16 * c);
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        dst[i] = make_uint4(
-                            store_pair<kHalf>(v[8 * i], v[8 * i + 1]), store_pair<kHalf>(v[8 * i + 2], v[8 * i + 3]),
-                            store_pair<kHalf>(v[8 * i + 4], v[8 * i + 5]), store_pair<kHalf>(v[8 * i + 6], v[8 * i + 7]));
                 }
             }
             if (real) {
@@ -326,116 +402,121 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
         const int32_t* pt = a.page_table + (int64_t)b * a.pt_stride;
         int64_t* offs = reinterpret_cast<int64_t*>(sm + S::kOff);
         const int vis_sel = kSel ? (int)visible_keys(s.len, s.nq, tok0 - s.t0, a.causal) : 0;
-        // K: keys 8 * (cw + 4i) + lane % 8, pieces lane / 8 (+ 4); V: keys 8 * kg .. + 7, dims of dg
-        const int kg = (lane & 7) + 8 * (cw & 1), dg = (lane >> 3) + 4 * (cw >> 1);
+        // 8 lanes take consecutive pieces of a row (a memory request then touches few lines). K: 16-byte piece kp
+        // of keys k_key + i * kKeyStep; V: kVB bytes from dim kVB * dg of keys 8 * kg .. + 7, whose
+        // dim kVB * dg + y goes to row 8 * y + dg of the transposed tile (8 lanes, 8 chunks).
+        const int kp = D == 128 ? lane & 7 : lane & 3;
+        const int k_key = D == 128 ? (lane >> 3) + 4 * cw : (lane >> 3) + (lane & 4) + 8 * cw;
+        constexpr int kKeyStep = D == 128 ? 16 : 32;
+        const int kg = (lane >> 3) + 4 * cw, dg = lane & 7;
         uint4 rk[kPieces], rv[8];
-        float4 my_scale = make_float4(1.0f, neg_inf(), 0.0f, 0.0f);
+        uint32_t my_scale = 0;  // the key's or block's two scale bytes, bit 16 set; 0: not to be used
         bool bad = false;
 
-        // With a list, thread ct looks up entry ct of a step: the entry two steps ahead, its page one
-        // step ahead, its row's place for the loads.
-        int32_t ent_n = -1, ent = -1, page = -1;
-        int32_t pages[2] = {-1, -1};  // dense: the step's pages (the second for P = 64)
+        // Lookups run ahead: a step's pages are loaded one step before its rows, and with a list (thread
+        // ct looks after entry ct of a step) its entries two steps before.
+        int32_t ent = -1, ent_n = -1;
+        int32_t page[2] = {-1, -1};                     // the second: keys 64 .. of the step
+        const uint8_t* rows_at[2] = {nullptr, nullptr};  // key 0 of the step, seen from either half
+        int keys = 0;                                    // of the step
         auto load_entry = [&](int j) -> int32_t {
             const int e = k0 + j * kKeysT + ct;
-            return (j < n && e < k1) ? a.sel[tok0 * a.sel_stride + e] : -1;
+            return e < k1 ? a.sel[tok0 * a.sel_stride + e] : -1;
         };
-        auto lookup = [&](int j) {  // pages of step j
+        auto lookup = [&](int j) {
             if constexpr (kSel) {
-                page = (ent >= 0 && ent < vis_sel) ? pt[ent >> lp] : -1;
+                page[0] = (ent >= 0 && ent < vis_sel) ? pt[ent >> lp] : -1;
             } else {
                 const int kt = k0 + j * kKeysT;
-                pages[0] = j < n ? pt[kt >> lp] : -1;
-                pages[1] = P == 128 ? pages[0] : ((j < n && kt + 64 < k1) ? pt[(kt >> 6) + 1] : -1);
+                page[0] = kt < k1 ? pt[kt >> lp] : -1;
+                page[1] = kt + 64 < k1 ? pt[(kt + 64) >> lp] : -1;
             }
         };
-        // where step j's keys are, and the scales (kept in registers until the tile is written)
         auto place = [&](int j) {
-            int64_t at = -1;
-            int tok = 0;
+            my_scale = 0;
             if constexpr (kSel) {
-                const bool seen = ent >= 0 && ent < vis_sel;
-                if (seen && (uint32_t)page >= (uint64_t)a.num_pages) bad = true;
-                if (seen && (uint32_t)page < (uint64_t)a.num_pages) {
-                    tok = ent & (P - 1);
-                    at = (int64_t)page * a.page_stride;
+                const bool seen = ent >= 0 && ent < vis_sel, in = (uint32_t)page[0] < (uint64_t)a.num_pages;
+                int64_t at = -1;
+                bad |= seen && !in;
+                if (seen && in) {
+                    const int tok = ent & (P - 1);
+                    at = (int64_t)page[0] * a.page_stride;
+                    my_scale = *reinterpret_cast<const uint16_t*>(pool + at + 2ll * P * D + 2 * (tok / kKvBlock)) | 65536u;
+                    at += (int64_t)tok * 2 * D;
                 }
                 // the places of step j - 2 have been read: conv_all() came since
-                offs[(j & 1) * kKeysT + ct] = at < 0 ? -1 : at + (int64_t)tok * 2 * D;
+                offs[(j & 1) * kKeysT + ct] = at;
                 conv_sync();
             } else {
-                const int key = k0 + j * kKeysT + ct;
-                const int32_t pg = pages[P == 64 && ct >= 64];
-                if (j < n && key < k1) {
-                    if ((uint32_t)pg < (uint64_t)a.num_pages)
-                        at = (int64_t)pg * a.page_stride;
-                    else
-                        bad = true;
+                keys = k1 - (k0 + j * kKeysT);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const bool in = (uint32_t)page[h] < (uint64_t)a.num_pages;
+                    bad |= !in && 64 * h < keys;
+                    const uint8_t* at = pool + (int64_t)page[h] * a.page_stride;
+                    // this thread's block of 16 keys
+                    if (in && (ct & 15) == 0 && ct / 64 == h && ct < keys)
+                        my_scale = *reinterpret_cast<const uint16_t*>(at + 2ll * P * D + 2 * ((ct & (P - 1)) / kKvBlock)) | 65536u;
+                    rows_at[h] = in ? at - (h && P == 64 ? 64 * 2 * D : 0) : nullptr;
                 }
-                tok = key & (P - 1);
-            }
-            my_scale = make_float4(1.0f, neg_inf(), 0.0f, 0.0f);
-            if (at >= 0 && (kSel || (ct & 15) == 0)) {
-                const uint32_t two = *reinterpret_cast<const uint16_t*>(pool + at + 2ll * P * D + 2 * (tok / kKvBlock));
-                const float ev = v_exponent(two);
-                my_scale = make_float4(k_scale(two), ev, ex2(-ev), 0.0f);
-            }
-        };
-        auto row_of = [&](int j, int key) -> const uint8_t* {  // key's 2*D bytes, or null
-            if constexpr (kSel) {
-                const int64_t at = offs[(j & 1) * kKeysT + key];
-                return at < 0 ? nullptr : pool + at;
-            } else {
-                const int32_t pg = pages[P == 64 && key >= 64];
-                const int at = k0 + j * kKeysT + key;
-                if (j >= n || at >= k1 || (uint32_t)pg >= (uint64_t)a.num_pages) return nullptr;
-                return pool + (int64_t)pg * a.page_stride + (int64_t)(at & (P - 1)) * 2 * D;
             }
         };
         auto load_k = [&](int j) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint8_t* src = row_of(j, 8 * (cw + 4 * i) + (lane & 7));
-#pragma unroll
-                for (int x = 0; x < D / 64; ++x) {
-                    rk[i * (D / 64) + x] = make_uint4(0, 0, 0, 0);
-                    if (src) rk[i * (D / 64) + x] = reinterpret_cast<const uint4*>(src)[(lane >> 3) + 4 * x];
+            for (int i = 0; i < kPieces; ++i) {
+                const int key = k_key + kKeyStep * i;
+                const uint8_t* half = rows_at[2 * i / kPieces];
+                const uint8_t* src = half + key * 2 * D;
+                bool in = half != nullptr && key < keys;
+                if constexpr (kSel) {
+                    const int64_t at = offs[(j & 1) * kKeysT + key];
+                    src = pool + at;
+                    in = at >= 0;
                 }
+                uint4 w = make_uint4(0, 0, 0, 0);
+                if (in) w = reinterpret_cast<const uint4*>(src)[kp];
+                rk[i] = w;
             }
         };
         auto load_v = [&](int j) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const uint8_t* src = row_of(j, 8 * kg + i);
-                rv[i] = make_uint4(0, 0, 0, 0);
-                if (src) {
-                    if constexpr (D == 128) {
-                        rv[i] = *reinterpret_cast<const uint4*>(src + D + 16 * dg);
-                    } else {
-                        const uint2 w = *reinterpret_cast<const uint2*>(src + D + 8 * dg);
-                        rv[i].x = w.x;
-                        rv[i].y = w.y;
-                    }
+                const int key = 8 * kg + i;
+                const uint8_t* half = cw >= 2 ? rows_at[1] : rows_at[0];
+                const uint8_t* src = half + key * 2 * D;
+                bool in = half != nullptr && key < keys;
+                if constexpr (kSel) {
+                    const int64_t at = offs[(j & 1) * kKeysT + key];
+                    src = pool + at;
+                    in = at >= 0;
                 }
+                uint4 w = make_uint4(0, 0, 0, 0);
+                if constexpr (D == 128) {
+                    if (in) w = *reinterpret_cast<const uint4*>(src + D + 16 * dg);
+                } else {
+                    uint2 y = make_uint2(0, 0);
+                    if (in) y = *reinterpret_cast<const uint2*>(src + D + 8 * dg);
+                    w.x = y.x;
+                    w.y = y.y;
+                }
+                rv[i] = w;
             }
         };
-        auto write_k = [&](int j, const float4& sc) {
+        auto write_k = [&](int j) {
+            const float ev = v_exponent(my_scale);
+            const float4 sc = my_scale ? make_float4(k_scale(my_scale), ev, ex2(-ev), 0.0f)
+                                       : make_float4(1.0f, neg_inf(), 0.0f, 0.0f);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int key = 8 * (cw + 4 * i) + (lane & 7);
-#pragma unroll
-                for (int x = 0; x < D / 64; ++x) {
-                    const uint4 w = rk[i * (D / 64) + x];
-                    uint4 lo, hi;
-                    e4m3x4_to_f16x4(w.x, lo.x, lo.y);
-                    e4m3x4_to_f16x4(w.y, lo.z, lo.w);
-                    e4m3x4_to_f16x4(w.z, hi.x, hi.y);
-                    e4m3x4_to_f16x4(w.w, hi.z, hi.w);
-                    uint8_t* row = sm + S::kK + x * (kKeysT * 128) + key * 128;
-                    const int kc = 2 * (lane >> 3);
-                    *reinterpret_cast<uint4*>(row + ((kc ^ (key & 7)) << 4)) = lo;
-                    *reinterpret_cast<uint4*>(row + (((kc + 1) ^ (key & 7)) << 4)) = hi;
-                }
+            for (int i = 0; i < kPieces; ++i) {
+                const int key = k_key + kKeyStep * i;
+                uint4 lo, hi;
+                e4m3x4_to_f16x4(rk[i].x, lo.x, lo.y);
+                e4m3x4_to_f16x4(rk[i].y, lo.z, lo.w);
+                e4m3x4_to_f16x4(rk[i].z, hi.x, hi.y);
+                e4m3x4_to_f16x4(rk[i].w, hi.z, hi.w);
+                uint8_t* row = sm + S::kK + key * 128;
+                *reinterpret_cast<uint4*>(row + dims_sub<D>(0) * (kKeysT * 128) + ((dims_chunk<D>(2 * kp) ^ (key & 7)) << 4)) = lo;
+                *reinterpret_cast<uint4*>(row + dims_sub<D>(1) * (kKeysT * 128) + ((dims_chunk<D>(2 * kp + 1) ^ (key & 7)) << 4)) = hi;
             }
             if constexpr (kSel)
                 scales[(j & 1) * kKeysT + ct] = sc;
@@ -458,115 +539,56 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
                 }
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
-                    const int dim = kVB * dg + 4 * w + y;
-                    *reinterpret_cast<uint4*>(sm + S::kV + (kg >> 3) * (D * 128) + dim * 128 +
-                                              (((kg & 7) ^ (dim & 7)) << 4)) =
+                    const int row = 8 * (4 * w + y) + dg;  // of dim kVB * dg + 4 * w + y
+                    *reinterpret_cast<uint4*>(sm + S::kV + (kg >> 3) * (D * 128) + row * 128 + (((kg & 7) ^ dg) << 4)) =
                         make_uint4(t[y][0], t[y][1], t[y][2], t[y][3]);
                 }
             }
             tc::fence_proxy_async();
             tc::mbar_arrive(v_full);
         };
-        // the MMAs of a step, by one thread
-        const bool issuer = warp == 7 && lane == 0;
-        const uint32_t base = tc::smem_u32(sm);
-        auto issue_s = [&]() {
-            tc::tc_fence_after();
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                const uint32_t at = (k / 4) * (128 * 128) + (k % 4) * 32;
-                tc::mma_f16(tm_s, tc::smem_desc_sw128(base + S::kQ + at), tc::smem_desc_sw128(base + S::kK + at),
-                            tc::idesc_f16(kRowsT, kKeysT), k > 0);
-            }
-            tc::mma_commit(s_full);
-        };
-        auto issue_o = [&](bool accumulate) {
-            tc::tc_fence_after();
-#pragma unroll
-            for (int k = 0; k < kKeysT / 16; ++k)
-                tc::mma_f16_ta(tm_o, tm_s + 8 * k,
-                               tc::smem_desc_sw128(base + S::kV + (k / 4) * (D * 128) + (k % 4) * 32),
-                               tc::idesc_f16(kRowsT, D), accumulate || k > 0);
-            tc::mma_commit(o_done);
-        };
-
         if (n > 0) {
             if constexpr (kSel) {
                 ent = load_entry(0);
                 ent_n = load_entry(1);
             }
             lookup(0);
-            place(0);
-            load_k(0);
-            load_v(0);
-            float4 sc = my_scale;
-            if constexpr (kSel) {
-                ent = ent_n;
-                ent_n = load_entry(2);
-            }
-            lookup(1);
-            write_k(0, sc);
-            if (issuer) {
-                ok = tc::mbar_wait(q_full, 0) && tc::mbar_wait(k_full, 0);
-                if (ok) issue_s();
-            }
-            ok = __all_sync(kFull, ok);
-            write_v();
-            place(1);
-            load_k(1);
-            load_v(1);
-            for (int j = 0; j < n; ++j) {
-                // K of step j + 1 goes where step j's product has read; its V where O += P V has
-                if (j + 1 < n) {
-                    ok = warp_wait(s_full, j & 1) && ok;
-                    if constexpr (kSel) ok = conv_all(ok);  // leave together: place() has a barrier
-                    if (!ok) break;
-                    sc = my_scale;
-                    if constexpr (kSel) {
-                        ent = ent_n;
-                        ent_n = load_entry(j + 3);
-                    }
-                    lookup(j + 2);
-                    write_k(j + 1, sc);
-                }
-                if (issuer && ok) {
-                    ok = tc::mbar_wait(v_full, j & 1) && tc::mbar_wait(p_full, j & 1);
-                    if (ok) issue_o(j > 0);
-                    // P lies where the next S goes: its product has to be done
-                    if (ok && j + 1 < n) {
-                        ok = tc::mbar_wait(k_full, (j + 1) & 1) && tc::mbar_wait(o_done, j & 1);
-                        if (ok) issue_s();
-                    }
-                }
-                ok = __all_sync(kFull, ok);
-                if (j + 1 < n) {
-                    ok = warp_wait(o_done, j & 1) && ok;
-                    if (!kSel && !ok) break;
-                    write_v();
+            // Round j: K of step j + 1 to shared memory (where step j's product has read), loads of step
+            // j + 2's K; V of step j + 1 (where O += P V has read), loads of step j + 2's V.
+#pragma unroll 1
+            for (int j = -2; j + 1 < n; ++j) {
+                if (j >= 0) ok = warp_wait<kNsConv>(s_full, j & 1) && ok;
+                if constexpr (kSel) ok = conv_all(ok);  // leave together: place() has a barrier
+                if (!ok) break;
+                if (j >= -1) write_k(j + 1);
+                if (j + 2 < n) {
                     place(j + 2);
                     load_k(j + 2);
-                    load_v(j + 2);
+                    if constexpr (kSel) {
+                        ent = ent_n;
+                        ent_n = load_entry(j + 4);
+                    }
+                    lookup(j + 3);
                 }
+                if (j >= 0) ok = warp_wait<kNsConv>(o_done, j & 1) && ok;
+                if (j >= -1) write_v();
+                if (j + 2 < n) load_v(j + 2);
             }
-            if (issuer) {  // what was issued has to finish before the tensor memory is given back
-                tc::mma_commit(drain);
-                if (!tc::mbar_wait(drain, 0)) ok = false;
-            }
-            __syncwarp();
         }
         if (bad) report(a.dev_status, IDX_STATUS_BAD_PAGE);
     }
     if (!ok) report(a.dev_status, IDX_STATUS_TIMEOUT);
     tc::tc_fence_before();
     __syncthreads();
-    if (warp == 7) tc::tmem_dealloc(tm_s, 256);
+    if (warp == 0) tc::tmem_dealloc(tm_s, 256);
 }
 
 template <int D, bool kHalf, bool kSel>
 cudaError_t launch_tile(const AttnArgs& a, cudaStream_t st) {
     constexpr int smem = SmemT<D>::kBytes;
     auto* kernel = attn_tile_kernel<D, kHalf, kSel>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e = allow_smem(allowed, kernel, smem);
     if (e != cudaSuccess) return e;
     const int64_t units = kSel ? a.T * ((a.group + kRowsT - 1) / kRowsT)
                                : a.B * (((int64_t)a.max_q_len * a.group + kRowsT - 1) / kRowsT);

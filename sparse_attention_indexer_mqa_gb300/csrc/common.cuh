@@ -9,6 +9,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <utility>
 
 #include "../../include/idx.h"
@@ -39,12 +40,19 @@ __device__ __forceinline__ void pdl_launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// idx_step_meta writes what the kernels read before pdl_wait(), so the call behind it on its
+// stream is launched without programmatic serialization: it starts when the metadata are
+// visible, and what follows it starts no earlier. The metadata call leaves a mark (meta.cu).
+extern std::atomic<int> g_order_marks;     // streams with a mark
+bool take_order_mark(cudaStream_t st);     // true, once, if st has one
+
 // Launch with programmatic stream serialization (the kernel calls pdl_wait()) when pdl is
 // true, else as an ordinary stream-ordered launch (the previous kernel has finished, and its
 // writes are visible, before this one starts).
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_k(bool pdl, void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                             cudaStream_t st, Args&&... args) {
+    if (g_order_marks.load(std::memory_order_relaxed) > 0 && take_order_mark(st)) pdl = false;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -103,6 +111,19 @@ __device__ __forceinline__ int mx_exponent(float amax) {
 
 // 2^-E as fp32 for E in [-127, 125] (always a normal number).
 __device__ __forceinline__ float pow2_neg(int e) { return __uint_as_float((uint32_t)(127 - e) << 23); }
+
+// Raises a kernel's limit of dynamic shared memory, once per device (64 devices at most are remembered).
+template <typename Kernel>
+inline cudaError_t allow_smem(std::atomic<uint64_t>& done, Kernel* kernel, int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 // ---- paged cache layout (see idx.h) ------------------------------------------------------
 // MXFP4: byte offset in a page of 16-byte chunk c (scale block c) of in-page token s.

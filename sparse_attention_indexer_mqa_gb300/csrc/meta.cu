@@ -9,12 +9,32 @@
 // request by binary search in the sums, which stay in shared memory (8 bytes a request).
 // Reads and writes of the page table never meet: a row reads entries below ceil(ctx/P) or
 // the free list, and only entries from ceil(ctx/P) on are written.
-#include "kernels.h"
+#include <algorithm>
+#include <mutex>
+#include <thread>
+#include <tuple>
+#include <vector>
+
 #include "common.cuh"
+#include "kernels.h"
 
 namespace idx {
 
+std::atomic<int> g_order_marks{0};
+
 namespace {
+
+// Streams whose last library call was idx_step_meta. A per-thread default stream has one handle in every
+// thread, and a device's legacy stream has the handle of every other's.
+using StreamKey = std::tuple<cudaStream_t, int, std::thread::id>;
+std::mutex order_mutex;
+std::vector<StreamKey> ordered;
+
+StreamKey key_of(cudaStream_t st) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    return {st, dev, st == cudaStreamPerThread ? std::this_thread::get_id() : std::thread::id()};
+}
 
 // Exclusive sum over the CTA of one value per thread, and the total.
 __device__ __forceinline__ int64_t cta_scan(int64_t v, int64_t* warp_sums, int64_t& total) {
@@ -145,12 +165,16 @@ __global__ void step_meta_kernel(const MetaArgs a, int rows_per_cta) {
     }
 }
 
-// Launched behind step_meta_kernel without programmatic serialisation: it starts when that
-// kernel's writes are visible. A call launched behind it with programmatic serialisation may
-// start beside it, but not beside step_meta_kernel.
-__global__ void order_kernel() {}
-
 }  // namespace
+
+bool take_order_mark(cudaStream_t st) {
+    std::lock_guard<std::mutex> lock(order_mutex);
+    const auto it = std::find(ordered.begin(), ordered.end(), key_of(st));
+    if (it == ordered.end()) return false;
+    ordered.erase(it);
+    g_order_marks.store((int)ordered.size(), std::memory_order_relaxed);
+    return true;
+}
 
 cudaError_t launch_step_meta(const MetaArgs& a, cudaStream_t st) {
     // the sums need a thread per request, the rows want four per thread
@@ -164,8 +188,13 @@ cudaError_t launch_step_meta(const MetaArgs& a, cudaStream_t st) {
         if (e != cudaSuccess) return e;
     }
     const cudaError_t e = launch_k(false, step_meta_kernel, dim3((unsigned)ctas), dim3(threads), smem, st, a, rows);
-    if (e != cudaSuccess) return e;
-    return launch_k(false, order_kernel, dim3(1), dim3(32), 0, st);
+    if (e == cudaSuccess) {
+        std::lock_guard<std::mutex> lock(order_mutex);
+        const StreamKey k = key_of(st);
+        if (std::find(ordered.begin(), ordered.end(), k) == ordered.end()) ordered.push_back(k);
+        g_order_marks.store((int)ordered.size(), std::memory_order_relaxed);
+    }
+    return e;
 }
 
 }  // namespace idx

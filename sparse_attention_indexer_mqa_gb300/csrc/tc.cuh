@@ -59,6 +59,20 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
     }
 }
 
+// The same, bounded by a number of tests (each takes tens of cycles: seconds in all) instead of the
+// global timer. kNs > 0: sleeps that long between tests. A warp that tests without a pause takes
+// shared-memory cycles from the tensor core's operand reads.
+constexpr uint32_t kWaitTests = 1u << 24;
+template <int kNs>
+__device__ __forceinline__ bool mbar_spin(uint64_t* bar, uint32_t parity) {
+#pragma unroll 1
+    for (uint32_t i = 0; i < kWaitTests; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (kNs > 0) __nanosleep(kNs);
+    }
+    return false;
+}
+
 // Wait for the phase with the given parity, giving up at the global-timer deadline.
 __device__ __forceinline__ bool mbar_wait_until(uint64_t* bar, uint32_t parity, uint64_t deadline_ns) {
     for (;;) {

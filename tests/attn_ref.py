@@ -139,8 +139,9 @@ def attention(q, pool, P, Hkv, table, lens, cu, causal, scale, sel=None, out_typ
     rounding, 2^-23), the factor's three roundings and u's own (8 * 2^-24 * (|s| + 64 for Ev and
     the shift, in units of ln 2)), and bf16 q below 2^-28 of the row's largest (2^-39 of it). The
     weights follow with a relative 2 * ds + 2^-21 (ex2.approx: 2 ulp), and fp16 rounds them by
-    2^-11; below fp16's normal range (2^-26 of the row's largest u) by 2^-37 of the row's largest
-    weighted code (u carries V's block scale, so that is taken over p * 2^Ev). Sums over n keys: n * 2^-23
+    2^-11; below fp16's normal range (largest weight at least 2^7, half a subnormal step 2^-25) by
+    2^-32 of the row's largest weighted code (u carries V's block scale, so that is taken over
+    p * 2^Ev). Sums over n keys: n * 2^-23
     relative. The output's own rounding is half a step of its type."""
     dev = q.device
     T, Hq, D = q.shape
@@ -189,6 +190,6 @@ def attention(q, pool, P, Hkv, table, lens, cu, causal, scale, sel=None, out_typ
                 top = (p * torch.exp2(ev)).amax(-1, keepdim=True)
                 A = p @ v.abs()
                 o = out[t, hs]
-                otol[t, hs] = (2.0 ** -11 + 2 * rel) * A + N * 2.0 ** -37 * 448.0 * top + half * o.abs() * 1.01 + tiny
+                otol[t, hs] = (2.0 ** -11 + 2 * rel) * A + N * 2.0 ** -32 * 448.0 * top + half * o.abs() * 1.01 + tiny
                 ltol[t, hs] = (ds + N * 2.0 ** -23)[:, 0] + 2.0 ** -22 * (1 + lse[t, hs].abs() + 64)
     return out, lse, otol, ltol
