@@ -358,14 +358,14 @@ def idx_step_meta(ctx_lens, q_lens, page_table, page_size, max_seq_len_k, free_p
     if slot_mapping.dtype is not _torch.int64 or slot_mapping.dim() != 1 or slot_mapping.get_device() != dev or \
             not slot_mapping.is_contiguous():
         _refuse(fn, "slot_mapping", slot_mapping, _torch.int64, 1, True)
-    B, T = len(ctx_lens), len(slot_mapping)
+    B, T = ctx_lens.numel(), slot_mapping.numel()
     rows, width = page_table.shape
-    if (len(q_lens) != B or rows != B or len(seq_lens_k) != B or len(cu_seqlens_q) != B + 1 or len(positions) != T
-            or len(free_span) != 2 or len(free_next) != 1):
+    if (q_lens.numel() != B or rows != B or seq_lens_k.numel() != B or cu_seqlens_q.numel() != B + 1
+            or positions.numel() != T or free_span.numel() != 2 or free_next.numel() != 1):
         raise ValueError(f"{fn}: shapes do not belong to {B} requests and {T} rows")
     st = (_lib or load()).idx_step_meta(
         ctx_lens.data_ptr(), q_lens.data_ptr(), B, page_table.data_ptr(), width, page_size, max_seq_len_k,
-        free_pages.data_ptr(), len(free_pages), free_span.data_ptr(), num_pages, cu_seqlens_q.data_ptr(),
+        free_pages.data_ptr(), free_pages.numel(), free_span.data_ptr(), num_pages, cu_seqlens_q.data_ptr(),
         seq_lens_k.data_ptr(), positions.data_ptr(), slot_mapping.data_ptr(), T, free_next.data_ptr(),
         _ptr(dev_status), _stream(stream))
     if st:
@@ -398,8 +398,8 @@ def idx_kv_store(k, v, slot_mapping, pool, num_pages, page_size, page_stride, de
             not slot_mapping.is_contiguous():
         _refuse(fn, "slot_mapping", slot_mapping, _torch.int64, 1, True)
     n, H, D = k.shape
-    if v.shape != k.shape or len(slot_mapping) != n:
-        raise ValueError(f"{fn}: k {tuple(k.shape)}, v {tuple(v.shape)} and {len(slot_mapping)} slots do not match")
+    if v.shape != k.shape or slot_mapping.numel() != n:
+        raise ValueError(f"{fn}: k {tuple(k.shape)}, v {tuple(v.shape)} and {slot_mapping.numel()} slots do not match")
     kr, kh, kd = k.stride()
     vr, vh, vd = v.stride()
     if n > 0 and (kd != 1 or vd != 1):
@@ -441,11 +441,11 @@ def idx_attn_paged(q, pool, num_pages, page_size, page_stride, kv_heads, page_ta
         if x.dtype is not i32 or x.dim() != 1 or x.get_device() != dev or not x.is_contiguous():
             _refuse(fn, "seq_lens_k and cu_seqlens_q", x, i32, 1, True)
     T, H, D = q.shape
-    B = len(seq_lens_k)
+    B = seq_lens_k.numel()
     rows, width = page_table.shape
-    if out.shape != q.shape or rows != B or len(cu_seqlens_q) != B + 1:
+    if out.shape != q.shape or rows != B or cu_seqlens_q.numel() != B + 1:
         raise ValueError(f"{fn}: q {tuple(q.shape)}, out {tuple(out.shape)}, page_table {tuple(page_table.shape)}, "
-                         f"seq_lens_k {B} and cu_seqlens_q {len(cu_seqlens_q)} do not match")
+                         f"seq_lens_k {B} and cu_seqlens_q {cu_seqlens_q.numel()} do not match")
     qr, qh, qd = q.stride()
     orow, oh, od = out.stride()
     if T > 0 and (qd != 1 or od != 1):

@@ -2,13 +2,12 @@
 // split key axis, and the choice between this kernel and the tensor-memory one (attn_tc.cu).
 //
 // A unit is up to 16 query rows of one kv head (the rows of its group of heads, token after
-// token) against a range of keys. Its four warps take 16 keys in turn, each with a running softmax
+// token) against a range of keys. Its four warps take 32 keys in turn, each with a running softmax
 // of its own; they are joined at the end. With 16 rows the work is streaming: 2*D bytes a key,
-// 64*D multiply-adds. So K and V go from memory to the registers of the thread that uses them, by
-// way of a ring of private 16-byte pieces in shared memory (cp.async: 4 stages in flight
-// without registers or barriers; no thread reads what another one copied), and from there as
-// fp16 (exact for e4m3) into mma.m16n8k16. Both products are free to permute their contraction
-// axis, so a thread's piece is 16 consecutive bytes in memory:
+// 64*D multiply-adds. K and V go by cp.async (whole 128-byte lines: a quarter warp that touches more
+// lines than one pays for each) into a ring of the warp's own in shared memory, a step in flight while one is
+// worked on, and from there as fp16 (exact for e4m3) into mma.m16n8k16. Both products are free to
+// permute their contraction axis, so a thread's operands are 16 consecutive bytes:
 //   S = Q K^T: thread (r, c) = (lane / 4, lane % 4) holds key r's dims 64i + 16c .. + 15, the
 //     B operand of four steps over dims; Q is laid out to match.
 //   O = P V: S's accumulator is P's A operand as it stands: rows r, r + 8, keys 2c, 2c+1, 8+2c,
@@ -21,7 +20,8 @@ namespace idx {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kStages = 4;
+constexpr int kStages = 2;
+constexpr int kKeys = 32;  // of a warp's step
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -30,15 +30,9 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// kBytes from global to this thread's piece of the ring; zeros when ok is false
-template <int kBytes>
+// 16 bytes from global to shared memory; zeros when ok is false
 __device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool ok) {
-    const int n = ok ? kBytes : 0;
-    if constexpr (kBytes == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(n), "n"(kBytes)
-                     : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kLeft>
@@ -46,23 +40,25 @@ __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
-// One stage of a warp's ring: per lane kK 16-byte pieces of K, four kVB-byte pieces of V, scale words.
-template <int D, bool kSel>
+// A warp's ring: per stage 32 keys, their D bytes of K and of V in rows of 128 bytes (D = 128: K rows, then
+// V rows; D = 64: K and V halves of one row). 16-byte chunk x of key t's row lies at chunk
+// x ^ swizzle(t), which keeps both products' reads free of bank conflicts: 8 lanes read K chunks
+// 4d .. 4d+3 of two neighbouring keys, or V chunks of two dims groups of keys 0, 2, 4, 6 apart.
+template <int D>
 struct Ring {
-    static constexpr int kK = 2 * (D / 64);
-    static constexpr int kVB = D / 8;
-    static constexpr int kS = kSel ? 4 : 1;  // scale words: each key's, or the block's
-    static constexpr int kVAt = kK * 512, kSAt = kVAt + 4 * kVB * 32;
-    static constexpr int kStage = kSAt + kS * 128;
+    static constexpr int kVB = D / 8;               // bytes of V per key and lane
+    static constexpr int kVAt = D == 128 ? kKeys * 128 : 0;
+    static constexpr int kStage = kKeys * 2 * D;
     static constexpr int kRing = kWarps * kStages * kStage;
     static constexpr int kLd = D + 4;  // row of the join buffer
     static constexpr int kJoin = kWarps * 16 * kLd * 4;
     static constexpr int kBytes = kRing > kJoin ? kRing : kJoin;
 };
+__device__ __forceinline__ constexpr int swizzle(int t) { return (((t >> 1) & 3) << 1) ^ ((t & 1) << 2); }
 
 template <int D, bool kHalf, bool kSel>
 __global__ void __launch_bounds__(kWarps * 32, 3) attn_rows_kernel(const AttnArgs a) {
-    using R = Ring<D, kSel>;
+    using R = Ring<D>;
     extern __shared__ __align__(16) uint8_t sm[];
     __shared__ float2 ml[kWarps][16];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, c = lane & 3;
@@ -161,86 +157,80 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attn_rows_kernel(const AttnArg
 
     // ---- the key loop -------------------------------------------------------------------------------
     uint8_t* ring = sm + warp * kStages * R::kStage;
-    const uint32_t ring_s = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + 16 * lane;
-    const uint32_t ring_v = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + R::kVAt + R::kVB * lane;
-    const uint32_t ring_x = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + R::kSAt + 4 * lane;
+    const uint32_t ring_s = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+    // copies: a lane takes 16-byte piece ci of key ck + i * kCopyKeys (a quarter warp: one 128-byte line)
+    constexpr int kPieces = D / 8, kCopyKeys = 32 / kPieces, kCopies = kKeys / kCopyKeys;
+    const int ci = lane % kPieces, ck = lane / kPieces;
+    auto ring_at = [&](int t) -> uint32_t {  // where piece ci of key t goes
+        return (D == 128 ? (ci >> 3) * R::kVAt : 0) + t * 128 + (((ci & 7) ^ swizzle(t)) << 4);
+    };
     const int P = a.page_size, lp = P == 128 ? 7 : 6;
-    const int64_t hb = kv_head_bytes(P, D);
-    const uint8_t* pool = a.pool + (int64_t)head * hb;
+    const uint8_t* pool = a.pool + (int64_t)head * kv_head_bytes(P, D);
     const int32_t* pt = a.page_table + (int64_t)b * a.pt_stride;
-    const int n_it = k1 > k0 ? (k1 - k0 - 16 * warp + 16 * kWarps - 1) / (16 * kWarps) : 0;
-    const int kw = k0 + 16 * warp;  // this warp's first key; its next ones are 16 * kWarps further
+    constexpr int kStep = kWarps * kKeys;
+    const int kw = k0 + kKeys * warp;  // this warp's first key; its next ones are kStep further
+    const int n_it = k1 > kw ? (k1 - kw + kStep - 1) / kStep : 0;
+    const int vis_lo = __shfl_sync(kFull, vis[0], 0);  // rows see more and more keys: row 0 the fewest
     bool bad_page = false;
 
-    // Lookups run ahead of the copies: the page of step it + 1 (and, with a list, the entry of
-    // step it + 2) is loaded while step it's copies are issued. With a list, lane l holds entry l.
-    int32_t page_n = -1, entry_n = -1, entry_c = -1;
+    // Lookups run ahead: a step's page is loaded one step before its copies are issued and, with a
+    // list (lane l looks after entry l of the step), its entry two steps before.
+    int32_t page = -1, ent = -1, ent_n = -1;
     auto load_entry = [&](int it) -> int32_t {
-        const int e = kw + 16 * kWarps * it + (lane & 15);
-        return (it < n_it && e < k1) ? a.sel[tok0 * a.sel_stride + e] : -1;
+        const int e = kw + kStep * it + lane;
+        return e < k1 ? a.sel[tok0 * a.sel_stride + e] : -1;
     };
-    auto load_page = [&](int it, int32_t entry) -> int32_t {
-        if constexpr (kSel) {
-            return (entry >= 0 && entry < vis[0]) ? pt[entry >> lp] : -1;
-        } else {
-            return it < n_it ? pt[(kw + 16 * kWarps * it) >> lp] : -1;
-        }
+    auto load_page = [&](int it) -> int32_t {
+        if constexpr (kSel) return (ent >= 0 && ent < vis[0]) ? pt[ent >> lp] : -1;
+        return it < n_it ? pt[(kw + kStep * it) >> lp] : -1;
     };
-    uint32_t valid = 0;  // 4 bits per stage: the thread's keys 2c, 2c+1, 8+2c, 9+2c may be used
-    uint32_t half_sel = 0;  // 4 bits per stage: which half of the scale word is the key's (list)
+    // The scale bytes of a step, loaded with its copies. Dense: K, V of block 0, K, V of block 1, the same in
+    // every lane. List: K, V of entry l's block, bit 16 set where the entry counts.
+    uint32_t scales_n = 0;
+    bool page_ok_n = false;
     auto issue = [&](int it) {
-        const int st = it & (kStages - 1);
-        const uint32_t at = st * R::kStage;
+        const uint32_t at = (it & (kStages - 1)) * R::kStage;
+        scales_n = 0;
         if constexpr (kSel) {
-            int32_t page = page_n;
-            const int32_t ent = entry_c;
-            const bool seen = it < n_it && ent >= 0 && ent < vis[0];
-            if (seen && (uint32_t)page >= (uint64_t)a.num_pages) bad_page = true;
-            if (!seen || (uint32_t)page >= (uint64_t)a.num_pages) page = -1;
-            const int32_t tok = ent & (P - 1);
-            valid &= ~(15u << (4 * st));
-            half_sel &= ~(15u << (4 * st));
+            const bool seen = ent >= 0 && ent < vis[0], in = (uint32_t)page < (uint64_t)a.num_pages;
+            bad_page |= seen && !in;
+            const int pg = seen && in ? page : -1, tok = ent & (P - 1);
+            if (pg >= 0)
+                scales_n = *reinterpret_cast<const uint16_t*>(pool + (int64_t)pg * a.page_stride + 2ll * P * D +
+                                                             2 * (tok / kKvBlock)) | 65536u;
+            const int64_t row = pg < 0 ? -1 : (int64_t)pg * a.page_stride + tok * 2 * D;
+            const int lo = (int)row, hi = (int)(row >> 32);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {  // K: keys r, 8 + r
-                const int32_t pg = __shfl_sync(kFull, page, 8 * j + r), tk = __shfl_sync(kFull, tok, 8 * j + r);
-                const uint8_t* src = pool + (pg < 0 ? 0 : (int64_t)pg * a.page_stride + (int64_t)tk * 2 * D) + 16 * c;
-#pragma unroll
-                for (int d = 0; d < D / 64; ++d)
-                    cp_async<16>(ring_s + at + (j * (D / 64) + d) * 512, src + 64 * d, pg >= 0);
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {  // V and scales: keys 2c, 2c+1, 8+2c, 9+2c
-                const int from = (k >> 1) * 8 + 2 * c + (k & 1);
-                const int32_t pg = __shfl_sync(kFull, page, from), tk = __shfl_sync(kFull, tok, from);
-                const uint8_t* base = pool + (pg < 0 ? 0 : (int64_t)pg * a.page_stride);
-                const int t2 = pg < 0 ? 0 : tk;
-                cp_async<R::kVB>(ring_v + at + k * R::kVB * 32, base + (int64_t)t2 * 2 * D + D + r * R::kVB, pg >= 0);
-                cp_async<4>(ring_x + at + k * 128, base + 2ll * P * D + ((t2 / kKvBlock) & ~1) * 2, pg >= 0);
-                valid |= (pg >= 0 ? 1u : 0u) << (4 * st + k);
-                half_sel |= ((t2 / kKvBlock) & 1u) << (4 * st + k);
+            for (int i = 0; i < kCopies; ++i) {
+                const int t = ck + kCopyKeys * i;
+                const uint32_t l = __shfl_sync(kFull, lo, t);
+                const int h = __shfl_sync(kFull, hi, t);
+                const int64_t from = (int64_t)(((uint64_t)(uint32_t)h << 32) | l);
+                cp_async(ring_s + at + ring_at(t), pool + (h < 0 ? 0 : from + 16 * ci), h >= 0);
             }
         } else {
-            const int kb = kw + 16 * kWarps * it;
-            const bool in = it < n_it;
-            const bool okp = in && (uint32_t)page_n < (uint64_t)a.num_pages;
-            if (in && !okp) bad_page = true;
-            const int tk = kb & (P - 1);
-            const uint8_t* base = pool + (okp ? (int64_t)page_n * a.page_stride : 0);
-            const uint8_t* tok = base + (okp ? (int64_t)tk * 2 * D : 0);
+            const int kb = kw + kStep * it;
+            page_ok_n = it < n_it && (uint32_t)page < (uint64_t)a.num_pages;
+            bad_page |= it < n_it && !page_ok_n;
+            if (page_ok_n) {
+                const uint8_t* base = pool + (int64_t)page * a.page_stride;
+                const int tok = kb & (P - 1);
+                scales_n = *reinterpret_cast<const uint32_t*>(base + 2ll * P * D + 2 * (tok / kKvBlock));
+                const uint8_t* row = base + tok * 2 * D;
+                const uint8_t* src = row + ck * 2 * D + 16 * ci;
+                auto copy = [&](auto whole_tag) {  // whole: no key of the step lies behind the end
+                    constexpr bool kWhole = decltype(whole_tag)::value;
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int d = 0; d < D / 64; ++d)
-                    cp_async<16>(ring_s + at + (j * (D / 64) + d) * 512,
-                                 tok + (8 * j + r) * 2 * D + 16 * c + 64 * d, okp && kb + 8 * j + r < k1);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int key = (k >> 1) * 8 + 2 * c + (k & 1);
-                cp_async<R::kVB>(ring_v + at + k * R::kVB * 32, tok + key * 2 * D + D + r * R::kVB,
-                                 okp && kb + key < k1);
+                    for (int i = 0; i < kCopies; ++i) {
+                        const int t = ck + kCopyKeys * i;
+                        cp_async(ring_s + at + ring_at(t), src + kCopyKeys * i * 2 * D, kWhole || kb + t < k1);
+                    }
+                };
+                if (kb + kKeys <= k1)
+                    copy(std::true_type{});
+                else
+                    copy(std::false_type{});
             }
-            cp_async<4>(ring_x + at, base + 2ll * P * D + (okp ? ((tk / kKvBlock) & ~1) * 2 : 0), okp);
-            valid = (valid & ~(1u << st)) | (okp ? 1u : 0u) << st;
         }
         cp_async_commit();
     };
@@ -252,137 +242,155 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attn_rows_kernel(const AttnArg
 #pragma unroll
         for (int x = 0; x < 4; ++x) o[j][x] = 0.0f;
 
-    if (n_it > 0) {
-        entry_c = kSel ? load_entry(0) : -1;
-        entry_n = kSel ? load_entry(1) : -1;
-        page_n = load_page(0, entry_c);
-#pragma unroll 1
-        for (int it = -(kStages - 1); it < n_it; ++it) {
-            const int ahead = it + kStages - 1;
-            {
-                const int32_t e2 = kSel ? load_entry(ahead + 2) : -1;
-                const int32_t p2 = load_page(ahead + 1, entry_n);
-                issue(ahead);
-                page_n = p2;
-                entry_c = entry_n;
-                entry_n = e2;
-            }
-            if (it < 0) continue;
-            cp_async_wait<kStages - 1>();
-            const int st = it & (kStages - 1);
-            const uint8_t* sp = ring + st * R::kStage;
-
-            float sc[2][4];
+    // kMask: some key may not be visible to some row (the end of what a row sees; lists)
+    auto compute = [&](int it, uint32_t scales, auto mask_tag) {
+        [[maybe_unused]] constexpr bool kMask = decltype(mask_tag)::value;
+        const uint8_t* sp = ring + (it & (kStages - 1)) * R::kStage;
+        [[maybe_unused]] const int kb = kw + kStep * it;
+        float sc[kKeys / 8][4];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < kKeys / 8; ++j)
 #pragma unroll
-                for (int x = 0; x < 4; ++x) sc[j][x] = 0.0f;
+            for (int x = 0; x < 4; ++x) sc[j][x] = 0.0f;
 #pragma unroll
-                for (int d = 0; d < D / 64; ++d) {
-                    const uint4 w = *reinterpret_cast<const uint4*>(sp + (j * (D / 64) + d) * 512 + 16 * lane);
-                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        for (int d = 0; d < D / 64; ++d)
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        uint32_t lo, hi;
-                        e4m3x4_to_f16x4(u[x], lo, hi);
-                        mma16816(sc[j], qa[d][x], lo, hi);
-                    }
+            for (int j = 0; j < kKeys / 8; ++j) {
+                const uint4 w = *reinterpret_cast<const uint4*>(sp + (8 * j + r) * 128 + (((4 * d + c) ^ swizzle(r)) << 4));
+                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    uint32_t lo, hi;
+                    e4m3x4_to_f16x4(u[x], lo, hi);
+                    mma16816(sc[j], qa[d][x], lo, hi);
                 }
             }
-            // u = s * c + Ev for the thread's four keys and two rows; masked ones to -inf
-            float ev[4], kc[4];
-            const int kb = kw + 16 * kWarps * it;
+        // u = s * c + Ev; masked ones to -inf
+        float ev[kKeys / 4], mx[2] = {neg_inf(), neg_inf()};
+        [[maybe_unused]] uint32_t use = ~0u;  // bit k: the thread's key 8(k/2) + 2c + k%2 counts
+#pragma unroll
+        for (int k = 0; k < kKeys / 4; ++k) {
+            uint32_t two;
             if constexpr (kSel) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t w = *reinterpret_cast<const uint32_t*>(sp + R::kSAt + k * 128 + 4 * lane);
-                    const uint32_t by = (half_sel >> (4 * st + k)) & 1u ? w >> 16 : w;
-                    kc[k] = k_scale(by);
-                    ev[k] = v_exponent(by);
-                }
+                two = __shfl_sync(kFull, scales, (k >> 1) * 8 + 2 * c + (k & 1));
+                if (!(two >> 16)) use &= ~(1u << k);
             } else {
-                const uint32_t w = *reinterpret_cast<const uint32_t*>(sp + R::kSAt + 4 * lane);
-                const uint32_t by = ((kb & (P - 1)) / kKvBlock) & 1 ? w >> 16 : w;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    kc[k] = k_scale(by);
-                    ev[k] = v_exponent(by);
-                }
+                two = k < 4 ? scales : scales >> 16;
             }
-            float mx[2] = {neg_inf(), neg_inf()};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    float& v = sc[k >> 1][2 * i + (k & 1)];
-                    bool see;
-                    if constexpr (kSel)
-                        see = (valid >> (4 * st + k)) & 1u;
-                    else
-                        see = ((valid >> st) & 1u) && kb + 8 * (k >> 1) + 2 * c + (k & 1) < vis[i];
-                    v = see ? fmaf(v, rc[i] * kc[k], ev[k]) : neg_inf();
-                    mx[i] = fmaxf(mx[i], v);
-                }
-            }
-            bool raise = false;
-            float f[2];
+            const float kc = k_scale(two);
+            ev[k] = v_exponent(two);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                mx[i] = fmaxf(mx[i], __shfl_xor_sync(kFull, mx[i], 1));
-                mx[i] = fmaxf(mx[i], __shfl_xor_sync(kFull, mx[i], 2));
-                f[i] = 1.0f;
-                if (mx[i] > m[i] + kLazy) {  // from -inf too
-                    f[i] = ex2(m[i] - mx[i]);
-                    m[i] = mx[i];
-                    raise = true;
-                }
+                float& v = sc[k >> 1][2 * i + (k & 1)];
+                v = fmaf(v, rc[i] * kc, ev[k]);
+                if constexpr (kSel)
+                    v = (use >> k) & 1u ? v : neg_inf();
+                else if constexpr (kMask)
+                    v = kb + (k >> 1) * 8 + 2 * c + (k & 1) < vis[i] ? v : neg_inf();
+                mx[i] = fmaxf(mx[i], v);
             }
-            if (__any_sync(kFull, raise)) {
+        }
+        bool raise = false;
+        float f[2];
 #pragma unroll
-                for (int j = 0; j < D / 8; ++j) {
-                    o[j][0] *= f[0]; o[j][1] *= f[0];
-                    o[j][2] *= f[1]; o[j][3] *= f[1];
-                }
-                l[0] *= f[0];
-                l[1] *= f[1];
+        for (int i = 0; i < 2; ++i) {
+            mx[i] = fmaxf(mx[i], __shfl_xor_sync(kFull, mx[i], 1));
+            mx[i] = fmaxf(mx[i], __shfl_xor_sync(kFull, mx[i], 2));
+            f[i] = 1.0f;
+            if (mx[i] > m[i] + kLazy) {  // from -inf too
+                f[i] = ex2(m[i] - mx[i]);
+                m[i] = mx[i];
+                raise = true;
             }
-            uint32_t pa[4];
+        }
+        if (__any_sync(kFull, raise)) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                // a row that saw nothing yet: its weights are 2^-inf
-                const float sub = m[i] == neg_inf() ? 0.0f : kShift - m[i];
+            for (int j = 0; j < D / 8; ++j) {
+                o[j][0] *= f[0]; o[j][1] *= f[0];
+                o[j][2] *= f[1]; o[j][3] *= f[1];
+            }
+            l[0] *= f[0];
+            l[1] *= f[1];
+        }
+        uint32_t pa[kKeys / 16][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            // a row that saw nothing yet: its weights are 2^-inf
+            const float sub = m[i] == neg_inf() ? 0.0f : kShift - m[i];
+#pragma unroll
+            for (int h = 0; h < kKeys / 16; ++h) {
                 float p[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) p[k] = ex2(sc[k >> 1][2 * i + (k & 1)] + sub);
+                for (int k = 0; k < 4; ++k) p[k] = ex2(sc[2 * h + (k >> 1)][2 * i + (k & 1)] + sub);
                 if constexpr (kSel) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        l[i] = fmaf(p[k], (valid >> (4 * st + k)) & 1u ? ex2(-ev[k]) : 0.0f, l[i]);
+                        l[i] = fmaf(p[k], (use >> (4 * h + k)) & 1u ? ex2(-ev[4 * h + k]) : 0.0f, l[i]);
                 } else {
-                    l[i] = fmaf(p[0] + p[1] + p[2] + p[3], (valid >> st) & 1u ? ex2(-ev[0]) : 0.0f, l[i]);
+                    l[i] = fmaf((p[0] + p[1]) + (p[2] + p[3]), ex2(-ev[4 * h]), l[i]);
                 }
-                pa[i] = half2_bits(p[0], p[1]);
-                pa[2 + i] = half2_bits(p[2], p[3]);
+                pa[h][i] = half2_bits(p[0], p[1]);
+                pa[h][2 + i] = half2_bits(p[2], p[3]);
             }
-            // O += P V
+        }
+        // O += P V, 4 dims of four keys at a time
 #pragma unroll
-            for (int h = 0; h < (D == 128 ? 2 : 1); ++h) {  // 8 dims at a time
-                uint2 v[4];
+        for (int h = 0; h < kKeys / 16; ++h) {
+            uint4 v[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    v[k] = *reinterpret_cast<const uint2*>(sp + R::kVAt + k * R::kVB * 32 + R::kVB * lane + 8 * h);
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const uint32_t w0 = x ? v[0].y : v[0].x, w1 = x ? v[1].y : v[1].x;
-                    const uint32_t w2 = x ? v[2].y : v[2].x, w3 = x ? v[3].y : v[3].x;
-                    uint32_t b0[4], b1[4];
-                    e4m3x4_to_f16x4(__byte_perm(w0, w1, 0x5140), b0[0], b0[1]);
-                    e4m3x4_to_f16x4(__byte_perm(w0, w1, 0x7362), b0[2], b0[3]);
-                    e4m3x4_to_f16x4(__byte_perm(w2, w3, 0x5140), b1[0], b1[1]);
-                    e4m3x4_to_f16x4(__byte_perm(w2, w3, 0x7362), b1[2], b1[3]);
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) mma16816(o[8 * h + 4 * x + y], pa, b0[y], b1[y]);
+            for (int k = 0; k < 4; ++k) {
+                const int t = 16 * h + (k >> 1) * 8 + 2 * c + (k & 1);
+                if constexpr (D == 128) {
+                    v[k] = *reinterpret_cast<const uint4*>(sp + R::kVAt + t * 128 + ((r ^ swizzle(t)) << 4));
+                } else {
+                    const uint2 w = *reinterpret_cast<const uint2*>(sp + t * 128 + (((4 + (r >> 1)) ^ swizzle(t)) << 4) + 8 * (r & 1));
+                    v[k].x = w.x;
+                    v[k].y = w.y;
                 }
+            }
+#pragma unroll
+            for (int y = 0; y < R::kVB / 4; ++y) {
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w[k] = y == 0 ? v[k].x : y == 1 ? v[k].y : y == 2 ? v[k].z : v[k].w;
+                uint32_t b0[4], b1[4];
+                e4m3x4_to_f16x4(__byte_perm(w[0], w[1], 0x5140), b0[0], b0[1]);
+                e4m3x4_to_f16x4(__byte_perm(w[0], w[1], 0x7362), b0[2], b0[3]);
+                e4m3x4_to_f16x4(__byte_perm(w[2], w[3], 0x5140), b1[0], b1[1]);
+                e4m3x4_to_f16x4(__byte_perm(w[2], w[3], 0x7362), b1[2], b1[3]);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) mma16816(o[4 * y + q], pa[h], b0[q], b1[q]);
+            }
+        }
+    };
+
+    if (n_it > 0) {
+        if constexpr (kSel) {
+            ent = load_entry(0);
+            ent_n = load_entry(1);
+        }
+        page = load_page(0);
+#pragma unroll 1
+        for (int it = -1; it < n_it; ++it) {
+            const uint32_t scales = scales_n;
+            const bool page_ok = page_ok_n;
+            __syncwarp();  // the stage that comes next has been read by every lane
+            issue(it + 1);
+            if constexpr (kSel) {
+                ent = ent_n;
+                ent_n = load_entry(it + 3);
+            }
+            page = load_page(it + 2);
+            if (it < 0) continue;
+            cp_async_wait<kStages - 1>();
+            __syncwarp();  // every lane's copies have arrived
+            if constexpr (kSel) {
+                compute(it, scales, std::true_type{});
+            } else if (page_ok) {  // else none of these keys exists
+                if (kw + kStep * it + kKeys <= vis_lo)
+                    compute(it, scales, std::false_type{});
+                else
+                    compute(it, scales, std::true_type{});
             }
         }
         cp_async_wait<0>();
@@ -447,42 +455,63 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attn_rows_kernel(const AttnArg
     }
 }
 
-// Joins the splits of a key axis: a warp per (query row, head).
+// Joins the splits of a key axis: a CTA per (query row, head), its warps taking splits in turn so that
+// their loads are in flight together, then summed in shared memory.
+constexpr int kJoinWarps = 4;
 template <int D, bool kHalf>
-__global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const AttnArgs a) {
     constexpr int kPer = D / 32;  // dims of a lane
-    const int lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    __shared__ float part[kJoinWarps][D];
+    __shared__ float part_l[kJoinWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t row = blockIdx.x, t = row / a.q_heads, step = a.T * a.q_heads;
+    const int hq = (int)(row % a.q_heads);
     pdl_wait();
     pdl_launch_dependents();
-    if (row >= a.T * a.q_heads) return;
-    const int64_t t = row / a.q_heads;
-    const int hq = (int)(row % a.q_heads);
     const int b = seq_of_query(a.cu_seqlens_q, a.B, t);
     if (b < 0 || seq_rows(a, b).nq < 0) return;
-    const int64_t step = a.T * a.q_heads;
+    // every warp: all maxima, two splits to a lane at most
+    float2 ml[2];
     float M = neg_inf();
-    for (int z = lane; z < a.n_split; z += 32) M = fmaxf(M, a.part_ml[row + z * step].x);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        ml[i] = lane + 32 * i < a.n_split ? a.part_ml[row + (lane + 32 * i) * step] : make_float2(neg_inf(), 0.0f);
+        M = fmaxf(M, ml[i].x);
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
-    float L = 0.0f, v[kPer];
+    float g[2], L = 0.0f, v[kPer];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) g[i] = ml[i].x == M ? 1.0f : ex2(ml[i].x - M);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) v[i] = 0.0f;
 #pragma unroll 4
-    for (int z = 0; z < a.n_split; ++z) {
-        const int64_t pr = row + z * step;
-        const float2 x = a.part_ml[pr];
-        if (x.y == 0.0f) continue;  // that split had no key for this row and wrote no O
-        const float g = x.x == M ? 1.0f : ex2(x.x - M);
-        L = fmaf(g, x.y, L);
+    for (int z = warp; z < a.n_split; z += kJoinWarps) {
+        const float gz = __shfl_sync(kFull, z < 32 ? g[0] : g[1], z & 31);
+        const float lz = __shfl_sync(kFull, z < 32 ? ml[0].y : ml[1].y, z & 31);
+        if (lz == 0.0f) continue;  // that split had no key for this row and wrote no O
+        L = fmaf(gz, lz, L);
+        const float* src = a.part_o + (row + z * step) * D + kPer * lane;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) v[i] = fmaf(g, a.part_o[pr * D + kPer * lane + i], v[i]);
+        for (int i = 0; i < kPer; ++i) v[i] = fmaf(gz, src[i], v[i]);
     }
-    const float g = L == 0.0f ? 0.0f : 1.0f / L;
-    uint32_t* out = reinterpret_cast<uint32_t*>(a.out + t * a.out_row_stride + (int64_t)hq * a.out_head_stride + kPer * lane);
 #pragma unroll
-    for (int i = 0; i < kPer; i += 2) out[i / 2] = store_pair<kHalf>(v[i] * g, v[i + 1] * g);
-    if (a.lse && lane == 0) a.lse[row] = lse_of(M, L);
+    for (int i = 0; i < kPer; ++i) part[warp][kPer * lane + i] = v[i];
+    if (lane == 0) part_l[warp] = L;
+    __syncthreads();
+    if (threadIdx.x >= D / 2) return;
+    L = 0.0f;
+    float x = 0.0f, y = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+        L += part_l[w];
+        x += part[w][2 * threadIdx.x];
+        y += part[w][2 * threadIdx.x + 1];
+    }
+    const float n = L == 0.0f ? 0.0f : 1.0f / L;
+    uint16_t* out = a.out + t * a.out_row_stride + (int64_t)hq * a.out_head_stride;
+    reinterpret_cast<uint32_t*>(out)[threadIdx.x] = store_pair<kHalf>(x * n, y * n);
+    if (a.lse && threadIdx.x == 0) a.lse[row] = lse_of(M, L);
 }
 
 // Rows that share their keys: those of a sequence and a kv head, or with a list those of a query's group.
@@ -492,7 +521,7 @@ bool use_tile(const AttnArgs& a) { return shared_rows(a) > 16; }
 
 template <int D, bool kHalf, bool kSel>
 cudaError_t launch_rows(const AttnArgs& a, cudaStream_t st) {
-    constexpr int smem = Ring<D, kSel>::kBytes;
+    constexpr int smem = Ring<D>::kBytes;
     auto* kernel = attn_rows_kernel<D, kHalf, kSel>;
     static std::atomic<uint64_t> allowed{0};
     const cudaError_t e = allow_smem(allowed, kernel, smem);
@@ -510,7 +539,7 @@ cudaError_t launch_d(const AttnArgs& a, cudaStream_t st) {
                                 : launch_rows<D, kHalf, false>(a, st);
     if (e != cudaSuccess || a.n_split <= 1) return e;
     const int64_t rows = a.T * a.q_heads;
-    return launch_pdl(attn_join_kernel<D, kHalf>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, st, a);
+    return launch_pdl(attn_join_kernel<D, kHalf>, dim3((unsigned)rows), dim3(kJoinWarps * 32), 0, st, a);
 }
 
 }  // namespace
@@ -523,12 +552,19 @@ int64_t attn_plan(AttnArgs& a, int64_t bytes) {
     const int64_t units = (a.n_sel ? a.T : a.B) * ((shared_rows(a) + per_unit - 1) / per_unit) * a.kv_heads;
     const int64_t keys = a.n_sel ? a.n_sel : a.max_seq_len_k;
     const int64_t per_split = a.T * a.q_heads * (a.head_dim + 2) * 4;
-    // two rounds of resident CTAs (three or two to an SM), four steps of keys to a CTA at least
-    const int64_t slots = 2ll * sms * (tile ? 2 : 3), least = tile ? 512 : 256;
-    int64_t want = units > 0 ? (slots + units - 1) / units : 1;
-    want = want < (keys + least - 1) / least ? want : (keys + least - 1) / least;
-    want = want > 64 ? 64 : want;
-    if (want < 1) want = 1;
+    // Splits. Units that fill the resident CTAs (three or two to an SM) by themselves are cut until there are
+    // about four rounds of them, in pieces of 1024 keys at least (64 sequences of 8192 keys, 8
+    // kv heads: 203 / 196 / 188 / 194 us with 1 / 2 / 4 / 7 splits); fewer units are cut until they fill one
+    // round, in pieces of 512 keys at least (two sequences of 131071 keys, 4 kv heads: 36 / 32 / 31
+    // / 43 us with 32 / 38 / 57 / 64, the last one round and a bit).
+    const int64_t slots = (int64_t)sms * (tile ? 2 : 3);
+    int64_t want = 1;
+    if (units > 0) {
+        const auto least = [](int64_t x, int64_t y) { return x < y ? x : y; };
+        want = least(64, least(4 * slots / units, keys / 1024));
+        if (units * want < slots + slots / 2) want = least(64, least(slots / units, keys / 512));
+        if (want < 1) want = 1;
+    }
     const int64_t fits = per_split > 0 ? bytes / per_split : 1;
     int64_t n = want < fits ? want : fits;
     if (n < 1) n = 1;

@@ -190,9 +190,9 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
         // One step of the running softmax: S to P, with the rows' visibility tested key by key
         // (kCut, the tiles that some row of the warp does not see whole) or not.
         auto step = [&](int j, auto cut_tag) {
-            constexpr bool kCut = decltype(cut_tag)::value;
+            [[maybe_unused]] constexpr bool kCut = decltype(cut_tag)::value;
             const float4* sc = scales + (j & 1) * kKeysT;
-            const int left = vis - (k0 + j * kKeysT);  // keys of this step that the row sees
+            [[maybe_unused]] const int left = vis - (k0 + j * kKeysT);  // keys of this step that the row sees
             float mx = neg_inf();
 #pragma unroll 1
             for (int c = 0; c < 4; c += 2) {
