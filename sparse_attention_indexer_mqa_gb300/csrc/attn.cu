@@ -556,13 +556,15 @@ int64_t attn_plan(AttnArgs& a, int64_t bytes) {
     // about four rounds of them, in pieces of 1024 keys at least (64 sequences of 8192 keys, 8
     // kv heads: 203 / 196 / 188 / 194 us with 1 / 2 / 4 / 7 splits); fewer units are cut until they fill one
     // round, in pieces of 512 keys at least (two sequences of 131071 keys, 4 kv heads: 36 / 32 / 31
-    // / 43 us with 32 / 38 / 57 / 64, the last one round and a bit).
+    // / 43 us with 32 / 38 / 57 / 64, the last one round and a bit), or of 256 where those are fewer
+    // than the SMs (one sequence of 4000 keys: 20.7 / 13.6 / 10.6 / 9.2 us with 2 / 4 / 8 / 16).
     const int64_t slots = (int64_t)sms * (tile ? 2 : 3);
     int64_t want = 1;
     if (units > 0) {
         const auto least = [](int64_t x, int64_t y) { return x < y ? x : y; };
         want = least(64, least(4 * slots / units, keys / 1024));
-        if (units * want < slots + slots / 2) want = least(64, least(slots / units, keys / 512));
+        if (units * want < slots + slots / 2)
+            want = least(64, least(slots / units, keys / (units * keys <= 256ll * sms ? 256 : 512)));
         if (want < 1) want = 1;
     }
     const int64_t fits = per_split > 0 ? bytes / per_split : 1;

@@ -88,6 +88,11 @@ __device__ __forceinline__ int q_exponent(float amax) {
     return amax > 0.0f ? max(e, -100) - 14 : 0;
 }
 
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 template <bool kHalf>
 __device__ __forceinline__ float2 load_pair(uint32_t w) {
     if constexpr (kHalf) return __half22float2(*reinterpret_cast<const __half2*>(&w));

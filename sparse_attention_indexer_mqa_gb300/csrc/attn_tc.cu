@@ -28,12 +28,9 @@ namespace {
 constexpr int kRowsT = 128;   // rows of a tile
 constexpr int kKeysT = 128;   // keys of a step
 constexpr int kThreadsT = 256;
-#ifndef NSI
-#define NSI 0
-#define NSS 20
-#define NSC 40
-#endif
-constexpr int kNsIssue = NSI, kNsSoft = NSS, kNsConv = NSC;
+constexpr int kModePlain = 0, kModeCut = 1, kModeKeyed = 2;
+// Pauses between tests of a barrier (ns). None was measurably better or worse from 0 to 200.
+constexpr int kNsIssue = 0, kNsSoft = 20, kNsConv = 40;
 
 // Where 8 consecutive dims (chunk i) of q and k lie in the operand tiles: any order serves, and this one
 // lets 8 lanes that convert one key's consecutive 16-byte pieces write 8 different chunks.
@@ -49,7 +46,9 @@ struct SmemT {
     static constexpr int kV = kK + kKeysT * D * 2;          // [2][D dims][128 B]
     static constexpr int kScale = kV + kKeysT * D * 2;      // [2][128] float4: 2^Ek, Ev, 2^-Ev
     static constexpr int kOff = kScale + 2 * kKeysT * 16;   // [2][128] int64: a listed key's row in the pool
-    static constexpr int kBar = kOff + 2 * kKeysT * 8;
+    static constexpr int kKey = kOff + 2 * kKeysT * 8;      // [2][128] scale bytes of the listed keys
+    static constexpr int kRange = kKey + 2 * kKeysT * 4;    // [2][4] their ranges, a word per warp
+    static constexpr int kBar = kRange + 32;
     static constexpr int kBytes = kBar + 64 + 1024;         // 1024: alignment of the operand tiles
 };
 
@@ -187,10 +186,12 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
         const uint32_t lanes = (uint32_t)(warp * 32) << 16;
         const bool idle = 32 * warp >= rows;  // no row of this warp exists
         float m = neg_inf(), l = 0.0f;
-        // One step of the running softmax: S to P, with the rows' visibility tested key by key
-        // (kCut, the tiles that some row of the warp does not see whole) or not.
-        auto step = [&](int j, auto cut_tag) {
-            [[maybe_unused]] constexpr bool kCut = decltype(cut_tag)::value;
+        // One step of the running softmax: S to P. kPlain: a scale pair per 16 keys, all visible. kCut: the
+        // rows' visibility tested key by key (tiles that some row of the warp does not see whole).
+        // kKeyed: a scale pair per key, Ev = -inf where a key does not count (lists).
+        auto step = [&](int j, auto mode_tag) {
+            constexpr int kMode = decltype(mode_tag)::value;
+            constexpr bool kCut = kMode == kModeCut, kKeyed = kMode == kModeKeyed;
             const float4* sc = scales + (j & 1) * kKeysT;
             [[maybe_unused]] const int left = vis - (k0 + j * kKeysT);  // keys of this step that the row sees
             float mx = neg_inf();
@@ -205,7 +206,7 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
                 for (int h = 0; h < 4; ++h) {
                     const uint32_t* x = &r[h >> 1][16 * (h & 1)];
                     const int at = 32 * c + 16 * h;
-                    if constexpr (kSel) {
+                    if constexpr (kKeyed) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             const float4 k = sc[at + i];
@@ -263,7 +264,7 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
                     for (int h = 0; h < 2; ++h) {
                         const uint32_t* x = &r[g][16 * h];
                         const int at = 32 * (c + g) + 16 * h;
-                        if constexpr (kSel) {
+                        if constexpr (kKeyed) {
 #pragma unroll
                             for (int i = 0; i < 16; i += 2) {
                                 const float4 ka = sc[at + i], kb = sc[at + i + 1];
@@ -338,10 +339,12 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
             ok = warp_wait<kNsSoft>(s_full, (j + 1) & 1);
             if (!ok) break;
             tc::tc_fence_after();
-            if (!kSel && __any_sync(kFull, k0 + (j + 2) * kKeysT > vis))
-                step(j + 1, std::true_type{});
+            const bool special = kSel ? scales[((j + 1) & 1) * kKeysT].w != 0.0f
+                                      : __any_sync(kFull, k0 + (j + 2) * kKeysT > vis);
+            if (special)
+                step(j + 1, std::integral_constant<int, kSel ? kModeKeyed : kModeCut>{});
             else
-                step(j + 1, std::false_type{});
+                step(j + 1, std::integral_constant<int, kModePlain>{});
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(p_full);
         }
@@ -502,10 +505,37 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
                 rv[i] = w;
             }
         };
+        // A list's keys have scales of their own. Where a step's lie within 2^15 of one another and every key
+        // counts, they are folded into the fp16 operands (exact: a code is at least 2^-9, fp16
+        // reaches 2^-24) and the softmax sees one scale pair; otherwise it takes a pair per key.
+        uint32_t* key_scales = reinterpret_cast<uint32_t*>(sm + S::kKey);
+        uint32_t* ranges = reinterpret_cast<uint32_t*>(sm + S::kRange);
+        int k_top = 0, v_top = 0;  // largest scale bytes of the step
+        bool fold = false;
+        auto publish = [&](int j) {  // before the barrier
+            const uint32_t ek = scale_byte(my_scale), ev = scale_byte(my_scale >> 8);
+            const bool in = my_scale != 0;
+            const uint32_t k_hi = __reduce_max_sync(kFull, in ? ek : 255u), k_lo = __reduce_min_sync(kFull, in ? ek : 0u);
+            const uint32_t v_hi = __reduce_max_sync(kFull, in ? ev : 255u), v_lo = __reduce_min_sync(kFull, in ? ev : 0u);
+            key_scales[(j & 1) * kKeysT + ct] = my_scale;
+            if (lane == 0) ranges[(j & 1) * 4 + cw] = k_hi | k_lo << 8 | v_hi << 16 | v_lo << 24;
+        };
+        auto collect = [&](int j) {  // behind it
+            const uint4 r = *reinterpret_cast<const uint4*>(ranges + (j & 1) * 4);
+            const uint32_t hi = __vmaxu4(__vmaxu4(r.x, r.y), __vmaxu4(r.z, r.w));
+            const uint32_t lo = __vminu4(__vminu4(r.x, r.y), __vminu4(r.z, r.w));
+            k_top = hi & 255;
+            v_top = hi >> 16 & 255;
+            // a key that does not count makes the range too wide
+            fold = k_top - (int)(lo >> 8 & 255) <= 15 && v_top - (int)(lo >> 24) <= 15;
+        };
+        auto down = [&](int by) -> uint32_t {  // 2^-by as fp16 bits, by in 0 .. 15
+            return by < 15 ? (uint32_t)(15 - by) << 10 : 0x0200u;
+        };
         auto write_k = [&](int j) {
             const float ev = v_exponent(my_scale);
-            const float4 sc = my_scale ? make_float4(k_scale(my_scale), ev, ex2(-ev), 0.0f)
-                                       : make_float4(1.0f, neg_inf(), 0.0f, 0.0f);
+            const float4 sc = my_scale ? make_float4(k_scale(my_scale), ev, ex2(-ev), 1.0f)
+                                       : make_float4(1.0f, neg_inf(), 0.0f, 1.0f);
 #pragma unroll
             for (int i = 0; i < kPieces; ++i) {
                 const int key = k_key + kKeyStep * i;
@@ -514,18 +544,42 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
                 e4m3x4_to_f16x4(rk[i].y, lo.z, lo.w);
                 e4m3x4_to_f16x4(rk[i].z, hi.x, hi.y);
                 e4m3x4_to_f16x4(rk[i].w, hi.z, hi.w);
+                if constexpr (kSel) {
+                    if (fold) {
+                        const uint32_t f = down(k_top - (int)scale_byte(key_scales[(j & 1) * kKeysT + key])) * 65537u;
+                        lo.x = mul_f16x2(lo.x, f); lo.y = mul_f16x2(lo.y, f);
+                        lo.z = mul_f16x2(lo.z, f); lo.w = mul_f16x2(lo.w, f);
+                        hi.x = mul_f16x2(hi.x, f); hi.y = mul_f16x2(hi.y, f);
+                        hi.z = mul_f16x2(hi.z, f); hi.w = mul_f16x2(hi.w, f);
+                    }
+                }
                 uint8_t* row = sm + S::kK + key * 128;
                 *reinterpret_cast<uint4*>(row + dims_sub<D>(0) * (kKeysT * 128) + ((dims_chunk<D>(2 * kp) ^ (key & 7)) << 4)) = lo;
                 *reinterpret_cast<uint4*>(row + dims_sub<D>(1) * (kKeysT * 128) + ((dims_chunk<D>(2 * kp + 1) ^ (key & 7)) << 4)) = hi;
             }
-            if constexpr (kSel)
-                scales[(j & 1) * kKeysT + ct] = sc;
-            else if ((ct & 15) == 0)
+            if constexpr (kSel) {
+                if (!fold)
+                    scales[(j & 1) * kKeysT + ct] = sc;
+                else if (ct < 8)
+                    scales[(j & 1) * kKeysT + ct] = make_float4(__uint_as_float((uint32_t)k_top << 23), (float)(v_top - 127),
+                                                                ex2((float)(127 - v_top)), 0.0f);
+            } else if ((ct & 15) == 0) {
                 scales[(j & 1) * kKeysT + ct / 16] = sc;
+            }
             tc::fence_proxy_async();
             tc::mbar_arrive(k_full);
         };
-        auto write_v = [&]() {
+        auto write_v = [&](int j) {
+            uint32_t f[4] = {0, 0, 0, 0};  // factors of pairs of keys
+            if constexpr (kSel) {
+                if (fold) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint2 two = *reinterpret_cast<const uint2*>(key_scales + (j & 1) * kKeysT + 8 * kg + 2 * i);
+                        f[i] = down(v_top - (int)scale_byte(two.x >> 8)) | down(v_top - (int)scale_byte(two.y >> 8)) << 16;
+                    }
+                }
+            }
 #pragma unroll
             for (int w = 0; w < kVB / 4; ++w) {
                 uint32_t u[8];
@@ -537,6 +591,14 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
                     e4m3x4_to_f16x4(__byte_perm(u[2 * i], u[2 * i + 1], 0x5140), t[0][i], t[1][i]);
                     e4m3x4_to_f16x4(__byte_perm(u[2 * i], u[2 * i + 1], 0x7362), t[2][i], t[3][i]);
                 }
+                if constexpr (kSel) {
+                    if (fold) {
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) t[y][i] = mul_f16x2(t[y][i], f[i]);
+                    }
+                }
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
                     const int row = 8 * (4 * w + y) + dg;  // of dim kVB * dg + 4 * w + y
@@ -547,6 +609,7 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
             tc::fence_proxy_async();
             tc::mbar_arrive(v_full);
         };
+
         if (n > 0) {
             if constexpr (kSel) {
                 ent = load_entry(0);
@@ -558,7 +621,11 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
 #pragma unroll 1
             for (int j = -2; j + 1 < n; ++j) {
                 if (j >= 0) ok = warp_wait<kNsConv>(s_full, j & 1) && ok;
-                if constexpr (kSel) ok = conv_all(ok);  // leave together: place() has a barrier
+                if constexpr (kSel) {
+                    if (j >= -1) publish(j + 1);
+                    ok = conv_all(ok);  // leave together: place() has a barrier
+                    if (j >= -1) collect(j + 1);
+                }
                 if (!ok) break;
                 if (j >= -1) write_k(j + 1);
                 if (j + 2 < n) {
@@ -571,7 +638,7 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
                     lookup(j + 3);
                 }
                 if (j >= 0) ok = warp_wait<kNsConv>(o_done, j & 1) && ok;
-                if (j >= -1) write_v();
+                if (j >= -1) write_v(j + 1);
                 if (j + 2 < n) load_v(j + 2);
             }
         }
