@@ -28,7 +28,6 @@ namespace {
 constexpr int kRowsT = 128;   // rows of a tile
 constexpr int kKeysT = 128;   // keys of a step
 constexpr int kThreadsT = 256;
-constexpr int kModePlain = 0, kModeCut = 1, kModeKeyed = 2;
 // Pauses between tests of a barrier (ns). None was measurably better or worse from 0 to 200.
 constexpr int kNsIssue = 0, kNsSoft = 20, kNsConv = 40;
 
@@ -186,44 +185,8 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
         const uint32_t lanes = (uint32_t)(warp * 32) << 16;
         const bool idle = 32 * warp >= rows;  // no row of this warp exists
         float m = neg_inf(), l = 0.0f;
-        // One step of the running softmax: S to P. kPlain: a scale pair per 16 keys, all visible. kCut: the
-        // rows' visibility tested key by key (tiles that some row of the warp does not see whole).
-        // kKeyed: a scale pair per key, Ev = -inf where a key does not count (lists).
-        auto step = [&](int j, auto mode_tag) {
-            constexpr int kMode = decltype(mode_tag)::value;
-            constexpr bool kCut = kMode == kModeCut, kKeyed = kMode == kModeKeyed;
-            const float4* sc = scales + (j & 1) * kKeysT;
-            [[maybe_unused]] const int left = vis - (k0 + j * kKeysT);  // keys of this step that the row sees
-            float mx = neg_inf();
-#pragma unroll 1
-            for (int c = 0; c < 4; c += 2) {
-                uint32_t r[2][32];
-                __syncwarp();
-                tc::tmem_ld32(tm_s + lanes + 32 * c, r[0]);
-                tc::tmem_ld32(tm_s + lanes + 32 * c + 32, r[1]);
-                tc::tmem_ld_wait();
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    const uint32_t* x = &r[h >> 1][16 * (h & 1)];
-                    const int at = 32 * c + 16 * h;
-                    if constexpr (kKeyed) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float4 k = sc[at + i];
-                            mx = fmaxf(mx, fmaf(__uint_as_float(x[i]), rc * k.x, k.y));
-                        }
-                    } else {
-                        const float4 k = sc[at / 16];
-                        float bm = neg_inf();
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            bm = fmaxf(bm, !kCut || at + i < left ? __uint_as_float(x[i]) : neg_inf());
-                        // nothing visible: bm is -inf whatever the factor
-                        const float u = fmaf(bm, rc * k.x, k.y);
-                        mx = fmaxf(mx, kCut && bm == neg_inf() ? bm : u);
-                    }
-                }
-            }
+        // A row whose largest u passes m by more than kLazy: m raised, O and l scaled.
+        auto raise_to = [&](int j, float mx) {
             float f = 1.0f;
             const bool raise = mx > m + kLazy;
             if (raise) {
@@ -249,6 +212,36 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
                     tc::tmem_st16(tm_o + lanes + 32 * c + 16, r[1]);
                 }
             }
+        };
+        // One step of the running softmax, S to P, with a scale pair per 16 keys. kCut: the rows' visibility
+        // tested key by key (tiles that some row of the warp does not see whole).
+        auto step = [&](int j, auto cut_tag) {
+            constexpr bool kCut = decltype(cut_tag)::value;
+            const float4* sc = scales + (j & 1) * kKeysT;
+            [[maybe_unused]] const int left = vis - (k0 + j * kKeysT);  // keys of this step that the row sees
+            float mx = neg_inf();
+#pragma unroll 1
+            for (int c = 0; c < 4; c += 2) {
+                uint32_t r[2][32];
+                __syncwarp();
+                tc::tmem_ld32(tm_s + lanes + 32 * c, r[0]);
+                tc::tmem_ld32(tm_s + lanes + 32 * c + 32, r[1]);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    const uint32_t* x = &r[h >> 1][16 * (h & 1)];
+                    const int at = 32 * c + 16 * h;
+                    const float4 k = sc[at / 16];
+                    float bm = neg_inf();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        bm = fmaxf(bm, !kCut || at + i < left ? __uint_as_float(x[i]) : neg_inf());
+                    // nothing visible: bm is -inf whatever the factor
+                    const float u = fmaf(bm, rc * k.x, k.y);
+                    mx = fmaxf(mx, kCut && bm == neg_inf() ? bm : u);
+                }
+            }
+            raise_to(j, mx);
             const float top = m == neg_inf() ? 0.0f : kShift - m;
 #pragma unroll 1
             for (int c = 0; c < 4; c += 2) {
@@ -264,38 +257,66 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
                     for (int h = 0; h < 2; ++h) {
                         const uint32_t* x = &r[g][16 * h];
                         const int at = 32 * (c + g) + 16 * h;
-                        if constexpr (kKeyed) {
+                        const float4 k = sc[at / 16];
+                        const float cc = rc * k.x, sub = k.y + top;
+                        float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-                            for (int i = 0; i < 16; i += 2) {
-                                const float4 ka = sc[at + i], kb = sc[at + i + 1];
-                                const float pa = ex2(fmaf(__uint_as_float(x[i]), rc * ka.x, ka.y + top));
-                                const float pb = ex2(fmaf(__uint_as_float(x[i + 1]), rc * kb.x, kb.y + top));
-                                l = fmaf(pa, ka.z, l);
-                                l = fmaf(pb, kb.z, l);
-                                p2[8 * h + i / 2] = half2_bits(pa, pb);
+                        for (int i = 0; i < 16; i += 2) {
+                            float2 u = fma2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])),
+                                            make_float2(cc, cc), make_float2(sub, sub));
+                            if constexpr (kCut) {
+                                u.x = at + i < left ? u.x : neg_inf();
+                                u.y = at + i + 1 < left ? u.y : neg_inf();
                             }
-                        } else {
-                            const float4 k = sc[at / 16];
-                            const float cc = rc * k.x, sub = k.y + top;
-                            float2 sum = make_float2(0.0f, 0.0f);
-#pragma unroll
-                            for (int i = 0; i < 16; i += 2) {
-                                float2 u = fma2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])),
-                                                make_float2(cc, cc), make_float2(sub, sub));
-                                if constexpr (kCut) {
-                                    u.x = at + i < left ? u.x : neg_inf();
-                                    u.y = at + i + 1 < left ? u.y : neg_inf();
-                                }
-                                const float2 p = make_float2(ex2(u.x), ex2(u.y));
-                                sum = add2(sum, p);
-                                p2[8 * h + i / 2] = half2_bits(p.x, p.y);
-                            }
-                            l = fmaf(sum.x + sum.y, k.z, l);
+                            const float2 p = make_float2(ex2(u.x), ex2(u.y));
+                            sum = add2(sum, p);
+                            p2[8 * h + i / 2] = half2_bits(p.x, p.y);
                         }
+                        l = fmaf(sum.x + sum.y, k.z, l);
                     }
                     // columns 16(c+g) .. +15 held scores that have been read
                     tc::tmem_st16(tm_s + lanes + 16 * (c + g), p2);
                 }
+            }
+            tc::tmem_st_wait();
+            tc::tc_fence_before();
+        };
+        // The same with a scale pair per key (lists), Ev = -inf where a key does not count. 16 keys at a
+        // time: more registers would spill, and reloads that miss L1 hold up the thread that issues
+        // the MMAs.
+        auto step_keyed = [&](int j) {
+            const float4* sc = scales + (j & 1) * kKeysT;
+            float mx = neg_inf();
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+                uint32_t r[16];
+                __syncwarp();
+                tc::tmem_ld16(tm_s + lanes + 16 * c, r);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float4 k = sc[16 * c + i];
+                    mx = fmaxf(mx, fmaf(__uint_as_float(r[i]), rc * k.x, k.y));
+                }
+            }
+            raise_to(j, mx);
+            const float top = m == neg_inf() ? 0.0f : kShift - m;
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+                uint32_t r[16], p2[8];
+                __syncwarp();
+                tc::tmem_ld16(tm_s + lanes + 16 * c, r);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) {
+                    const float4 ka = sc[16 * c + i], kb = sc[16 * c + i + 1];
+                    const float pa = ex2(fmaf(__uint_as_float(r[i]), rc * ka.x, ka.y + top));
+                    const float pb = ex2(fmaf(__uint_as_float(r[i + 1]), rc * kb.x, kb.y + top));
+                    l = fmaf(pa, ka.z, l);
+                    l = fmaf(pb, kb.z, l);
+                    p2[i / 2] = half2_bits(pa, pb);
+                }
+                tc::tmem_st8(tm_s + lanes + 8 * c, p2);  // columns that have been read
             }
             tc::tmem_st_wait();
             tc::tc_fence_before();
@@ -339,12 +360,17 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
             ok = warp_wait<kNsSoft>(s_full, (j + 1) & 1);
             if (!ok) break;
             tc::tc_fence_after();
-            const bool special = kSel ? scales[((j + 1) & 1) * kKeysT].w != 0.0f
-                                      : __any_sync(kFull, k0 + (j + 2) * kKeysT > vis);
-            if (special)
-                step(j + 1, std::integral_constant<int, kSel ? kModeKeyed : kModeCut>{});
-            else
-                step(j + 1, std::integral_constant<int, kModePlain>{});
+            if constexpr (kSel) {
+                if (scales[((j + 1) & 1) * kKeysT].w != 0.0f)
+                    step_keyed(j + 1);
+                else
+                    step(j + 1, std::false_type{});
+            } else {
+                if (__any_sync(kFull, k0 + (j + 2) * kKeysT > vis))
+                    step(j + 1, std::true_type{});
+                else
+                    step(j + 1, std::false_type{});
+            }
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(p_full);
         }
