@@ -350,13 +350,12 @@ def idx_step_meta(ctx_lens, q_lens, page_table, page_size, max_seq_len_k, free_p
     fn, dev = "idx_step_meta", _device()
     i32 = _torch.int32
     for x in (ctx_lens, q_lens, free_pages, free_span, cu_seqlens_q, seq_lens_k, positions, free_next):
-        if x.dtype is not i32 or x.dim() != 1 or x.get_device() != dev or not x.is_contiguous():
+        if x.dtype is not i32 or x.get_device() != dev or not x.is_contiguous():
             _refuse(fn, "every list of lengths, pages or positions", x, i32, 1, True)
     if page_table.dtype is not i32 or page_table.dim() != 2 or page_table.get_device() != dev or \
             not page_table.is_contiguous():
         _refuse(fn, "page_table", page_table, i32, 2, True)
-    if slot_mapping.dtype is not _torch.int64 or slot_mapping.dim() != 1 or slot_mapping.get_device() != dev or \
-            not slot_mapping.is_contiguous():
+    if slot_mapping.dtype is not _torch.int64 or slot_mapping.get_device() != dev or not slot_mapping.is_contiguous():
         _refuse(fn, "slot_mapping", slot_mapping, _torch.int64, 1, True)
     B, T = ctx_lens.numel(), slot_mapping.numel()
     rows, width = page_table.shape
@@ -394,8 +393,7 @@ def idx_kv_store(k, v, slot_mapping, pool, num_pages, page_size, page_stride, de
         _refuse(fn, "k", k, k.dtype, 3, False)
     if v.dtype is not k.dtype or v.get_device() != dev:
         _refuse(fn, "v", v, k.dtype, 3, False)
-    if slot_mapping.dtype is not _torch.int64 or slot_mapping.dim() != 1 or slot_mapping.get_device() != dev or \
-            not slot_mapping.is_contiguous():
+    if slot_mapping.dtype is not _torch.int64 or slot_mapping.get_device() != dev or not slot_mapping.is_contiguous():
         _refuse(fn, "slot_mapping", slot_mapping, _torch.int64, 1, True)
     n, H, D = k.shape
     if v.shape != k.shape or slot_mapping.numel() != n:
@@ -438,7 +436,7 @@ def idx_attn_paged(q, pool, num_pages, page_size, page_stride, kv_heads, page_ta
             not page_table.is_contiguous():
         _refuse(fn, "page_table", page_table, i32, 2, True)
     for x in (seq_lens_k, cu_seqlens_q):
-        if x.dtype is not i32 or x.dim() != 1 or x.get_device() != dev or not x.is_contiguous():
+        if x.dtype is not i32 or x.get_device() != dev or not x.is_contiguous():
             _refuse(fn, "seq_lens_k and cu_seqlens_q", x, i32, 1, True)
     T, H, D = q.shape
     B = seq_lens_k.numel()

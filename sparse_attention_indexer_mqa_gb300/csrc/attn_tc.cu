@@ -29,7 +29,7 @@ constexpr int kRowsT = 128;   // rows of a tile
 constexpr int kKeysT = 128;   // keys of a step
 constexpr int kThreadsT = 256;
 // Pauses between tests of a barrier (ns). None was measurably better or worse from 0 to 200.
-constexpr int kNsIssue = 0, kNsSoft = 20, kNsConv = 40;
+constexpr int kNsIssue = 0, kNsSoft = 0, kNsConv = 20;
 
 // Where 8 consecutive dims (chunk i) of q and k lie in the operand tiles: any order serves, and this one
 // lets 8 lanes that convert one key's consecutive 16-byte pieces write 8 different chunks.

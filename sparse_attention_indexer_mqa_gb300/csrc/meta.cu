@@ -177,9 +177,10 @@ bool take_order_mark(cudaStream_t st) {
 }
 
 cudaError_t launch_step_meta(const MetaArgs& a, cudaStream_t st) {
-    // the sums need a thread per request, the rows want four per thread
+    // a thread per request for the sums where that fits, and a thread per row (512 requests, 66173 rows: 7.8 us, 11.8
+    // with four rows a thread)
     const int threads = a.B <= 256 ? 256 : 1024;
-    const int rows = 4 * threads;
+    const int rows = threads;
     const int64_t ctas = a.T_cap > rows ? (a.T_cap + rows - 1) / rows : 1;
     const size_t smem = (2 * (size_t)a.B + 1) * sizeof(int32_t);
     if (smem > 48 * 1024) {
