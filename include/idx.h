@@ -386,8 +386,12 @@ int idx_debug_wait_timeout(int32_t limit_us, int32_t* dev_status, cudaStream_t s
  *     In place, the call appends the pages that ctx + q tokens need: entries ceil(ctx/P) ..
  *     ceil((ctx+q)/P) - 1. Nothing else of it is written, and the appended entries are not read.
  *   free_pages: int32 [free_cap], page ids; free_span: int32 [2], the free ones are entries
- *     free_span[0] .. free_span[1] - 1. Requests take theirs from the front in request order;
- *     *free_next becomes the first entry not taken (the next step's free_span[0]).
+ *     free_span[0] .. free_span[1] - 1. Requests take theirs from the front in request order.
+ *     *free_next (int32 [1]) becomes free_span[0] + the pages that requests 0 .. b asked for, b the last
+ *     request that was not refused for want of pages: the first entry not taken, and so the next
+ *     step's free_span[0], unless IDX_STATUS_NO_PAGE is set. With that, what a refused request asked for
+ *     in front of b is counted too (it was not given out) and *free_next may lie behind free_span[1]:
+ *     whoever sees the bit takes stock of the free pages anew, by the page tables.
  *   Outputs: cu_seqlens_q int32 [B+1] (prefix sums of q_lens, at most T_cap); seq_lens_k int32
  *     [B] = ctx + q; for each row t < T_cap: positions[t] (int32) = ctx + i and
  *     slot_mapping[t] (int64) = page * P + position % P for the i-th new token of its request.

@@ -379,8 +379,7 @@ def idx_kv_layout(kv_heads: int, head_dim: int, page_size: int) -> IdxKvLayout:
 
 def _pool_bytes(fn, pool, num_pages, page_stride, page_bytes, dev):
     """The pool holds its pages: the library only sees a pointer."""
-    if pool.get_device() != dev or (num_pages > 0 and
-                                    pool.numel() * pool.element_size() < (num_pages - 1) * page_stride + page_bytes):
+    if pool.get_device() != dev or (num_pages > 0 and pool.nbytes < (num_pages - 1) * page_stride + page_bytes):
         raise ValueError(f"{fn}: the pool ({tuple(pool.shape)}, {pool.dtype}, {pool.device}) does not hold {num_pages} pages "
                          f"{page_stride} bytes apart on the current CUDA device")
 
@@ -395,8 +394,8 @@ def idx_kv_store(k, v, slot_mapping, pool, num_pages, page_size, page_stride, de
         _refuse(fn, "v", v, k.dtype, 3, False)
     if slot_mapping.dtype is not _torch.int64 or slot_mapping.get_device() != dev or not slot_mapping.is_contiguous():
         _refuse(fn, "slot_mapping", slot_mapping, _torch.int64, 1, True)
-    n, H, D = k.shape
-    if v.shape != k.shape or slot_mapping.numel() != n:
+    n, H, D = shape = k.shape
+    if v.shape != shape or slot_mapping.numel() != n:
         raise ValueError(f"{fn}: k {tuple(k.shape)}, v {tuple(v.shape)} and {slot_mapping.numel()} slots do not match")
     kr, kh, kd = k.stride()
     vr, vh, vd = v.stride()
@@ -438,10 +437,10 @@ def idx_attn_paged(q, pool, num_pages, page_size, page_stride, kv_heads, page_ta
     for x in (seq_lens_k, cu_seqlens_q):
         if x.dtype is not i32 or x.get_device() != dev or not x.is_contiguous():
             _refuse(fn, "seq_lens_k and cu_seqlens_q", x, i32, 1, True)
-    T, H, D = q.shape
+    T, H, D = shape = q.shape
     B = seq_lens_k.numel()
     rows, width = page_table.shape
-    if out.shape != q.shape or rows != B or cu_seqlens_q.numel() != B + 1:
+    if out.shape != shape or rows != B or cu_seqlens_q.numel() != B + 1:
         raise ValueError(f"{fn}: q {tuple(q.shape)}, out {tuple(out.shape)}, page_table {tuple(page_table.shape)}, "
                          f"seq_lens_k {B} and cu_seqlens_q {cu_seqlens_q.numel()} do not match")
     qr, qh, qd = q.stride()
@@ -470,7 +469,7 @@ def idx_attn_paged(q, pool, num_pages, page_size, page_stride, kv_heads, page_ta
     if workspace is not None:
         if workspace.get_device() != dev:
             raise ValueError(f"{fn}: the workspace is on {workspace.device}, not on the current CUDA device")
-        wsb, ws_p = workspace.numel() * workspace.element_size(), workspace.data_ptr()
+        wsb, ws_p = workspace.nbytes, workspace.data_ptr()
     st = (_lib or load()).idx_attn_paged(
         q.data_ptr(), ft, T, H, kv_heads, D, qr, qh, pool.data_ptr(), num_pages, page_size, page_stride,
         page_table.data_ptr(), width, seq_lens_k.data_ptr(), cu_seqlens_q.data_ptr(), B, 1 if causal else 0, max_q_len,

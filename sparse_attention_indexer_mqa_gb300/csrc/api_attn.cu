@@ -9,6 +9,8 @@
 
 namespace {
 
+constexpr int32_t kMaxKeys = INT32_MAX - 65536;
+
 inline bool valid_ftype(int32_t f) { return f == IDX_BF16 || f == IDX_FP16; }
 
 // pool checks of the 8-bit KV cache
@@ -106,10 +108,12 @@ int idx_attn_workspace_bytes(int64_t T, int32_t q_heads, int32_t kv_heads, int32
     if (!bytes || T < 0 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads || B < 0 || max_q_len < 0 ||
         max_seq_len_k < 0 || n_sel < 0)
         return IDX_EINVAL;
-    if ((head_dim != 64 && head_dim != 128) || kv_heads > 1024) return IDX_EUNSUPPORTED;
+    if ((head_dim != 64 && head_dim != 128) || kv_heads > 1024 || max_seq_len_k > kMaxKeys || n_sel > kMaxKeys ||
+        T > INT32_MAX || T * q_heads > INT32_MAX - 256)
+        return IDX_EUNSUPPORTED;
     idx::AttnArgs a{};
     a.T = T; a.q_heads = q_heads; a.kv_heads = kv_heads; a.group = q_heads / kv_heads; a.head_dim = head_dim;
-    a.B = B; a.max_q_len = max_q_len; a.max_seq_len_k = max_seq_len_k; a.n_sel = n_sel;
+    a.B = B; a.max_q_len = (int32_t)(max_q_len < T ? max_q_len : T); a.max_seq_len_k = max_seq_len_k; a.n_sel = n_sel;
     const int64_t n = idx::attn_plan(a, 0);
     if (n < 0) return IDX_ECUDA;
     *bytes = (size_t)n;
@@ -133,17 +137,20 @@ int idx_attn_paged(const void* q, int32_t ftype, int64_t T, int32_t q_heads, int
     if (max_seq_len_k > (int64_t)pt_stride * page_size) return IDX_EINVAL;
     if (sel_idx ? sel_stride < n_sel || !aligned(sel_idx, 4) || n_sel < 1 : n_sel != 0) return IDX_EINVAL;
     if (!aligned(workspace, 256)) return IDX_EINVAL;
-    if (max_seq_len_k > INT32_MAX - 256 || n_sel > INT32_MAX - 256) return IDX_EUNSUPPORTED;
-    // grids: one unit per 16 rows of a sequence, or of a query's group of heads
-    const int64_t group = q_heads / kv_heads;
-    if (T > INT32_MAX || (int64_t)T * q_heads > INT32_MAX ||
-        (__int128)B * (((int64_t)max_q_len * group + 15) / 16) > INT32_MAX)
+    // 32-bit key positions with room for a step behind the end, 32-bit row numbers
+    if (max_seq_len_k > kMaxKeys || n_sel > kMaxKeys || T > INT32_MAX || T * q_heads > INT32_MAX - 256)
         return IDX_EUNSUPPORTED;
+    const int64_t group = q_heads / kv_heads;
+    if (max_q_len > T) max_q_len = (int32_t)T;  // no sequence within cu_seqlens_q[B] <= T has more
+    // grids: one unit per 16 rows of a sequence, or of a query's group of heads
+    if (B * ((max_q_len * group + 15) / 16) > INT32_MAX) return IDX_EUNSUPPORTED;
     if (T == 0 || B == 0 || max_q_len == 0) return IDX_OK;
     if (!row_strides(q, q_row_stride, q_head_stride) || !row_strides(out, out_row_stride, out_head_stride))
         return IDX_EINVAL;
     if ((T > 1 && out_row_stride < head_dim) || (q_heads > 1 && out_head_stride < head_dim)) return IDX_EINVAL;
     if (!seq_lens_k || !cu_seqlens_q || (max_seq_len_k > 0 && !page_table)) return IDX_EINVAL;
+    if (!aligned(seq_lens_k, 4) || !aligned(cu_seqlens_q, 4) || !aligned(page_table, 4) || !aligned(lse, 4))
+        return IDX_EINVAL;
     idx::AttnArgs a{};
     a.q = static_cast<const uint16_t*>(q); a.ftype = ftype; a.T = T; a.q_heads = q_heads; a.kv_heads = kv_heads;
     a.head_dim = head_dim; a.group = (int32_t)group; a.q_row_stride = q_row_stride; a.q_head_stride = q_head_stride;

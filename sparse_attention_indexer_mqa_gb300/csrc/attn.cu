@@ -516,8 +516,21 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const AttnAr
 
 // Rows that share their keys: those of a sequence and a kv head, or with a list those of a query's group.
 int64_t shared_rows(const AttnArgs& a) { return a.n_sel ? a.group : (int64_t)a.max_q_len * a.group; }
-// More rows than one mma.sync tile: the tensor-memory kernel.
-bool use_tile(const AttnArgs& a) { return shared_rows(a) > 16; }
+
+// Which kernel. Dense: up to two mma.sync tiles of shared rows this file's (32 heads over one kv head,
+// 64 x 8192 keys: 60 us against 64; 3000 keys of one sequence: 10.1 against 14.5), more the
+// tensor-memory one (64 heads: 74 against 96). Lists, whose keys are gathered for each tile: up to one (32 heads,
+// 4096 queries x 1024 keys: 434 us in two tiles, 386 in tensor memory).
+struct Choice {
+    bool tile;
+    int64_t units;
+    int per_sm;  // resident CTAs
+};
+Choice choose(const AttnArgs& a) {
+    const int64_t rows = shared_rows(a), times = (a.n_sel ? a.T : (int64_t)a.B) * a.kv_heads;
+    if (rows <= (a.n_sel ? 16 : 32)) return {false, times * ((rows + 15) / 16), 3};
+    return {true, times * ((rows + 127) / 128), 2};
+}
 
 template <int D, bool kHalf, bool kSel>
 cudaError_t launch_rows(const AttnArgs& a, cudaStream_t st) {
@@ -534,9 +547,9 @@ cudaError_t launch_rows(const AttnArgs& a, cudaStream_t st) {
 
 template <int D, bool kHalf>
 cudaError_t launch_d(const AttnArgs& a, cudaStream_t st) {
-    cudaError_t e = use_tile(a) ? launch_attn_tile(a, st)
-                    : a.sel     ? launch_rows<D, kHalf, true>(a, st)
-                                : launch_rows<D, kHalf, false>(a, st);
+    cudaError_t e = choose(a).tile ? launch_attn_tile(a, st)
+                    : a.sel        ? launch_rows<D, kHalf, true>(a, st)
+                                   : launch_rows<D, kHalf, false>(a, st);
     if (e != cudaSuccess || a.n_split <= 1) return e;
     const int64_t rows = a.T * a.q_heads;
     return launch_pdl(attn_join_kernel<D, kHalf>, dim3((unsigned)rows), dim3(kJoinWarps * 32), 0, st, a);
@@ -547,9 +560,8 @@ cudaError_t launch_d(const AttnArgs& a, cudaStream_t st) {
 int64_t attn_plan(AttnArgs& a, int64_t bytes) {
     const int sms = device_sm_count();
     if (sms <= 0) return -1;
-    const bool tile = use_tile(a);
-    const int64_t per_unit = tile ? 128 : 16;
-    const int64_t units = (a.n_sel ? a.T : a.B) * ((shared_rows(a) + per_unit - 1) / per_unit) * a.kv_heads;
+    const Choice choice = choose(a);
+    const int64_t units = choice.units;
     const int64_t keys = a.n_sel ? a.n_sel : a.max_seq_len_k;
     const int64_t per_split = a.T * a.q_heads * (a.head_dim + 2) * 4;
     // Splits. Units that fill the resident CTAs (three or two to an SM) by themselves are cut until there are
@@ -558,7 +570,7 @@ int64_t attn_plan(AttnArgs& a, int64_t bytes) {
     // round, in pieces of 512 keys at least (two sequences of 131071 keys, 4 kv heads: 36 / 32 / 31
     // / 43 us with 32 / 38 / 57 / 64, the last one round and a bit), or of 256 where those are fewer
     // than the SMs (one sequence of 4000 keys: 20.7 / 13.6 / 10.6 / 9.2 us with 2 / 4 / 8 / 16).
-    const int64_t slots = (int64_t)sms * (tile ? 2 : 3);
+    const int64_t slots = (int64_t)sms * choice.per_sm;
     int64_t want = 1;
     if (units > 0) {
         const auto least = [](int64_t x, int64_t y) { return x < y ? x : y; };

@@ -6,8 +6,8 @@
 //     u = s * c + Ev,   p' = 2^(u - m + kShift),   O += p' * v_code,   l += p' * 2^-Ev:
 // V's scale is part of the weight, so both products run on bare codes and nothing has to be
 // scaled element by element. m follows the largest u; it is raised only when a u passes it by more than
-// kLazy, since raising it means rescaling O and l (of 128-key steps with 32 rows in a warp every
-// second one raised some row with 3, one in twenty with 8: 8192-token prefill XXX us). p' <=
+// kLazy, since raising it means rescaling O and l (with 3 some row of a warp's 32 was raised in every
+// second step of 128 keys, by the counter of O's loads in a 4096-token prompt; with 8 in few). p' <=
 // 2^(kShift + kLazy) = 2^15 stays in fp16's range; weights down to 2^-21 of the largest keep fp16's full
 // 11 bits, and below that an absolute 2^-32 of it.
 //     out = O / l,   lse = ln 2 * (m - kShift + log2 l).

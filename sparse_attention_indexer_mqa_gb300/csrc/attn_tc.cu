@@ -18,25 +18,13 @@
 // 8-bit halves each would cost the same tensor time and more conversion. Two CTAs share an SM
 // (tensor memory 2 x 256 columns, shared memory 2 x 103 KB): one's products run under the other's
 // softmax.
-#include "attn.cuh"
-#include "tc.cuh"
+#include "attn_tc.cuh"
 
 namespace idx {
 
 namespace {
 
-constexpr int kRowsT = 128;   // rows of a tile
-constexpr int kKeysT = 128;   // keys of a step
 constexpr int kThreadsT = 256;
-// Pauses between tests of a barrier (ns). None was measurably better or worse from 0 to 200.
-constexpr int kNsIssue = 0, kNsSoft = 0, kNsConv = 20;
-
-// Where 8 consecutive dims (chunk i) of q and k lie in the operand tiles: any order serves, and this one
-// lets 8 lanes that convert one key's consecutive 16-byte pieces write 8 different chunks.
-template <int D>
-__device__ __forceinline__ constexpr int dims_sub(int i) { return D == 128 ? i & 1 : 0; }
-template <int D>
-__device__ __forceinline__ constexpr int dims_chunk(int i) { return D == 128 ? i >> 1 : (i >> 1) + 4 * (i & 1); }
 
 template <int D>
 struct SmemT {
@@ -62,12 +50,6 @@ __device__ __forceinline__ bool conv_all(bool v) {
         : "memory");
     return r != 0;
 }
-// Bounded wait of a whole warp: every lane gets the same answer.
-template <int kNs>
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
-    return __all_sync(kFull, tc::mbar_spin<kNs>(bar, parity));
-}
-
 template <int D, bool kHalf, bool kSel>
 __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs a) {
     using S = SmemT<D>;
@@ -146,42 +128,10 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
         const int64_t tok = kSel ? tok0 : tok0 + row / G;
         const int hq = head * G + (kSel ? row : row % G);
         const int vis = (int)visible_keys(s.len, s.nq, tok - s.t0, a.causal);
-        float rc = 0.0f;
-        {
-            const uint4* q = reinterpret_cast<const uint4*>(a.q + tok * a.q_row_stride + (int64_t)hq * a.q_head_stride);
-            float amax = 0.0f;
-            bool odd = false;
-#pragma unroll 4
-            for (int i = 0; i < D / 8; ++i) {
-                const uint4 w = real ? q[i] : make_uint4(0, 0, 0, 0);
-                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const float2 f = load_pair<kHalf>(u[x]);
-                    odd |= !(fabsf(f.x) < __int_as_float(0x7f800000)) || !(fabsf(f.y) < __int_as_float(0x7f800000));
-                    amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-                }
-            }
-            const int e = odd ? 0 : q_exponent<kHalf>(amax);
-            const float up = pow2f(-e);
-            rc = odd ? __int_as_float(0x7fc00000) : a.scale * kLog2e * pow2f(e);
-#pragma unroll 4
-            for (int i = 0; i < D / 8; ++i) {  // again, from L1
-                const uint4 w = real ? q[i] : make_uint4(0, 0, 0, 0);
-                uint32_t u[4] = {w.x, w.y, w.z, w.w};
-                if constexpr (!kHalf) {
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const float2 f = load_pair<kHalf>(u[x]);
-                        u[x] = half2_bits(f.x * up, f.y * up);
-                    }
-                }
-                *reinterpret_cast<uint4*>(sm + S::kQ + dims_sub<D>(i) * (kRowsT * 128) + tid * 128 +
-                                          ((dims_chunk<D>(i) ^ (tid & 7)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
-            }
-            tc::fence_proxy_async();
-            tc::mbar_arrive(q_full);
-        }
+        const float rc = write_q_row<D, kHalf>(sm + S::kQ, a.q + tok * a.q_row_stride + (int64_t)hq * a.q_head_stride,
+                                               real, tid, a.scale);
+        tc::fence_proxy_async();
+        tc::mbar_arrive(q_full);
         const uint32_t lanes = (uint32_t)(warp * 32) << 16;
         const bool idle = 32 * warp >= rows;  // no row of this warp exists
         float m = neg_inf(), l = 0.0f;
@@ -321,41 +271,22 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
             tc::tmem_st_wait();
             tc::tc_fence_before();
         };
-        // The MMAs of a step, by one thread of warp 0, which has nothing else to do meanwhile.
+        // Warp 0 issues the MMAs: it has nothing else to do meanwhile.
         const uint32_t base = tc::smem_u32(sm);
-        auto issue_s = [&]() {
-            tc::tc_fence_after();
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                const uint32_t at = (k / 4) * (128 * 128) + (k % 4) * 32;
-                tc::mma_f16(tm_s, tc::smem_desc_sw128(base + S::kQ + at), tc::smem_desc_sw128(base + S::kK + at),
-                            tc::idesc_f16(kRowsT, kKeysT), k > 0);
-            }
-            tc::mma_commit(s_full);
-        };
-        auto issue_o = [&](bool accumulate) {
-            tc::tc_fence_after();
-#pragma unroll
-            for (int k = 0; k < kKeysT / 16; ++k)
-                tc::mma_f16_ta(tm_o, tm_s + 8 * k,
-                               tc::smem_desc_sw128(base + S::kV + (k / 4) * (D * 128) + (k % 4) * 32),
-                               tc::idesc_f16(kRowsT, D), accumulate || k > 0);
-            tc::mma_commit(o_done);
-        };
         // Round j: O += P V of step j and S of step j + 1, then the softmax of step j + 1.
         for (int j = -1; j < n && !idle; ++j) {
-            if (tid == 0) {
+            if (warp == 0) {
                 if (j >= 0) {
-                    ok = tc::mbar_spin<kNsIssue>(v_full, j & 1) && tc::mbar_spin<kNsIssue>(p_full, j & 1);
-                    if (ok) issue_o(j > 0);
+                    ok = warp_wait<kNsIssue>(v_full, j & 1) && warp_wait<kNsIssue>(p_full, j & 1);
+                    if (ok) issue_outputs<D>(tm_o, tm_s, base + S::kV, j > 0, o_done);
                 }
                 if (ok && j + 1 < n) {
                     // P of step j lies where the next S goes: its product has to be done
-                    ok = tc::mbar_spin<kNsIssue>(k_full, (j + 1) & 1) && tc::mbar_spin<kNsIssue>(j < 0 ? q_full : o_done, j < 0 ? 0 : j & 1);
-                    if (ok) issue_s();
+                    ok = warp_wait<kNsIssue>(k_full, (j + 1) & 1) &&
+                         warp_wait<kNsIssue>(j < 0 ? q_full : o_done, j < 0 ? 0 : j & 1);
+                    if (ok) issue_scores<D>(tm_s, base + S::kQ, base + S::kK, s_full);
                 }
             }
-            ok = __all_sync(kFull, ok);
             if (!ok || j + 1 >= n) break;
             ok = warp_wait<kNsSoft>(s_full, (j + 1) & 1);
             if (!ok) break;
@@ -374,70 +305,29 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(p_full);
         }
-        if (tid == 0) {  // what was issued has to finish before the tensor memory is given back
-            tc::mma_commit(drain);
-            if (!tc::mbar_spin<kNsIssue>(drain, 0)) ok = false;
+        if (warp == 0) {  // what was issued has to finish before the tensor memory is given back
+            if (tc::elect_one()) tc::mma_commit(drain);
+            __syncwarp();
+            ok = warp_wait<kNsIssue>(drain, 0) && ok;
         }
-        ok = __all_sync(kFull, ok);
         // ---- the row's result -------------------------------------------------------------------------
         if (ok && n > 0 && !idle) ok = warp_wait<kNsSoft>(o_done, (n - 1) & 1);
         if (ok && !idle) {
             tc::tc_fence_after();
-            const float g = a.n_split > 1 ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
-            const int64_t pr = ((int64_t)z * a.T + tok) * a.q_heads + hq;
-            uint16_t* out = a.out + tok * a.out_row_stride + (int64_t)hq * a.out_head_stride;
-            // column 8y + dg of O is dim (D/8) * dg + y: 32 columns are 4 dims of each dg
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-                uint32_t r[32];
-                __syncwarp();
-                if (n > 0) {
-                    tc::tmem_ld32(tm_o + lanes + 32 * c, r);
-                    tc::tmem_ld_wait();
-                }
-                if (!(n > 0 && l != 0.0f)) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) r[i] = 0;
-                }
-#pragma unroll
-                for (int x = 0; x < 8; ++x) {
-                    float v[4];
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) v[y] = __uint_as_float(r[8 * y + x]) * g;
-                    const int dim = D / 8 * x + 4 * c;
-                    if (real && a.n_split > 1) {
-                        if (l != 0.0f)
-                            *reinterpret_cast<float4*>(a.part_o + pr * D + dim) = make_float4(v[0], v[1], v[2], v[3]);
-                    } else if (real) {
-                        *reinterpret_cast<uint2*>(out + dim) = make_uint2(store_pair<kHalf>(v[0], v[1]), store_pair<kHalf>(v[2], v[3]));
-                    }
-                }
-            }
-            if (real) {
-                if (a.n_split > 1)
-                    a.part_ml[pr] = make_float2(m, l);
-                else if (a.lse)
-                    a.lse[tok * a.q_heads + hq] = lse_of(m, l);
-            }
+            store_rows<D, kHalf>(a, tm_o + lanes, n > 0, real, tok, hq, z, m, l);
         }
     } else {
         // ---- converters --------------------------------------------------------------------------------
         const int ct = tid - 128, cw = ct >> 5;
-        constexpr int kPieces = D / 16;          // 16-byte pieces of K per thread
-        constexpr int kVB = D / 8;               // bytes of V per key and thread: 16 or 8
+        using C = ConvShare<D>;
+        const C my(ct);
+        constexpr int kPieces = C::kPieces;
         const int P = a.page_size, lp = P == 128 ? 7 : 6;
         const int64_t hb = kv_head_bytes(P, D);
         const uint8_t* pool = a.pool + (int64_t)head * hb;
         const int32_t* pt = a.page_table + (int64_t)b * a.pt_stride;
         int64_t* offs = reinterpret_cast<int64_t*>(sm + S::kOff);
         const int vis_sel = kSel ? (int)visible_keys(s.len, s.nq, tok0 - s.t0, a.causal) : 0;
-        // 8 lanes take consecutive pieces of a row (a memory request then touches few lines). K: 16-byte piece kp
-        // of keys k_key + i * kKeyStep; V: kVB bytes from dim kVB * dg of keys 8 * kg .. + 7, whose
-        // dim kVB * dg + y goes to row 8 * y + dg of the transposed tile (8 lanes, 8 chunks).
-        const int kp = D == 128 ? lane & 7 : lane & 3;
-        const int k_key = D == 128 ? (lane >> 3) + 4 * cw : (lane >> 3) + (lane & 4) + 8 * cw;
-        constexpr int kKeyStep = D == 128 ? 16 : 32;
-        const int kg = (lane >> 3) + 4 * cw, dg = lane & 7;
         uint4 rk[kPieces], rv[8];
         uint32_t my_scale = 0;  // the key's or block's two scale bytes, bit 16 set; 0: not to be used
         bool bad = false;
@@ -493,7 +383,7 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
         auto load_k = [&](int j) {
 #pragma unroll
             for (int i = 0; i < kPieces; ++i) {
-                const int key = k_key + kKeyStep * i;
+                const int key = my.k_key + C::kKeyStep * i;
                 const uint8_t* half = rows_at[2 * i / kPieces];
                 const uint8_t* src = half + key * 2 * D;
                 bool in = half != nullptr && key < keys;
@@ -503,14 +393,14 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
                     in = at >= 0;
                 }
                 uint4 w = make_uint4(0, 0, 0, 0);
-                if (in) w = reinterpret_cast<const uint4*>(src)[kp];
+                if (in) w = reinterpret_cast<const uint4*>(src)[my.kp];
                 rk[i] = w;
             }
         };
         auto load_v = [&](int j) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const int key = 8 * kg + i;
+                const int key = 8 * my.kg + i;
                 const uint8_t* half = cw >= 2 ? rows_at[1] : rows_at[0];
                 const uint8_t* src = half + key * 2 * D;
                 bool in = half != nullptr && key < keys;
@@ -521,10 +411,10 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
                 }
                 uint4 w = make_uint4(0, 0, 0, 0);
                 if constexpr (D == 128) {
-                    if (in) w = *reinterpret_cast<const uint4*>(src + D + 16 * dg);
+                    if (in) w = *reinterpret_cast<const uint4*>(src + D + 16 * my.dg);
                 } else {
                     uint2 y = make_uint2(0, 0);
-                    if (in) y = *reinterpret_cast<const uint2*>(src + D + 8 * dg);
+                    if (in) y = *reinterpret_cast<const uint2*>(src + D + 8 * my.dg);
                     w.x = y.x;
                     w.y = y.y;
                 }
@@ -564,24 +454,12 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
                                        : make_float4(1.0f, neg_inf(), 0.0f, 1.0f);
 #pragma unroll
             for (int i = 0; i < kPieces; ++i) {
-                const int key = k_key + kKeyStep * i;
-                uint4 lo, hi;
-                e4m3x4_to_f16x4(rk[i].x, lo.x, lo.y);
-                e4m3x4_to_f16x4(rk[i].y, lo.z, lo.w);
-                e4m3x4_to_f16x4(rk[i].z, hi.x, hi.y);
-                e4m3x4_to_f16x4(rk[i].w, hi.z, hi.w);
+                const int key = my.k_key + C::kKeyStep * i;
+                uint32_t f = 0;
                 if constexpr (kSel) {
-                    if (fold) {
-                        const uint32_t f = down(k_top - (int)scale_byte(key_scales[(j & 1) * kKeysT + key])) * 65537u;
-                        lo.x = mul_f16x2(lo.x, f); lo.y = mul_f16x2(lo.y, f);
-                        lo.z = mul_f16x2(lo.z, f); lo.w = mul_f16x2(lo.w, f);
-                        hi.x = mul_f16x2(hi.x, f); hi.y = mul_f16x2(hi.y, f);
-                        hi.z = mul_f16x2(hi.z, f); hi.w = mul_f16x2(hi.w, f);
-                    }
+                    if (fold) f = down(k_top - (int)scale_byte(key_scales[(j & 1) * kKeysT + key])) * 65537u;
                 }
-                uint8_t* row = sm + S::kK + key * 128;
-                *reinterpret_cast<uint4*>(row + dims_sub<D>(0) * (kKeysT * 128) + ((dims_chunk<D>(2 * kp) ^ (key & 7)) << 4)) = lo;
-                *reinterpret_cast<uint4*>(row + dims_sub<D>(1) * (kKeysT * 128) + ((dims_chunk<D>(2 * kp + 1) ^ (key & 7)) << 4)) = hi;
+                write_k_piece<D>(sm + S::kK, rk[i], key, my.kp, f);
             }
             if constexpr (kSel) {
                 if (!fold)
@@ -601,37 +479,12 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
                 if (fold) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const uint2 two = *reinterpret_cast<const uint2*>(key_scales + (j & 1) * kKeysT + 8 * kg + 2 * i);
+                        const uint2 two = *reinterpret_cast<const uint2*>(key_scales + (j & 1) * kKeysT + 8 * my.kg + 2 * i);
                         f[i] = down(v_top - (int)scale_byte(two.x >> 8)) | down(v_top - (int)scale_byte(two.y >> 8)) << 16;
                     }
                 }
             }
-#pragma unroll
-            for (int w = 0; w < kVB / 4; ++w) {
-                uint32_t u[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) u[i] = w == 0 ? rv[i].x : w == 1 ? rv[i].y : w == 2 ? rv[i].z : rv[i].w;
-                uint32_t t[4][4];  // [dim][pair of keys]
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    e4m3x4_to_f16x4(__byte_perm(u[2 * i], u[2 * i + 1], 0x5140), t[0][i], t[1][i]);
-                    e4m3x4_to_f16x4(__byte_perm(u[2 * i], u[2 * i + 1], 0x7362), t[2][i], t[3][i]);
-                }
-                if constexpr (kSel) {
-                    if (fold) {
-#pragma unroll
-                        for (int y = 0; y < 4; ++y)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) t[y][i] = mul_f16x2(t[y][i], f[i]);
-                    }
-                }
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    const int row = 8 * (4 * w + y) + dg;  // of dim kVB * dg + 4 * w + y
-                    *reinterpret_cast<uint4*>(sm + S::kV + (kg >> 3) * (D * 128) + row * 128 + (((kg & 7) ^ dg) << 4)) =
-                        make_uint4(t[y][0], t[y][1], t[y][2], t[y][3]);
-                }
-            }
+            write_v_block<D>(sm + S::kV, rv, my.kg, my.dg, kSel && fold, f);
             tc::fence_proxy_async();
             tc::mbar_arrive(v_full);
         };

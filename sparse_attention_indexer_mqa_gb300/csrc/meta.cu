@@ -91,7 +91,7 @@ __global__ void step_meta_kernel(const MetaArgs a, int rows_per_cta) {
     }
     if (tid == 0) start[a.B] = (int32_t)(total < a.T_cap ? total : a.T_cap);
     at = head + cta_scan(pages, warp_sums, total);
-    int64_t taken = head;  // behind the last entry that a request of this thread got
+    int64_t taken = head;  // where the demand up to this thread's last request that was not refused ends
     for (int b = b0; b < b1; ++b) {
         if (first[b] < 0) continue;
         const int64_t ctx = a.ctx_lens[b], q = a.q_lens[b];
@@ -99,13 +99,13 @@ __global__ void step_meta_kernel(const MetaArgs a, int rows_per_cta) {
         if (need > 0 && at + need > tail) {
             first[b] = -1;
             if (blockIdx.x == 0) report(a.dev_status, IDX_STATUS_NO_PAGE);
-        } else if (need > 0) {
-            first[b] = (int32_t)at;
+        } else {
+            if (need > 0) first[b] = (int32_t)at;
             taken = at + need;
         }
         at += need;
     }
-    // requests are given pages up to the first refusal, so the largest end is the first not taken
+    // the sums grow with the request, so the largest end is the last request's that was not refused
     if (blockIdx.x == 0) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
@@ -117,7 +117,7 @@ __global__ void step_meta_kernel(const MetaArgs a, int rows_per_cta) {
     __syncthreads();
     if (blockIdx.x == 0 && tid == 0) {
         for (int w = 1; w < (nt >> 5); ++w) taken = warp_sums[w] > taken ? warp_sums[w] : taken;
-        *a.free_next = (int32_t)taken;
+        *a.free_next = (int32_t)(taken < INT32_MAX ? taken : INT32_MAX);
         a.cu_seqlens_q[a.B] = start[a.B];
     }
 

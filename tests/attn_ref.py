@@ -107,9 +107,9 @@ def step_meta(ctx, new, table, P, longest, free, span, num_pages, cap):
             if j1 > j0 and at + j1 - j0 > tail:
                 ok = False
                 status |= 0x20
-            elif j1 > j0:
-                table[b][j0:j1] = free[at:at + j1 - j0]
-                nxt = at + j1 - j0
+            else:
+                nxt = at + j1 - j0  # where the demand up to the last request that was not refused ends
+                table[b][j0:j1] = free[at:at + j1 - j0] if j1 > j0 else []
                 if any(not 0 <= p < num_pages for p in table[b][j0:j1]):
                     status |= 0x4
             at += j1 - j0

@@ -478,6 +478,41 @@ def test_bad_pages_and_lengths(torch, Bn, Hq, nq, k):
     assert torch.equal(a.out[:3 * nq], before[:3 * nq]) and (a.out[3 * nq:] == 77).all()
 
 
+@pytest.mark.parametrize("Hq,k", [(8, 0), (64, 0), (8, 9), (64, 9)])
+def test_more_queries_than_the_bound(torch, Bn, Hq, k):
+    """A sequence with more queries than max_q_len is left alone; the others are not."""
+    a = Att(torch, [50, 60, 70], [2, 9, 1], Hq, 1, 64, 64, torch.float16, pad=1)
+    sel = lists(torch, a, 1, k) if k else None
+    Bn.idx_attn_paged(a.q, a.pool, a.pages, 64, a.pool.stride(0), 1, a.table, a.dev_lens, a.dev_cu, 1, 4, 70, a.scale,
+                      a.out, lse=a.lse, sel_idx=sel, dev_status=a.status)
+    assert int(a.status) == 0x10 and (a.out[2:11] == 77).all() and (a.lse[2:11] == 77).all()
+    o, _, otol, _ = ref.attention(a.q, a.pool, 64, 1, a.table, a.lens, a.cu, 1, a.scale, sel)
+    keep = [0, 1, 11]
+    assert ((a.out.double() - o).abs()[keep] <= otol[keep]).all()
+
+
+@pytest.mark.parametrize("Hq,k", [(8, 0), (64, 0), (8, 5), (64, 5)])
+def test_no_keys_at_all(torch, Bn, Hq, k):
+    """Every sequence empty, with a page table of no columns: zeros and -inf, also with splits to spare."""
+    a = Att(torch, [0, 0], [3, 1], Hq, 1, 128, 64, torch.bfloat16, width_extra=0, pad=2)
+    sel = torch.full((a.T, k), 3, dtype=torch.int32, device="cuda") if k else None
+    for ws in (None, torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda")):
+        a.out.fill_(77)
+        a.call(Bn, 1, sel, ws)
+        a.check(1, sel)
+
+
+def test_one_key_among_splits_that_have_none(torch, Bn):
+    """max_seq_len_k far above the lengths: most splits are empty and their parts of the workspace
+    hold what was there before."""
+    for Hq in (8, 64):
+        a = Att(torch, [1, 130], [1, 1], Hq, 1, 128, 64, torch.bfloat16, width_extra=600)
+        ws = torch.full((64 << 20,), 255, dtype=torch.uint8, device="cuda")
+        Bn.idx_attn_paged(a.q, a.pool, a.pages, 64, a.pool.stride(0), 1, a.table, a.dev_lens, a.dev_cu, 1, 1, 38000, a.scale,
+                          a.out, lse=a.lse, workspace=ws, dev_status=a.status)
+        a.check(1)
+
+
 def test_far_pages(torch, Bn):
     """Pages past 2^32 bytes of the pool, dense, selected, and with many rows."""
     stride, P, D = 1 << 28, 64, 128
