@@ -2,47 +2,41 @@
 // large groups of heads) on the tensor cores with tensor-memory accumulators.
 //
 // A unit is a tile of 128 query rows of one kv head (token-major: row = token * group + head of the
-// group; with a list of keys, the group's heads of one token) against a range of keys, 64 at a time:
-// S = Q K^T (M = 128 rows, N = 64 keys), the running softmax of attn.cuh, O += P V (N = D). Tensor memory holds
-// two S (the next step's is computed under this step's softmax) and O, 128 + D columns; P overwrites its
-// S as fp16 and is the second product's A operand from there. Roles of a CTA's three warpgroups:
-//   0  softmax: thread = row, the step's scores in registers. Q to shared memory at the start, O out at the
-//      end;
-//   1  converters: e4m3 from memory to fp16 operand tiles in shared memory (exact), two stages ahead of the
-//      products. The loads go to registers a step before, so any row order costs the same: pages and lists
-//      of keys need no gather pass. V is transposed on the way (8 keys x D/16 dims per thread, bytes paired by
-//      prmt), which makes both products K-major;
-//   2  one warp issues the MMAs.
+// group; with a list of keys, the group's heads of one token) against a range of keys, 128 at a
+// time: S = Q K^T (M = 128 rows, N = 128 keys), the running softmax of attn.cuh, O += P V (N = D). S and
+// O live in tensor memory (128 + D columns), P overwrites S as fp16 and is the second product's A
+// operand from there. Roles of a CTA's two warpgroups:
+//   0  softmax: thread = row. Q to shared memory at the start, S -> P per tile, O out at the end; one
+//      thread of warp 0 issues the MMAs, which its warp would wait for anyway (in a converter warp
+//      each step waited for that warp's other work, and a warp of its own costs every thread a
+//      quarter of its registers);
+//   1  converters: e4m3 from memory to fp16 operand tiles in shared memory (exact). The loads of a
+//      tile go out one tile ahead into registers, so any row order costs the same: pages and
+//      lists of keys need no gather pass. V is transposed on the way (8 keys x 16 dims per
+//      thread, bytes paired by prmt), which makes both products K-major.
 // fp16 runs at half the 8-bit rate, but 8-bit operands would leave q and the weights 4 bits; two
 // 8-bit halves each would cost the same tensor time and more conversion. Two CTAs share an SM
-// (tensor memory 2 x 256 columns, shared memory 2 x 101 KB).
+// (tensor memory 2 x 256 columns, shared memory 2 x 103 KB): one's products run under the other's
+// softmax.
 #include "attn_tc.cuh"
 
 namespace idx {
 
 namespace {
 
-constexpr int kThreadsT = 384;
-// Registers per thread: 80 at launch (two CTAs of 384 threads to an SM); the third warpgroup, of which one
-// warp works, gives to the first two: 112 + 88 + 40 = 3 * 80.
-constexpr int kRegsSoft = 112, kRegsConv = 88, kRegsIssue = 40;
-template <int kRegs>
-__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs)); }
-template <int kRegs>
-__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs)); }
+constexpr int kThreadsT = 256;
 
 template <int D>
 struct SmemT {
-    static constexpr int kTile = kKeysT * D * 2;            // bytes of a K or V tile
     static constexpr int kQ = 0;                            // [D/64][128 rows][128 B]
-    static constexpr int kK = kQ + kRowsT * D * 2;          // two stages
-    static constexpr int kV = kK + 2 * kTile;               // two stages
-    static constexpr int kScale = kV + 2 * kTile;           // [4][64] float4: 2^Ek, Ev, 2^-Ev
-    static constexpr int kOff = kScale + 4 * kKeysT * 16;   // [2][64] int64: a listed key's row in the pool
-    static constexpr int kKey = kOff + 2 * kKeysT * 8;      // [2][64] scale bytes of the listed keys
-    static constexpr int kRange = kKey + 2 * kKeysT * 4;    // [2][2] their ranges, a word per warp
-    static constexpr int kBar = kRange + 16;
-    static constexpr int kBytes = kBar + 128 + 1024;        // 1024: alignment of the operand tiles
+    static constexpr int kK = kQ + kRowsT * D * 2;          // [D/64][128 keys][128 B]
+    static constexpr int kV = kK + kKeysT * D * 2;          // [2][D dims][128 B]
+    static constexpr int kScale = kV + kKeysT * D * 2;      // [2][128] float4: 2^Ek, Ev, 2^-Ev
+    static constexpr int kOff = kScale + 2 * kKeysT * 16;   // [2][128] int64: a listed key's row in the pool
+    static constexpr int kKey = kOff + 2 * kKeysT * 8;      // [2][128] scale bytes of the listed keys
+    static constexpr int kRange = kKey + 2 * kKeysT * 4;    // [2][4] their ranges, a word per warp
+    static constexpr int kBar = kRange + 32;
+    static constexpr int kBytes = kBar + 64 + 1024;         // 1024: alignment of the operand tiles
 };
 
 // Barriers of the four converter warps, one of them with a vote.
@@ -63,10 +57,8 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
     __shared__ uint32_t tmem_slot;
     uint8_t* sm = sm_raw + ((1024u - (tc::smem_u32(sm_raw) & 1023u)) & 1023u);
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + S::kBar);
-    // one of each per parity of the step (and so per stage): who waits for a step may find that the
-    // next one's has come, but not the one's after it
-    uint64_t *k_full = bars, *v_full = bars + 2, *s_full = bars + 4, *p_full = bars + 6, *o_done = bars + 8,
-             *q_full = bars + 10, *drain = bars + 11;
+    uint64_t *q_full = bars, *k_full = bars + 1, *v_full = bars + 2, *s_full = bars + 3, *p_full = bars + 4,
+             *o_done = bars + 5, *drain = bars + 6;
     float4* scales = reinterpret_cast<float4*>(sm + S::kScale);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
@@ -107,19 +99,16 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
     }
     if (tid == 0) {
         tc::mbar_init(q_full, kRowsT);
+        tc::mbar_init(k_full, 128);
+        tc::mbar_init(v_full, 128);
+        tc::mbar_init(s_full, 1);
+        tc::mbar_init(p_full, (rows + 31) / 32);  // a warp without rows takes no part
+        tc::mbar_init(o_done, 1);
         tc::mbar_init(drain, 1);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(k_full + i, 128);
-            tc::mbar_init(v_full + i, 128);
-            tc::mbar_init(s_full + i, 1);
-            tc::mbar_init(p_full + i, (rows + 31) / 32);  // a warp without rows takes no part
-            tc::mbar_init(o_done + i, 1);
-        }
         tc::fence_mbar_init();
     }
     __syncwarp();
-    if (warp == 8) {
+    if (warp == 0) {
         tc::tmem_alloc(&tmem_slot, 256);
         tc::tmem_relinquish();
     }
@@ -134,7 +123,6 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
 
     if (warp < 4) {
         // ---- softmax: this thread's row --------------------------------------------------------------
-        regs_up<kRegsSoft>();
         const bool real = tid < rows;
         const int row = row0 + min(tid, rows - 1);
         const int64_t tok = kSel ? tok0 : tok0 + row / G;
@@ -146,8 +134,7 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
         const uint32_t lanes = (uint32_t)(warp * 32) << 16;
         const bool idle = 32 * warp >= rows;  // no row of this warp exists
         float m = neg_inf(), l = 0.0f;
-        // A row whose largest u passes m by more than kLazy: m raised, O (complete up to the step before) and
-        // l scaled.
+        // A row whose largest u passes m by more than kLazy: m raised, O and l scaled.
         auto raise_to = [&](int j, float mx) {
             float f = 1.0f;
             const bool raise = mx > m + kLazy;
@@ -157,86 +144,103 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
                 l *= f;
             }
             if (j > 0 && __any_sync(kFull, raise)) {
-                ok = warp_wait<kNsSoft>(o_done + ((j - 1) & 1), ((j - 1) >> 1) & 1) && ok;
-                tc::tc_fence_after();
+                // the scores were issued behind the completed O += P V of the step before
 #pragma unroll 1
-                for (int c = 0; c < D / 16; ++c) {
-                    uint32_t r[16];
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t r[2][16];
                     __syncwarp();
-                    tc::tmem_ld16(tm_o + lanes + 16 * c, r);
+                    tc::tmem_ld16(tm_o + lanes + 32 * c, r[0]);
+                    tc::tmem_ld16(tm_o + lanes + 32 * c + 16, r[1]);
                     tc::tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
-                    tc::tmem_st16(tm_o + lanes + 16 * c, r);
+                    for (int i = 0; i < 16; ++i) {
+                        r[0][i] = __float_as_uint(__uint_as_float(r[0][i]) * f);
+                        r[1][i] = __float_as_uint(__uint_as_float(r[1][i]) * f);
+                    }
+                    tc::tmem_st16(tm_o + lanes + 32 * c, r[0]);
+                    tc::tmem_st16(tm_o + lanes + 32 * c + 16, r[1]);
                 }
             }
         };
-        // One step of the running softmax, S to P, with a scale pair per 16 keys; the row's scores stay in
-        // registers. kCut: the rows' visibility tested key by key (tiles that some row of the warp does not
-        // see whole).
+        // One step of the running softmax, S to P, with a scale pair per 16 keys. kCut: the rows' visibility
+        // tested key by key (tiles that some row of the warp does not see whole).
         auto step = [&](int j, auto cut_tag) {
             constexpr bool kCut = decltype(cut_tag)::value;
-            const uint32_t tm = tm_s + kKeysT * (j & 1) + lanes;
-            const float4* sc = scales + (j & 3) * kKeysT;
+            const float4* sc = scales + (j & 1) * kKeysT;
             [[maybe_unused]] const int left = vis - (k0 + j * kKeysT);  // keys of this step that the row sees
-            uint32_t r[2][32];
-            __syncwarp();
-            tc::tmem_ld32(tm, r[0]);
-            tc::tmem_ld32(tm + 32, r[1]);
-            tc::tmem_ld_wait();
             float mx = neg_inf();
+#pragma unroll 1
+            for (int c = 0; c < 4; c += 2) {
+                uint32_t r[2][32];
+                __syncwarp();
+                tc::tmem_ld32(tm_s + lanes + 32 * c, r[0]);
+                tc::tmem_ld32(tm_s + lanes + 32 * c + 32, r[1]);
+                tc::tmem_ld_wait();
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                const uint32_t* x = &r[h >> 1][16 * (h & 1)];
-                const float4 k = sc[h];
-                float bm = neg_inf();
+                for (int h = 0; h < 4; ++h) {
+                    const uint32_t* x = &r[h >> 1][16 * (h & 1)];
+                    const int at = 32 * c + 16 * h;
+                    const float4 k = sc[at / 16];
+                    float bm = neg_inf();
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    bm = fmaxf(bm, !kCut || 16 * h + i < left ? __uint_as_float(x[i]) : neg_inf());
-                // nothing visible: bm is -inf whatever the factor
-                const float u = fmaf(bm, rc * k.x, k.y);
-                mx = fmaxf(mx, kCut && bm == neg_inf() ? bm : u);
+                    for (int i = 0; i < 16; ++i)
+                        bm = fmaxf(bm, !kCut || at + i < left ? __uint_as_float(x[i]) : neg_inf());
+                    // nothing visible: bm is -inf whatever the factor
+                    const float u = fmaf(bm, rc * k.x, k.y);
+                    mx = fmaxf(mx, kCut && bm == neg_inf() ? bm : u);
+                }
             }
             raise_to(j, mx);
             const float top = m == neg_inf() ? 0.0f : kShift - m;
+#pragma unroll 1
+            for (int c = 0; c < 4; c += 2) {
+                uint32_t r[2][32];
+                __syncwarp();
+                tc::tmem_ld32(tm_s + lanes + 32 * c, r[0]);
+                tc::tmem_ld32(tm_s + lanes + 32 * c + 32, r[1]);
+                tc::tmem_ld_wait();
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                uint32_t p2[16];
+                for (int g = 0; g < 2; ++g) {
+                    uint32_t p2[16];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t* x = &r[g][16 * h];
-                    const float4 k = sc[2 * g + h];
-                    const float cc = rc * k.x, sub = k.y + top;
-                    float2 sum = make_float2(0.0f, 0.0f);
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t* x = &r[g][16 * h];
+                        const int at = 32 * (c + g) + 16 * h;
+                        const float4 k = sc[at / 16];
+                        const float cc = rc * k.x, sub = k.y + top;
+                        float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-                    for (int i = 0; i < 16; i += 2) {
-                        float2 u = fma2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), make_float2(cc, cc),
-                                        make_float2(sub, sub));
-                        if constexpr (kCut) {
-                            u.x = 32 * g + 16 * h + i < left ? u.x : neg_inf();
-                            u.y = 32 * g + 16 * h + i + 1 < left ? u.y : neg_inf();
+                        for (int i = 0; i < 16; i += 2) {
+                            float2 u = fma2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])),
+                                            make_float2(cc, cc), make_float2(sub, sub));
+                            if constexpr (kCut) {
+                                u.x = at + i < left ? u.x : neg_inf();
+                                u.y = at + i + 1 < left ? u.y : neg_inf();
+                            }
+                            const float2 p = make_float2(ex2(u.x), ex2(u.y));
+                            sum = add2(sum, p);
+                            p2[8 * h + i / 2] = half2_bits(p.x, p.y);
                         }
-                        const float2 p = make_float2(ex2(u.x), ex2(u.y));
-                        sum = add2(sum, p);
-                        p2[8 * h + i / 2] = half2_bits(p.x, p.y);
+                        l = fmaf(sum.x + sum.y, k.z, l);
                     }
-                    l = fmaf(sum.x + sum.y, k.z, l);
+                    // columns 16(c+g) .. +15 held scores that have been read
+                    tc::tmem_st16(tm_s + lanes + 16 * (c + g), p2);
                 }
-                tc::tmem_st16(tm + 16 * g, p2);
             }
             tc::tmem_st_wait();
             tc::tc_fence_before();
         };
-        // The same with a scale pair per key (lists), Ev = -inf where a key does not count; 16 keys at a time.
+        // The same with a scale pair per key (lists), Ev = -inf where a key does not count. 16 keys at a
+        // time: more registers would spill, and reloads that miss L1 hold up the thread that issues
+        // the MMAs.
         auto step_keyed = [&](int j) {
-            const uint32_t tm = tm_s + kKeysT * (j & 1) + lanes;
-            const float4* sc = scales + (j & 3) * kKeysT;
+            const float4* sc = scales + (j & 1) * kKeysT;
             float mx = neg_inf();
 #pragma unroll 1
-            for (int c = 0; c < kKeysT / 16; ++c) {
+            for (int c = 0; c < 8; ++c) {
                 uint32_t r[16];
                 __syncwarp();
-                tc::tmem_ld16(tm + 16 * c, r);
+                tc::tmem_ld16(tm_s + lanes + 16 * c, r);
                 tc::tmem_ld_wait();
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
@@ -247,10 +251,10 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
             raise_to(j, mx);
             const float top = m == neg_inf() ? 0.0f : kShift - m;
 #pragma unroll 1
-            for (int c = 0; c < kKeysT / 16; ++c) {
+            for (int c = 0; c < 8; ++c) {
                 uint32_t r[16], p2[8];
                 __syncwarp();
-                tc::tmem_ld16(tm + 16 * c, r);
+                tc::tmem_ld16(tm_s + lanes + 16 * c, r);
                 tc::tmem_ld_wait();
 #pragma unroll
                 for (int i = 0; i < 16; i += 2) {
@@ -261,39 +265,58 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
                     l = fmaf(pb, kb.z, l);
                     p2[i / 2] = half2_bits(pa, pb);
                 }
-                tc::tmem_st8(tm + 8 * c, p2);  // columns that have been read
+                tc::tmem_st8(tm_s + lanes + 8 * c, p2);  // columns that have been read
             }
             tc::tmem_st_wait();
             tc::tc_fence_before();
         };
-        for (int j = 0; j < n && !idle; ++j) {
-            ok = warp_wait<kNsSoft>(s_full + (j & 1), (j >> 1) & 1);
+        // Warp 0 issues the MMAs: it has nothing else to do meanwhile.
+        const uint32_t base = tc::smem_u32(sm);
+        // Round j: O += P V of step j and S of step j + 1, then the softmax of step j + 1.
+        for (int j = -1; j < n && !idle; ++j) {
+            if (warp == 0) {
+                if (j >= 0) {
+                    ok = warp_wait<kNsIssue>(v_full, j & 1) && warp_wait<kNsIssue>(p_full, j & 1);
+                    if (ok) issue_outputs<D>(tm_o, tm_s, base + S::kV, j > 0, o_done);
+                }
+                if (ok && j + 1 < n) {
+                    // P of step j lies where the next S goes: its product has to be done
+                    ok = warp_wait<kNsIssue>(k_full, (j + 1) & 1) &&
+                         warp_wait<kNsIssue>(j < 0 ? q_full : o_done, j < 0 ? 0 : j & 1);
+                    if (ok) issue_scores<D>(tm_s, base + S::kQ, base + S::kK, s_full);
+                }
+            }
+            if (!ok || j + 1 >= n) break;
+            ok = warp_wait<kNsSoft>(s_full, (j + 1) & 1);
             if (!ok) break;
             tc::tc_fence_after();
             if constexpr (kSel) {
-                if (scales[(j & 3) * kKeysT].w != 0.0f)
-                    step_keyed(j);
+                if (scales[((j + 1) & 1) * kKeysT].w != 0.0f)
+                    step_keyed(j + 1);
                 else
-                    step(j, std::false_type{});
+                    step(j + 1, std::false_type{});
             } else {
-                if (__any_sync(kFull, k0 + (j + 1) * kKeysT > vis))
-                    step(j, std::true_type{});
+                if (__any_sync(kFull, k0 + (j + 2) * kKeysT > vis))
+                    step(j + 1, std::true_type{});
                 else
-                    step(j, std::false_type{});
+                    step(j + 1, std::false_type{});
             }
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(p_full + (j & 1));
-            if (!ok) break;
+            if (lane == 0) tc::mbar_arrive(p_full);
+        }
+        if (warp == 0) {  // what was issued has to finish before the tensor memory is given back
+            if (tc::elect_one()) tc::mma_commit(drain);
+            __syncwarp();
+            ok = warp_wait<kNsIssue>(drain, 0) && ok;
         }
         // ---- the row's result -------------------------------------------------------------------------
-        if (ok && n > 0 && !idle) ok = warp_wait<kNsSoft>(o_done + ((n - 1) & 1), ((n - 1) >> 1) & 1);
+        if (ok && n > 0 && !idle) ok = warp_wait<kNsSoft>(o_done, (n - 1) & 1);
         if (ok && !idle) {
             tc::tc_fence_after();
             store_rows<D, kHalf>(a, tm_o + lanes, n > 0, real, tok, hq, z, m, l);
         }
-    } else if (warp < 8) {
+    } else {
         // ---- converters --------------------------------------------------------------------------------
-        regs_up<kRegsConv>();
         const int ct = tid - 128, cw = ct >> 5;
         using C = ConvShare<D>;
         const C my(ct);
@@ -304,60 +327,65 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
         const int32_t* pt = a.page_table + (int64_t)b * a.pt_stride;
         int64_t* offs = reinterpret_cast<int64_t*>(sm + S::kOff);
         const int vis_sel = kSel ? (int)visible_keys(s.len, s.nq, tok0 - s.t0, a.causal) : 0;
-        uint4 rk[kPieces];
-        uint2 rv[8];
+        uint4 rk[kPieces], rv[8];
         uint32_t my_scale = 0;  // the key's or block's two scale bytes, bit 16 set; 0: not to be used
         bool bad = false;
 
-        // Lookups run ahead: a step's page is loaded one step before its rows, and with a list (thread ct
-        // looks after entry ct of a step) its entry two steps before.
-        int32_t ent = -1, ent_n = -1, page = -1;
-        const uint8_t* rows_at = nullptr;  // key 0 of the step
-        int keys = 0;                      // of the step
+        // Lookups run ahead: a step's pages are loaded one step before its rows, and with a list (thread
+        // ct looks after entry ct of a step) its entries two steps before.
+        int32_t ent = -1, ent_n = -1;
+        int32_t page[2] = {-1, -1};                     // the second: keys 64 .. of the step
+        const uint8_t* rows_at[2] = {nullptr, nullptr};  // key 0 of the step, seen from either half
+        int keys = 0;                                    // of the step
         auto load_entry = [&](int j) -> int32_t {
             const int e = k0 + j * kKeysT + ct;
-            return ct < kKeysT && e < k1 ? a.sel[tok0 * a.sel_stride + e] : -1;
+            return e < k1 ? a.sel[tok0 * a.sel_stride + e] : -1;
         };
         auto lookup = [&](int j) {
             if constexpr (kSel) {
-                page = (ent >= 0 && ent < vis_sel) ? pt[ent >> lp] : -1;
+                page[0] = (ent >= 0 && ent < vis_sel) ? pt[ent >> lp] : -1;
             } else {
                 const int kt = k0 + j * kKeysT;
-                page = kt < k1 ? pt[kt >> lp] : -1;
+                page[0] = kt < k1 ? pt[kt >> lp] : -1;
+                page[1] = kt + 64 < k1 ? pt[(kt + 64) >> lp] : -1;
             }
         };
         auto place = [&](int j) {
-            const bool in = (uint32_t)page < (uint64_t)a.num_pages;
             my_scale = 0;
             if constexpr (kSel) {
-                const bool seen = ent >= 0 && ent < vis_sel;
+                const bool seen = ent >= 0 && ent < vis_sel, in = (uint32_t)page[0] < (uint64_t)a.num_pages;
                 int64_t at = -1;
                 bad |= seen && !in;
                 if (seen && in) {
                     const int tok = ent & (P - 1);
-                    at = (int64_t)page * a.page_stride;
+                    at = (int64_t)page[0] * a.page_stride;
                     my_scale = *reinterpret_cast<const uint16_t*>(pool + at + 2ll * P * D + 2 * (tok / kKvBlock)) | 65536u;
                     at += (int64_t)tok * 2 * D;
                 }
                 // the places of step j - 2 have been read: conv_all() came since
-                if (ct < kKeysT) offs[(j & 1) * kKeysT + ct] = at;
+                offs[(j & 1) * kKeysT + ct] = at;
                 conv_sync();
             } else {
-                const int kt = k0 + j * kKeysT, tok = kt & (P - 1);
-                keys = k1 - kt;
-                bad |= !in;
-                const uint8_t* at = pool + (int64_t)page * a.page_stride;
-                if (in && (ct & 15) == 0 && ct < kKeysT && ct < keys)  // this thread's block of 16 keys
-                    my_scale = *reinterpret_cast<const uint16_t*>(at + 2ll * P * D + 2 * ((tok + ct) / kKvBlock)) | 65536u;
-                rows_at = in ? at + tok * 2 * D : nullptr;
+                keys = k1 - (k0 + j * kKeysT);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const bool in = (uint32_t)page[h] < (uint64_t)a.num_pages;
+                    bad |= !in && 64 * h < keys;
+                    const uint8_t* at = pool + (int64_t)page[h] * a.page_stride;
+                    // this thread's block of 16 keys
+                    if (in && (ct & 15) == 0 && ct / 64 == h && ct < keys)
+                        my_scale = *reinterpret_cast<const uint16_t*>(at + 2ll * P * D + 2 * ((ct & (P - 1)) / kKvBlock)) | 65536u;
+                    rows_at[h] = in ? at - (h && P == 64 ? 64 * 2 * D : 0) : nullptr;
+                }
             }
         };
         auto load_k = [&](int j) {
 #pragma unroll
             for (int i = 0; i < kPieces; ++i) {
                 const int key = my.k_key + C::kKeyStep * i;
-                const uint8_t* src = rows_at + key * 2 * D;
-                bool in = rows_at != nullptr && key < keys;
+                const uint8_t* half = rows_at[2 * i / kPieces];
+                const uint8_t* src = half + key * 2 * D;
+                bool in = half != nullptr && key < keys;
                 if constexpr (kSel) {
                     const int64_t at = offs[(j & 1) * kKeysT + key];
                     src = pool + at;
@@ -372,18 +400,22 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int key = 8 * my.kg + i;
-                const uint8_t* src = rows_at + key * 2 * D;
-                bool in = rows_at != nullptr && key < keys;
+                const uint8_t* half = cw >= 2 ? rows_at[1] : rows_at[0];
+                const uint8_t* src = half + key * 2 * D;
+                bool in = half != nullptr && key < keys;
                 if constexpr (kSel) {
                     const int64_t at = offs[(j & 1) * kKeysT + key];
                     src = pool + at;
                     in = at >= 0;
                 }
-                uint2 w = make_uint2(0, 0);
+                uint4 w = make_uint4(0, 0, 0, 0);
                 if constexpr (D == 128) {
-                    if (in) w = *reinterpret_cast<const uint2*>(src + D + 8 * my.dg);
+                    if (in) w = *reinterpret_cast<const uint4*>(src + D + 16 * my.dg);
                 } else {
-                    if (in) w.x = *reinterpret_cast<const uint32_t*>(src + D + 4 * my.dg);
+                    uint2 y = make_uint2(0, 0);
+                    if (in) y = *reinterpret_cast<const uint2*>(src + D + 8 * my.dg);
+                    w.x = y.x;
+                    w.y = y.y;
                 }
                 rv[i] = w;
             }
@@ -400,12 +432,13 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
             const bool in = my_scale != 0;
             const uint32_t k_hi = __reduce_max_sync(kFull, in ? ek : 255u), k_lo = __reduce_min_sync(kFull, in ? ek : 0u);
             const uint32_t v_hi = __reduce_max_sync(kFull, in ? ev : 255u), v_lo = __reduce_min_sync(kFull, in ? ev : 0u);
-            if (ct < kKeysT) key_scales[(j & 1) * kKeysT + ct] = my_scale;
-            if (lane == 0 && cw < 2) ranges[(j & 1) * 2 + cw] = k_hi | k_lo << 8 | v_hi << 16 | v_lo << 24;
+            key_scales[(j & 1) * kKeysT + ct] = my_scale;
+            if (lane == 0) ranges[(j & 1) * 4 + cw] = k_hi | k_lo << 8 | v_hi << 16 | v_lo << 24;
         };
         auto collect = [&](int j) {  // behind it
-            const uint2 r = *reinterpret_cast<const uint2*>(ranges + (j & 1) * 2);
-            const uint32_t hi = __vmaxu4(r.x, r.y), lo = __vminu4(r.x, r.y);
+            const uint4 r = *reinterpret_cast<const uint4*>(ranges + (j & 1) * 4);
+            const uint32_t hi = __vmaxu4(__vmaxu4(r.x, r.y), __vmaxu4(r.z, r.w));
+            const uint32_t lo = __vminu4(__vminu4(r.x, r.y), __vminu4(r.z, r.w));
             k_top = hi & 255;
             v_top = hi >> 16 & 255;
             // a key that does not count makes the range too wide
@@ -425,21 +458,18 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
                 if constexpr (kSel) {
                     if (fold) f = down(k_top - (int)scale_byte(key_scales[(j & 1) * kKeysT + key])) * 65537u;
                 }
-                write_k_piece<D>(sm + S::kK + (j & 1) * S::kTile, rk[i], key, my.kp, f);
+                write_k_piece<D>(sm + S::kK, rk[i], key, my.kp, f);
             }
-            // four buffers of scales: a softmax may still read those of the stage's last step
-            float4* to = scales + (j & 3) * kKeysT;
             if constexpr (kSel) {
-                if (!fold) {
-                    if (ct < kKeysT) to[ct] = sc;
-                } else if (ct < 4) {
-                    to[ct] = make_float4(__uint_as_float((uint32_t)k_top << 23), (float)(v_top - 127),
-                                         ex2((float)(127 - v_top)), 0.0f);
-                }
-            } else if ((ct & 15) == 0 && ct < kKeysT) {
-                to[ct / 16] = sc;
+                if (!fold)
+                    scales[(j & 1) * kKeysT + ct] = sc;
+                else if (ct < 8)
+                    scales[(j & 1) * kKeysT + ct] = make_float4(__uint_as_float((uint32_t)k_top << 23), (float)(v_top - 127),
+                                                                ex2((float)(127 - v_top)), 0.0f);
+            } else if ((ct & 15) == 0) {
+                scales[(j & 1) * kKeysT + ct / 16] = sc;
             }
-            tc::mbar_arrive(k_full + (j & 1));
+            tc::mbar_arrive(k_full);
         };
         auto write_v = [&](int j) {
             uint32_t f[4] = {0, 0, 0, 0};  // factors of pairs of keys
@@ -452,8 +482,8 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
                     }
                 }
             }
-            write_v_block<D>(sm + S::kV + (j & 1) * S::kTile, rv, my.kg, my.dg, kSel && fold, f);
-            tc::mbar_arrive(v_full + (j & 1));
+            write_v_block<D>(sm + S::kV, rv, my.kg, my.dg, kSel && fold, f);
+            tc::mbar_arrive(v_full);
         };
 
         if (n > 0) {
@@ -462,80 +492,38 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
                 ent_n = load_entry(1);
             }
             lookup(0);
-            place(0);
-            load_k(0);
-            load_v(0);
-            if constexpr (kSel) {
-                ent = ent_n;
-                ent_n = load_entry(2);
-            }
-            lookup(1);
+            // Round j: K of step j + 1 to shared memory (where step j's product has read), loads of step
+            // j + 2's K; V of step j + 1 (where O += P V has read), loads of step j + 2's V.
 #pragma unroll 1
-            for (int j = 0; j < n; ++j) {
-                // a stage's K is free when step j - 2's product has read it, its V when O += P V has
-                if (j >= 2) ok = warp_wait<kNsConv>(s_full + (j & 1), ((j - 2) >> 1) & 1) && ok;
+            for (int j = -2; j + 1 < n; ++j) {
+                if (j >= 0) ok = warp_wait<kNsConv>(s_full, j & 1) && ok;
                 if constexpr (kSel) {
-                    publish(j);
+                    if (j >= -1) publish(j + 1);
                     ok = conv_all(ok);  // leave together: place() has a barrier
-                    collect(j);
+                    if (j >= -1) collect(j + 1);
                 }
                 if (!ok) break;
-                write_k(j);
-                if (j + 1 < n) {
-                    place(j + 1);
-                    load_k(j + 1);
-                }
-                if (j >= 2) ok = warp_wait<kNsConv>(o_done + (j & 1), ((j - 2) >> 1) & 1) && ok;
-                write_v(j);
-                if (j + 1 < n) {
-                    load_v(j + 1);
+                if (j >= -1) write_k(j + 1);
+                if (j + 2 < n) {
+                    place(j + 2);
+                    load_k(j + 2);
                     if constexpr (kSel) {
                         ent = ent_n;
-                        ent_n = load_entry(j + 3);
+                        ent_n = load_entry(j + 4);
                     }
-                    lookup(j + 2);
+                    lookup(j + 3);
                 }
+                if (j >= 0) ok = warp_wait<kNsConv>(o_done, j & 1) && ok;
+                if (j >= -1) write_v(j + 1);
+                if (j + 2 < n) load_v(j + 2);
             }
         }
         if (bad) report(a.dev_status, IDX_STATUS_BAD_PAGE);
-    } else {
-        // ---- MMA: S of step j, then O += P V of step j - 1 ----------------------------------------------------
-        regs_down<kRegsIssue>();
-        if (warp == 8 && n > 0) {
-            const uint32_t base = tc::smem_u32(sm);
-            ok = warp_wait<kNsIssue>(q_full, 0);
-            for (int j = 0; j <= n && ok; ++j) {
-                const int st = j & 1;
-                if (j < n) {
-                    // P of step j - 2 lies where this S goes: its product has to be done
-                    ok = warp_wait<kNsIssue>(k_full + st, (j >> 1) & 1) &&
-                         (j < 2 || warp_wait<kNsIssue>(o_done + st, ((j - 2) >> 1) & 1));
-                    if (!ok) break;
-                    // The tiles were written with ordinary stores: the proxy fence between those and the MMAs' reads is
-                    // here, behind the barrier, because in the converters it would wait for the loads they have in
-                    // flight.
-                    tc::fence_proxy_async();
-                    issue_scores<D>(tm_s + kKeysT * st, base + S::kQ, base + S::kK + st * S::kTile, s_full + st);
-                }
-                if (j > 0) {
-                    const int pv = st ^ 1;
-                    ok = warp_wait<kNsIssue>(v_full + pv, ((j - 1) >> 1) & 1) &&
-                         warp_wait<kNsIssue>(p_full + pv, ((j - 1) >> 1) & 1);
-                    if (!ok) break;
-                    tc::fence_proxy_async();
-                    issue_outputs<D>(tm_o, tm_s + kKeysT * pv, base + S::kV + pv * S::kTile, j > 1, o_done + pv);
-                }
-            }
-            // what was issued has to finish before the tensor memory is given back
-            if (tc::elect_one()) tc::mma_commit(drain);
-            __syncwarp();
-            ok = warp_wait<kNsIssue>(drain, 0) && ok;
-        }
     }
     if (!ok) report(a.dev_status, IDX_STATUS_TIMEOUT);
     tc::tc_fence_before();
     __syncthreads();
-    if (warp == 8) tc::tmem_dealloc(tm_s, 256);
+    if (warp == 0) tc::tmem_dealloc(tm_s, 256);
 }
 
 template <int D, bool kHalf, bool kSel>

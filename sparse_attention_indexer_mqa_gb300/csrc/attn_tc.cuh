@@ -1,7 +1,7 @@
 // attn_tc.cuh -- the parts of the tensor-memory attention kernel (attn_tc.cu): operand tiles, MMA issue, the
-// rows' way in and out. A tile is 128 query rows by 64 keys. Operands are fp16, K-major with the
-// 128-byte swizzle: Q [D/64][128 rows][128 B], K [D/64][64 keys][128 B], V transposed
-// [D dims][128 B] (the 64 keys of a dim in a row).
+// rows' way in and out. A tile is 128 query rows by 128 keys. Operands are fp16, K-major with the
+// 128-byte swizzle: Q [D/64][128 rows][128 B], K [D/64][128 keys][128 B], V transposed
+// [2][D dims][128 B] (64 keys to a row).
 #pragma once
 
 #include "attn.cuh"
@@ -10,7 +10,7 @@
 namespace idx {
 
 constexpr int kRowsT = 128;   // rows of a tile
-constexpr int kKeysT = 64;    // keys of a step
+constexpr int kKeysT = 128;   // keys of a step
 
 // Pauses between tests of a barrier (ns). None was measurably better or worse from 0 to 200.
 constexpr int kNsIssue = 0, kNsSoft = 0, kNsConv = 20;
@@ -28,20 +28,20 @@ __device__ __forceinline__ constexpr int dims_sub(int i) { return D == 128 ? i &
 template <int D>
 __device__ __forceinline__ constexpr int dims_chunk(int i) { return D == 128 ? i >> 1 : (i >> 1) + 4 * (i & 1); }
 
-// A converter thread ct's share (of 128): lanes take consecutive pieces of a row, so that a memory
+// A converter thread ct's share (of 128): 8 lanes take consecutive pieces of a row, so that a memory
 // request touches few lines. K: 16-byte piece kp of keys k_key + i * kKeyStep. V: kVB bytes from dim
-// kVB * dg of keys 8 * kg .. + 7; dim kVB * dg + y goes to row 16 * y + dg of the transposed tile (8
+// kVB * dg of keys 8 * kg .. + 7; dim kVB * dg + y goes to row 8 * y + dg of the transposed tile (8
 // lanes, 8 chunks).
 template <int D>
 struct ConvShare {
-    static constexpr int kPieces = D / 32, kVB = D / 16, kKeyStep = D == 128 ? 16 : 32;
+    static constexpr int kPieces = D / 16, kVB = D / 8, kKeyStep = D == 128 ? 16 : 32;
     int kp, k_key, kg, dg;
     __device__ __forceinline__ explicit ConvShare(int ct) {
         const int lane = ct & 31, cw = ct >> 5;
         kp = D == 128 ? lane & 7 : lane & 3;
         k_key = D == 128 ? (lane >> 3) + 4 * cw : (lane >> 3) + (lane & 4) + 8 * cw;
-        kg = (lane >> 4) + 2 * cw;
-        dg = lane & 15;
+        kg = (lane >> 3) + 4 * cw;
+        dg = lane & 7;
     }
 };
 
@@ -67,16 +67,18 @@ __device__ __forceinline__ void write_k_piece(uint8_t* tile, const uint4& raw, i
 // A block of V (kVB dims of 8 keys) as fp16, transposed, into the V tile; fold: keys 2i, 2i + 1 times the
 // pair f[i].
 template <int D>
-__device__ __forceinline__ void write_v_block(uint8_t* tile, const uint2 (&rv)[8], int kg, int dg, bool fold,
+__device__ __forceinline__ void write_v_block(uint8_t* tile, const uint4 (&rv)[8], int kg, int dg, bool fold,
                                               const uint32_t (&f)[4]) {
 #pragma unroll
-    for (int w = 0; w < D / 64; ++w) {
+    for (int w = 0; w < D / 32; ++w) {
+        uint32_t u[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] = w == 0 ? rv[i].x : w == 1 ? rv[i].y : w == 2 ? rv[i].z : rv[i].w;
         uint32_t t[4][4];  // [dim][pair of keys]
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const uint32_t a = w ? rv[2 * i].y : rv[2 * i].x, b = w ? rv[2 * i + 1].y : rv[2 * i + 1].x;
-            e4m3x4_to_f16x4(__byte_perm(a, b, 0x5140), t[0][i], t[1][i]);
-            e4m3x4_to_f16x4(__byte_perm(a, b, 0x7362), t[2][i], t[3][i]);
+            e4m3x4_to_f16x4(__byte_perm(u[2 * i], u[2 * i + 1], 0x5140), t[0][i], t[1][i]);
+            e4m3x4_to_f16x4(__byte_perm(u[2 * i], u[2 * i + 1], 0x7362), t[2][i], t[3][i]);
         }
         if (fold) {
 #pragma unroll
@@ -86,8 +88,8 @@ __device__ __forceinline__ void write_v_block(uint8_t* tile, const uint2 (&rv)[8
         }
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
-            const int row = 16 * (4 * w + y) + dg;  // of dim kVB * dg + 4 * w + y
-            *reinterpret_cast<uint4*>(tile + row * 128 + ((kg ^ (dg & 7)) << 4)) =
+            const int row = 8 * (4 * w + y) + dg;  // of dim kVB * dg + 4 * w + y
+            *reinterpret_cast<uint4*>(tile + (kg >> 3) * (D * 128) + row * 128 + (((kg & 7) ^ dg) << 4)) =
                 make_uint4(t[y][0], t[y][1], t[y][2], t[y][3]);
         }
     }
@@ -131,18 +133,19 @@ __device__ __forceinline__ float write_q_row(uint8_t* tile, const uint16_t* src,
 }
 
 // S = Q K^T and O (+)= P V of a step, by one lane of the (converged) warp that calls. P lies in the
-// first half of S's columns, as fp16.
+// first half of S's columns, as fp16. The operand tiles were written with ordinary stores: the proxy fence
+// between those and the MMAs' reads is here, behind the barrier that says they are written, because in the
+// converters it would wait for the loads they have in flight.
 template <int D>
 __device__ __forceinline__ void issue_scores(uint32_t tm_s, uint32_t q_tile, uint32_t k_tile, uint64_t* done) {
     tc::tc_fence_after();
+    tc::fence_proxy_async();
     const uint64_t qd = tc::smem_desc_sw128(q_tile), kd = tc::smem_desc_sw128(k_tile);
     if (tc::elect_one()) {
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-            // in the descriptor's 16-byte units
-            const uint32_t q_at = ((k / 4) * (kRowsT * 128) + (k % 4) * 32) >> 4;
-            const uint32_t k_at = ((k / 4) * (kKeysT * 128) + (k % 4) * 32) >> 4;
-            tc::mma_f16(tm_s, qd + q_at, kd + k_at, tc::idesc_f16(kRowsT, kKeysT), k > 0);
+            const uint32_t at = ((k / 4) * (128 * 128) + (k % 4) * 32) >> 4;  // in the descriptor's 16-byte units
+            tc::mma_f16(tm_s, qd + at, kd + at, tc::idesc_f16(kRowsT, kKeysT), k > 0);
         }
         tc::mma_commit(done);
     }
@@ -152,11 +155,12 @@ template <int D>
 __device__ __forceinline__ void issue_outputs(uint32_t tm_o, uint32_t tm_p, uint32_t v_tile, bool accumulate,
                                               uint64_t* done) {
     tc::tc_fence_after();
+    tc::fence_proxy_async();
     const uint64_t vd = tc::smem_desc_sw128(v_tile);
     if (tc::elect_one()) {
 #pragma unroll
         for (int k = 0; k < kKeysT / 16; ++k)
-            tc::mma_f16_ta(tm_o, tm_p + 8 * k, vd + ((k * 32) >> 4),
+            tc::mma_f16_ta(tm_o, tm_p + 8 * k, vd + (((k / 4) * (D * 128) + (k % 4) * 32) >> 4),
                            tc::idesc_f16(kRowsT, D), accumulate || k > 0);
         tc::mma_commit(done);
     }
@@ -164,7 +168,7 @@ __device__ __forceinline__ void issue_outputs(uint32_t tm_o, uint32_t tm_p, uint
 }
 
 // A warp's rows out of tensor memory (tm_o: the warp's lanes): the result, or the split's part of it. some: O was
-// written at all. Column 16y + x of O is dim (D/16) * x + y, so 32 columns are 2 dims of each x.
+// written at all. Column 8y + x of O is dim (D/8) * x + y, so 32 columns are 4 dims of each x.
 template <int D, bool kHalf>
 __device__ __forceinline__ void store_rows(const AttnArgs& a, uint32_t tm_o, bool some, bool real, int64_t tok, int hq,
                                            int z, float m, float l) {
@@ -172,27 +176,27 @@ __device__ __forceinline__ void store_rows(const AttnArgs& a, uint32_t tm_o, boo
     const int64_t pr = ((int64_t)z * a.T + tok) * a.q_heads + hq;
     uint16_t* out = a.out + tok * a.out_row_stride + (int64_t)hq * a.out_head_stride;
 #pragma unroll 1
-    for (int c = 0; c < D / 64; ++c) {
-        uint32_t r[2][32];  // dims 4c .. 4c + 3 of each x
+    for (int c = 0; c < D / 32; ++c) {
+        uint32_t r[32];
         __syncwarp();
         if (some) {
-            tc::tmem_ld32(tm_o + 64 * c, r[0]);
-            tc::tmem_ld32(tm_o + 64 * c + 32, r[1]);
+            tc::tmem_ld32(tm_o + 32 * c, r);
             tc::tmem_ld_wait();
         }
         if (!(some && l != 0.0f)) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) r[0][i] = r[1][i] = 0;
+            for (int i = 0; i < 32; ++i) r[i] = 0;
         }
 #pragma unroll
-        for (int x = 0; x < 16; ++x) {
-            const float v0 = __uint_as_float(r[0][x]) * g, v1 = __uint_as_float(r[0][16 + x]) * g;
-            const float v2 = __uint_as_float(r[1][x]) * g, v3 = __uint_as_float(r[1][16 + x]) * g;
-            const int dim = D / 16 * x + 4 * c;
+        for (int x = 0; x < 8; ++x) {
+            float v[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) v[y] = __uint_as_float(r[8 * y + x]) * g;
+            const int dim = D / 8 * x + 4 * c;
             if (real && a.n_split > 1) {
-                if (l != 0.0f) *reinterpret_cast<float4*>(a.part_o + pr * D + dim) = make_float4(v0, v1, v2, v3);
+                if (l != 0.0f) *reinterpret_cast<float4*>(a.part_o + pr * D + dim) = make_float4(v[0], v[1], v[2], v[3]);
             } else if (real) {
-                *reinterpret_cast<uint2*>(out + dim) = make_uint2(store_pair<kHalf>(v0, v1), store_pair<kHalf>(v2, v3));
+                *reinterpret_cast<uint2*>(out + dim) = make_uint2(store_pair<kHalf>(v[0], v[1]), store_pair<kHalf>(v[2], v[3]));
             }
         }
     }
