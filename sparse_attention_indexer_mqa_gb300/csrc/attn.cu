@@ -13,6 +13,11 @@
 //   O = P V: S's accumulator is P's A operand as it stands: rows r, r + 8, keys 2c, 2c+1, 8+2c,
 //     9+2c. The thread holds those four keys' dims r*D/8 .. and pairs their bytes by prmt;
 //     column n of step j is dim n*D/8 + j, so a thread ends with D/4 consecutive dims of a row.
+// Measured (bf16): 64 sequences of 8192 keys, 64 heads over 8, D = 128: 190 us, 5.7 TB/s of cache, 84 % of
+// the measured copy rate (236 us with lanes' pieces of 16 bytes scattered over lines); two of 131071
+// keys, 32 heads over 4, D = 64: 32 us with the join, 4.2 TB/s. Eleven warps on an SM, each a chain of
+// loads, 64 mma.sync, two shuffles, exponentials and 64 mma.sync a step, do not hide all of it: DRAM
+// 62 %, issue 39 % busy.
 #include "attn.cuh"
 
 namespace idx {

@@ -6,18 +6,29 @@
 // time: S = Q K^T (M = 128 rows, N = 128 keys), the running softmax of attn.cuh, O += P V (N = D). S and
 // O live in tensor memory (128 + D columns), P overwrites S as fp16 and is the second product's A
 // operand from there. Roles of a CTA's two warpgroups:
-//   0  softmax: thread = row. Q to shared memory at the start, S -> P per tile, O out at the end; one
-//      thread of warp 0 issues the MMAs, which its warp would wait for anyway (in a converter warp
-//      each step waited for that warp's other work, and a warp of its own costs every thread a
-//      quarter of its registers);
+//   0  softmax: thread = row. Q to shared memory at the start, S -> P per tile, O out at the end; warp
+//      0 issues the MMAs, which it would wait for anyway (in a converter warp each step waited for that
+//      warp's other work, 674 us for a causal prompt of 8192 tokens, 32 heads over 8, against 630; in a
+//      warp of its own every thread had a quarter fewer registers and spilled, 898 us);
 //   1  converters: e4m3 from memory to fp16 operand tiles in shared memory (exact). The loads of a
 //      tile go out one tile ahead into registers, so any row order costs the same: pages and
 //      lists of keys need no gather pass. V is transposed on the way (8 keys x 16 dims per
 //      thread, bytes paired by prmt), which makes both products K-major.
 // fp16 runs at half the 8-bit rate, but 8-bit operands would leave q and the weights 4 bits; two
 // 8-bit halves each would cost the same tensor time and more conversion. Two CTAs share an SM
-// (tensor memory 2 x 256 columns, shared memory 2 x 103 KB): one's products run under the other's
+// (tensor memory 2 x 256 columns, shared memory 2 x 107 KB): one's products run under the other's
 // softmax.
+//
+// What bounds it. That prompt takes 626 us, 878 TFLOP/s of its visible pairs (45 % of a large bf16 product's measured
+// rate). Eight MMAs of 128 x 128 x 16 take 736 cycles (both operands in shared memory) or 679
+// (P in tensor memory) with nothing else on the SM, so a step needs 1415 cycles of the tensor pipe;
+// a CTA's step takes 4400: S 740, softmax 1950, O += P V 700, and 200 to 500 from each to
+// the next. Measured and no faster: 64-key steps with two S (S of the next step under this step's softmax;
+// an N = 64 MMA takes as long as an N = 128 one: 600 us, and 548 instead of 443 us with lists),
+// with K's and V's converters apart (645, 518); two tiles to a CTA that share converted K and V (698, and
+// 685 with the tiles' MMAs in turn); the softmax in one pass over S with P kept in registers
+// (665). With lists (4096 queries x 1024 keys, 64 heads over 1: 443 us) half of a tile's rows are
+// empty and a unit is only eight steps long; the order of the keys hardly matters (441 in order).
 #include "attn_tc.cuh"
 
 namespace idx {

@@ -9,6 +9,8 @@
 // request by binary search in the sums, which stay in shared memory (8 bytes a request).
 // Reads and writes of the page table never meet: a row reads entries below ceil(ctx/P) or
 // the free list, and only entries from ceil(ctx/P) on are written.
+// Measured: 64 requests of one token 5.6 us, 512 requests with 66173 rows 7.8 us (0.8 MB): launch,
+// two sums with four barriers, and per row a binary search and two dependent loads.
 #include <algorithm>
 #include <mutex>
 #include <thread>
