@@ -135,7 +135,7 @@ int idx_attn_paged(const void* q, int32_t ftype, int64_t T, int32_t q_heads, int
     if (q_heads < 1 || q_heads % kv_heads != 0) return IDX_EINVAL;
     if (!(softmax_scale > 0.0f) || !std::isfinite(softmax_scale)) return IDX_EINVAL;
     if (max_seq_len_k > (int64_t)pt_stride * page_size) return IDX_EINVAL;
-    if (sel_idx ? sel_stride < n_sel || !aligned(sel_idx, 4) || n_sel < 1 : n_sel != 0) return IDX_EINVAL;
+    if (T > 0 && (sel_idx ? sel_stride < n_sel || !aligned(sel_idx, 4) || n_sel < 1 : n_sel != 0)) return IDX_EINVAL;
     if (!aligned(workspace, 256)) return IDX_EINVAL;
     // 32-bit key positions with room for a step behind the end, 32-bit row numbers
     if (max_seq_len_k > kMaxKeys || n_sel > kMaxKeys || T > INT32_MAX || T * q_heads > INT32_MAX - 256)

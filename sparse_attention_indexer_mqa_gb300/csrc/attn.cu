@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attn_rows_kernel(const AttnArg
     if constexpr (kSel) {
         const int tiles = (G + 15) / 16;
         const int64_t t = blockIdx.x / tiles;
-        b = seq_of_query(a.cu_seqlens_q, a.B, t);
+        b = warp_seq_of_query(a, t);
         if (b < 0) return;
         s = seq_rows(a, b);
         row0 = (int)(blockIdx.x % tiles) * 16;
@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const AttnAr
     const int hq = (int)(row % a.q_heads);
     pdl_wait();
     pdl_launch_dependents();
-    const int b = seq_of_query(a.cu_seqlens_q, a.B, t);
+    const int b = warp_seq_of_query(a, t);
     if (b < 0 || seq_rows(a, b).nq < 0) return;
     // every warp: all maxima, two splits to a lane at most
     float2 ml[2];
@@ -575,13 +575,19 @@ int64_t attn_plan(AttnArgs& a, int64_t bytes) {
     // round, in pieces of 512 keys at least (two sequences of 131071 keys, 4 kv heads: 36 / 32 / 31
     // / 43 us with 32 / 38 / 57 / 64, the last one round and a bit), or of 256 where those are fewer
     // than the SMs (one sequence of 4000 keys: 20.7 / 13.6 / 10.6 / 9.2 us with 2 / 4 / 8 / 16).
+    // The tensor-memory kernel's steps are longer: its single-token units take one round where they can
+    // (64 x 8192 keys, 64 heads over 1: 83 / 79 / 67 / 76 us with 2 / 3 / 4 / 8), and where sequences
+    // have several queries, of which max_q_len only bounds the number and so most units may be empty, it is
+    // cut finer (8 ragged chunks on up to 3300 keys: 34 / 31 / 30 / 27 us with 2 / 3 / 4 / 6).
     const int64_t slots = (int64_t)sms * choice.per_sm;
+    const bool ragged = !a.n_sel && a.max_q_len > 1;
     int64_t want = 1;
     if (units > 0) {
         const auto least = [](int64_t x, int64_t y) { return x < y ? x : y; };
         want = least(64, least(4 * slots / units, keys / 1024));
-        if (units * want < slots + slots / 2)
-            want = least(64, least(slots / units, keys / (units * keys <= 256ll * sms ? 256 : 512)));
+        const bool one_round = units * want < slots + slots / 2 || (choice.tile && !ragged && units < slots);
+        if (one_round) want = least(64, least(slots / units, keys / (units * keys <= 256ll * sms ? 256 : 512)));
+        if (choice.tile && ragged) want = least(64, least(8 * slots / units, keys / 512));
         if (want < 1) want = 1;
     }
     const int64_t fits = per_split > 0 ? bytes / per_split : 1;

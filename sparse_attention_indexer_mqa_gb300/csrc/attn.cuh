@@ -79,6 +79,26 @@ __device__ __forceinline__ SeqRows seq_rows(const AttnArgs& a, int b) {
     return s;
 }
 
+// The sequence that owns query row t, or -1, found by a whole warp: each round cuts the range by 32 with one round
+// trip to memory, where a binary search takes five.
+__device__ __forceinline__ int warp_seq_of_query(const AttnArgs& a, int64_t t) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = a.B;  // cu[lo] <= t < cu[hi], if t is in any sequence
+    bool in = true;
+    for (bool first = true; first || hi - lo > 1; first = false) {
+        const int step = (hi - lo + 31) / 32;
+        const int at = min(lo + (lane + 1) * step, hi);
+        const int32_t c = a.cu_seqlens_q[at];
+        if (first) in = t >= a.cu_seqlens_q[0] && t < a.cu_seqlens_q[a.B];
+        const unsigned above = __ballot_sync(kFull, c > t);  // ends of parts that lie behind t; the last one does
+        const int part = above ? __ffs(above) - 1 : 31;
+        hi = min(lo + (part + 1) * step, hi);
+        lo = min(lo + part * step, hi - 1);
+        if (!in) break;
+    }
+    return in ? lo : -1;
+}
+
 // Power of two that brings a row of q with the given largest magnitude into fp16's range (its
 // largest value to [2^14, 2^15)), and the exponent it takes away. fp16 rows stay as they are.
 template <bool kHalf>

@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
     if constexpr (kSel) {
         const int tiles = (G + kRowsT - 1) / kRowsT;
         const int64_t t = blockIdx.x / tiles;
-        b = seq_of_query(a.cu_seqlens_q, a.B, t);
+        b = warp_seq_of_query(a, t);
         if (b >= 0) s = seq_rows(a, b);
         row0 = (int)(blockIdx.x % tiles) * kRowsT;
         tok0 = t;
@@ -141,6 +141,7 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
         const int vis = (int)visible_keys(s.len, s.nq, tok - s.t0, a.causal);
         const float rc = write_q_row<D, kHalf>(sm + S::kQ, a.q + tok * a.q_row_stride + (int64_t)hq * a.q_head_stride,
                                                real, tid, a.scale);
+        tc::fence_proxy_async();
         tc::mbar_arrive(q_full);
         const uint32_t lanes = (uint32_t)(warp * 32) << 16;
         const bool idle = 32 * warp >= rows;  // no row of this warp exists
@@ -480,6 +481,7 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
             } else if ((ct & 15) == 0) {
                 scales[(j & 1) * kKeysT + ct / 16] = sc;
             }
+            tc::fence_proxy_async();
             tc::mbar_arrive(k_full);
         };
         auto write_v = [&](int j) {
@@ -494,6 +496,7 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
                 }
             }
             write_v_block<D>(sm + S::kV, rv, my.kg, my.dg, kSel && fold, f);
+            tc::fence_proxy_async();
             tc::mbar_arrive(v_full);
         };
 

@@ -133,13 +133,10 @@ __device__ __forceinline__ float write_q_row(uint8_t* tile, const uint16_t* src,
 }
 
 // S = Q K^T and O (+)= P V of a step, by one lane of the (converged) warp that calls. P lies in the
-// first half of S's columns, as fp16. The operand tiles were written with ordinary stores: the proxy fence
-// between those and the MMAs' reads is here, behind the barrier that says they are written, because in the
-// converters it would wait for the loads they have in flight.
+// first half of S's columns, as fp16.
 template <int D>
 __device__ __forceinline__ void issue_scores(uint32_t tm_s, uint32_t q_tile, uint32_t k_tile, uint64_t* done) {
     tc::tc_fence_after();
-    tc::fence_proxy_async();
     const uint64_t qd = tc::smem_desc_sw128(q_tile), kd = tc::smem_desc_sw128(k_tile);
     if (tc::elect_one()) {
 #pragma unroll
@@ -155,7 +152,6 @@ template <int D>
 __device__ __forceinline__ void issue_outputs(uint32_t tm_o, uint32_t tm_p, uint32_t v_tile, bool accumulate,
                                               uint64_t* done) {
     tc::tc_fence_after();
-    tc::fence_proxy_async();
     const uint64_t vd = tc::smem_desc_sw128(v_tile);
     if (tc::elect_one()) {
 #pragma unroll

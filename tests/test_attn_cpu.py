@@ -82,7 +82,7 @@ def _attn(lib, **kw):
     (dict(out=None), -1), (dict(oh=32), -1), (dict(T=2, orow=32), -1), (dict(pt=None), -1), (dict(sl=None), -1),
     (dict(cu=None), -1), (dict(T=-1), -1), (dict(B=-1), -1), (dict(T=1 << 31), -2), (dict(ps=16), -1),
     (dict(B=1 << 30, T=1 << 20, mq=1 << 10), -2), (dict(T=1 << 28, Hq=8), -2), (dict(sl=18), -1), (dict(lse=6), -1),
-    (dict(mk=(1 << 31) - 65536, w=1 << 25), -2), (dict(sel=16, ss=1 << 31, ns=(1 << 31) - 1), -2), (dict(T=0, q=None), 0), (dict(B=0), 0), (dict(mq=0), 0),
+    (dict(mk=(1 << 31) - 65536, w=1 << 25), -2), (dict(sel=16, ss=1 << 31, ns=(1 << 31) - 1), -2), (dict(T=0, q=None), 0), (dict(T=0, q=None, ns=4), 0), (dict(B=0), 0), (dict(mq=0), 0),
 ])
 def test_attn_refusals(lib, kw, want):
     assert _attn(lib, **kw) == want

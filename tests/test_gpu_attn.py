@@ -562,6 +562,48 @@ def test_streams_and_graphs(torch, Bn):
         a.check(0, sel)
 
 
+def test_two_streams_at_once(torch, Bn):
+    """Metadata, stores and attention of two batches on two streams at the same time, a workspace each:
+    the bits of one after the other."""
+    def batch(seed):
+        a = Att(torch, [3000 + seed, 700], [1, 1], 64 if seed else 8, 1, 128, 64, torch.bfloat16, seed)
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        i32 = dict(dtype=torch.int32, device="cuda")
+        m = dict(ctx=torch.tensor([100 + seed, 63], **i32), new=torch.tensor([5, 9], **i32),
+                 table=torch.full((2, 4), 1, **i32), free=torch.arange(2, 30, **i32), span=torch.tensor([0, 20], **i32),
+                 cu=torch.zeros(3, **i32), lens=torch.zeros(2, **i32), pos=torch.zeros(16, **i32),
+                 slots=torch.zeros(16, dtype=torch.int64, device="cuda"), nxt=torch.zeros(1, **i32))
+        kv = torch.randn(16, 2, 1, 128, device="cuda", generator=g).bfloat16()
+        pool = torch.zeros(40, 2 * 64 * 128 + 16, dtype=torch.uint8, device="cuda")
+        return a, m, kv, pool, a.workspace(Bn)
+
+    def run(b):
+        a, m, kv, pool, ws = b
+        for _ in range(20):
+            Bn.idx_step_meta(m["ctx"], m["new"], m["table"], 64, 256, m["free"], m["span"], 40, m["cu"], m["lens"], m["pos"],
+                             m["slots"], m["nxt"])
+            Bn.idx_kv_store(kv[:, 0], kv[:, 1], m["slots"], pool, 40, 64, pool.stride(0))
+            a.call(Bn, 0, ws=ws)
+
+    both = [batch(0), batch(1)]
+    want = []
+    for b in both:
+        run(b)
+        torch.cuda.synchronize()
+        want.append([x.clone() for x in (b[0].out, b[0].lse, b[1]["slots"], b[3])])
+        for x in (b[0].out, b[0].lse, b[1]["slots"], b[3]):
+            x.zero_()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s, b in zip(streams, both):
+        with torch.cuda.stream(s):
+            run(b)
+    torch.cuda.synchronize()
+    for b, w in zip(both, want):
+        for x, y in zip((b[0].out, b[0].lse, b[1]["slots"], b[3]), w):
+            assert torch.equal(x, y)
+
+
 def test_step_of_all_together(torch, Bn):
     """Three decode steps of a sparse layer as a program runs them: metadata from the lengths, the
     indexer's K store and Q quant, its scores and top-k, the KV store, and the attention over the
