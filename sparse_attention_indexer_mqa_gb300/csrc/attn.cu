@@ -460,21 +460,24 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attn_rows_kernel(const AttnArg
     }
 }
 
-// Joins the splits of a key axis: a CTA per (query row, head), its warps taking splits in turn so that
-// their loads are in flight together, then summed in shared memory.
+// Joins the splits of a key axis. A (query row, head) is joined by kPerRow of a CTA's four warps: all four
+// take splits in turn where rows are few, so that their loads are in flight together, and sum in
+// shared memory (64 rows of 38 splits: 33 us with the attention against 39); enough rows to fill the GPU
+// take a warp each (4096 rows of 4 splits: 184 against 188 us with the attention, 32768 of 2: 56 against 80).
 constexpr int kJoinWarps = 4;
-template <int D, bool kHalf>
+constexpr int kJoinAlone = 8;  // rows per SM from which a warp joins one
+template <int D, bool kHalf, int kPerRow>
 __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const AttnArgs a) {
-    constexpr int kPer = D / 32;  // dims of a lane
-    __shared__ float part[kJoinWarps][D];
-    __shared__ float part_l[kJoinWarps];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t row = blockIdx.x, t = row / a.q_heads, step = a.T * a.q_heads;
+    constexpr int kDims = D / 32;  // dims of a lane
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, first = warp % kPerRow;
+    const int64_t step = a.T * a.q_heads;
+    const int64_t row = (int64_t)blockIdx.x * (kJoinWarps / kPerRow) + warp / kPerRow, t = row / a.q_heads;
     const int hq = (int)(row % a.q_heads);
     pdl_wait();
     pdl_launch_dependents();
+    if (row >= step) return;  // a whole warp, with kPerRow = kJoinWarps never
     const int b = warp_seq_of_query(a, t);
-    if (b < 0 || seq_rows(a, b).nq < 0) return;
+    if (b < 0 || seq_rows(a, b).nq < 0) return;  // the same for all warps of a row
     // every warp: all maxima, two splits to a lane at most
     float2 ml[2];
     float M = neg_inf();
@@ -485,38 +488,54 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const AttnAr
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
-    float g[2], L = 0.0f, v[kPer];
+    float g[2], L = 0.0f, v[kDims];
 #pragma unroll
     for (int i = 0; i < 2; ++i) g[i] = ml[i].x == M ? 1.0f : ex2(ml[i].x - M);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) v[i] = 0.0f;
+    for (int i = 0; i < kDims; ++i) v[i] = 0.0f;
 #pragma unroll 4
-    for (int z = warp; z < a.n_split; z += kJoinWarps) {
+    for (int z = first; z < a.n_split; z += kPerRow) {
         const float gz = __shfl_sync(kFull, z < 32 ? g[0] : g[1], z & 31);
         const float lz = __shfl_sync(kFull, z < 32 ? ml[0].y : ml[1].y, z & 31);
         if (lz == 0.0f) continue;  // that split had no key for this row and wrote no O
         L = fmaf(gz, lz, L);
-        const float* src = a.part_o + (row + z * step) * D + kPer * lane;
+        const float* src = a.part_o + (row + z * step) * D + kDims * lane;
+        float x[kDims];
+        if constexpr (kDims == 4)
+            *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(src);
+        else
+            *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(src);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) v[i] = fmaf(gz, src[i], v[i]);
+        for (int i = 0; i < kDims; ++i) v[i] = fmaf(gz, x[i], v[i]);
     }
+    if constexpr (kPerRow > 1) {
+        __shared__ float part[kJoinWarps][D];
+        __shared__ float part_l[kJoinWarps];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) part[warp][kPer * lane + i] = v[i];
-    if (lane == 0) part_l[warp] = L;
-    __syncthreads();
-    if (threadIdx.x >= D / 2) return;
-    L = 0.0f;
-    float x = 0.0f, y = 0.0f;
+        for (int i = 0; i < kDims; ++i) part[warp][kDims * lane + i] = v[i];
+        if (lane == 0) part_l[warp] = L;
+        __syncthreads();
+        if (warp > 0) return;
 #pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) {
-        L += part_l[w];
-        x += part[w][2 * threadIdx.x];
-        y += part[w][2 * threadIdx.x + 1];
+        for (int w = 1; w < kJoinWarps; ++w) {
+            L += part_l[w];
+#pragma unroll
+            for (int i = 0; i < kDims; ++i) v[i] += part[w][kDims * lane + i];
+        }
     }
     const float n = L == 0.0f ? 0.0f : 1.0f / L;
-    uint16_t* out = a.out + t * a.out_row_stride + (int64_t)hq * a.out_head_stride;
-    reinterpret_cast<uint32_t*>(out)[threadIdx.x] = store_pair<kHalf>(x * n, y * n);
-    if (a.lse && threadIdx.x == 0) a.lse[row] = lse_of(M, L);
+    uint32_t* out = reinterpret_cast<uint32_t*>(a.out + t * a.out_row_stride + (int64_t)hq * a.out_head_stride) +
+                    kDims / 2 * lane;
+#pragma unroll
+    for (int i = 0; i < kDims / 2; ++i) out[i] = store_pair<kHalf>(v[2 * i] * n, v[2 * i + 1] * n);
+    if (a.lse && first == 0 && lane == 0) a.lse[row] = lse_of(M, L);
+}
+
+template <int D, bool kHalf, int kPerRow>
+cudaError_t launch_join(const AttnArgs& a, cudaStream_t st) {
+    constexpr int rows = kJoinWarps / kPerRow;
+    const int64_t ctas = (a.T * a.q_heads + rows - 1) / rows;
+    return launch_pdl(attn_join_kernel<D, kHalf, kPerRow>, dim3((unsigned)ctas), dim3(kJoinWarps * 32), 0, st, a);
 }
 
 // Rows that share their keys: those of a sequence and a kv head, or with a list those of a query's group.
@@ -556,8 +575,8 @@ cudaError_t launch_d(const AttnArgs& a, cudaStream_t st) {
                     : a.sel        ? launch_rows<D, kHalf, true>(a, st)
                                    : launch_rows<D, kHalf, false>(a, st);
     if (e != cudaSuccess || a.n_split <= 1) return e;
-    const int64_t rows = a.T * a.q_heads;
-    return launch_pdl(attn_join_kernel<D, kHalf>, dim3((unsigned)rows), dim3(kJoinWarps * 32), 0, st, a);
+    const int64_t many = (int64_t)kJoinAlone * device_sm_count();
+    return a.T * a.q_heads < many ? launch_join<D, kHalf, kJoinWarps>(a, st) : launch_join<D, kHalf, 1>(a, st);
 }
 
 }  // namespace
@@ -575,19 +594,26 @@ int64_t attn_plan(AttnArgs& a, int64_t bytes) {
     // round, in pieces of 512 keys at least (two sequences of 131071 keys, 4 kv heads: 36 / 32 / 31
     // / 43 us with 32 / 38 / 57 / 64, the last one round and a bit), or of 256 where those are fewer
     // than the SMs (one sequence of 4000 keys: 20.7 / 13.6 / 10.6 / 9.2 us with 2 / 4 / 8 / 16).
-    // The tensor-memory kernel's steps are longer: its single-token units take one round where they can
-    // (64 x 8192 keys, 64 heads over 1: 83 / 79 / 67 / 76 us with 2 / 3 / 4 / 8), and where sequences
-    // have several queries, of which max_q_len only bounds the number and so most units may be empty, it is
-    // cut finer (8 ragged chunks on up to 3300 keys: 34 / 31 / 30 / 27 us with 2 / 3 / 4 / 6).
+    // The tensor-memory kernel's units hold up to 128 rows, whose partial results cost more than a
+    // second round: they are cut to fill one (64 x 8192 keys, 64 heads over 1: 83 / 79 / 67 / 76 us with 2 /
+    // 3 / 4 / 8; 512 queries on 8192 keys: 133 / 107 / 118 with 1 / 2 / 4) and not at all where
+    // they do by themselves (prompts of 1024 and 2048: 34 and 81 us whole, 56 and 116 in 2). max_q_len only
+    // bounds the number of queries, so the units that have rows are counted from T; where chunks are
+    // uneven they are cut to fill three rounds (8 of 3 to 301 queries on up to 3300 keys: 48 / 32 / 27 /
+    // 24 / 29 us with 1 / 2 / 4 / 6 / 8).
     const int64_t slots = (int64_t)sms * choice.per_sm;
-    const bool ragged = !a.n_sel && a.max_q_len > 1;
     int64_t want = 1;
     if (units > 0) {
         const auto least = [](int64_t x, int64_t y) { return x < y ? x : y; };
-        want = least(64, least(4 * slots / units, keys / 1024));
-        const bool one_round = units * want < slots + slots / 2 || (choice.tile && !ragged && units < slots);
-        if (one_round) want = least(64, least(slots / units, keys / (units * keys <= 256ll * sms ? 256 : 512)));
-        if (choice.tile && ragged) want = least(64, least(8 * slots / units, keys / 512));
+        const int64_t one_round_keys = units * keys <= 256ll * sms ? 256 : 512;
+        if (choice.tile) {
+            const int64_t filled = a.n_sel ? units : least(units, (a.T * a.group / 128 + a.B) * a.kv_heads);
+            const bool uneven = !a.n_sel && 4 * a.T < 3ll * a.B * a.max_q_len;
+            want = least(64, least((uneven ? 3 : 1) * slots / filled, keys / one_round_keys));
+        } else {
+            want = least(64, least(4 * slots / units, keys / 1024));
+            if (units * want < slots + slots / 2) want = least(64, least(slots / units, keys / one_round_keys));
+        }
         if (want < 1) want = 1;
     }
     const int64_t fits = per_split > 0 ? bytes / per_split : 1;

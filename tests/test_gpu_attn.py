@@ -382,6 +382,30 @@ def test_long_and_split(torch, Bn, Hq, Hkv, D):
     a.check(1)
 
 
+@pytest.mark.parametrize("Hq,Hkv,D,B", [(63, 1, 64, 21), (64, 8, 128, 21), (33, 1, 128, 41)])
+def test_many_rows_split(torch, Bn, Hq, Hkv, D, B):
+    """Enough rows for a join of a warp a row: an odd number of them, padded ones, sequences of no and one key."""
+    a = Att(torch, [0, 1, 2600] + [1500 + 37 * i for i in range(B - 3)], [1] * B, Hq, Hkv, D, 64, torch.float16, pad=4)
+    ws = a.workspace(Bn)
+    assert ws.numel() > 256 and a.T * Hq > 1216
+    a.call(Bn, 1, ws=ws)
+    a.check(1)
+    a.dev_lens[2] = 1 << 30  # refused: none of its rows is written
+    a.out[2], a.lse[2] = 77, 77
+    kept = a.out.clone()
+    a.call(Bn, 1, ws=ws)
+    assert torch.equal(a.out, kept) and (a.lse[2] == 77).all() and int(a.status) == Bn.IDX_STATUS_BAD_LEN
+
+
+def test_full_grids_are_not_split(torch, Bn):
+    """Partial results of tiles of many rows cost more than another round of them: prompts that fill the GPU ask for no
+    workspace, uneven chunks and short ones on long caches do."""
+    assert Bn.idx_attn_workspace_bytes(1024, 32, 8, 128, 1, 1024, 1024) == 0
+    assert Bn.idx_attn_workspace_bytes(4096, 32, 8, 128, 4, 1024, 16384) == 0
+    assert Bn.idx_attn_workspace_bytes(900, 12, 4, 64, 8, 301, 3300) > 0
+    assert Bn.idx_attn_workspace_bytes(128, 32, 8, 128, 1, 128, 16384) > 0
+
+
 @pytest.mark.parametrize("Hq,nq", [(8, 1), (64, 1), (16, 40)])
 def test_block_scales_far_apart(torch, Bn, Hq, nq):
     """V blocks whose scales differ by 2^30 and logits that favour the small ones."""
