@@ -490,7 +490,8 @@ int idx_kv_store(const void* k, const void* v, int32_t ftype, int64_t n_rows, in
  *   that is split over CTAs when the rows alone do not fill the GPU. idx_attn_workspace_bytes
  *   gives the size that the splitting would like; with less (or NULL) it splits less. One
  *   workspace serves one call at a time. The split, and so the order of sums, depends on the
- *   arguments' sizes alone: same call, same bits.
+ *   arguments' sizes and workspace_bytes alone: same call, same bits. Fewer rows may like a larger one (they are
+ *   split further): a program whose sizes change takes one of a size it can spare for all.
  */
 int idx_attn_workspace_bytes(int64_t T, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t B,
                              int32_t max_q_len, int32_t max_seq_len_k, int32_t n_sel,

@@ -13,7 +13,7 @@
 //   O = P V: S's accumulator is P's A operand as it stands: rows r, r + 8, keys 2c, 2c+1, 8+2c,
 //     9+2c. The thread holds those four keys' dims r*D/8 .. and pairs their bytes by prmt;
 //     column n of step j is dim n*D/8 + j, so a thread ends with D/4 consecutive dims of a row.
-// Measured (bf16): 64 sequences of 8192 keys, 64 heads over 8, D = 128: 190 us, 5.7 TB/s of cache, 84 % of
+// Measured (bf16): 64 sequences of 8192 keys, 64 heads over 8, D = 128: 183 us, 5.9 TB/s of cache, 87 % of
 // the measured copy rate (236 us with lanes' pieces of 16 bytes scattered over lines); two of 131071
 // keys, 32 heads over 4, D = 64: 32 us with the join, 4.2 TB/s. Eleven warps on an SM, each a chain of
 // loads, 64 mma.sync, two shuffles, exponentials and 64 mma.sync a step, do not hide all of it: DRAM
@@ -543,7 +543,7 @@ int64_t shared_rows(const AttnArgs& a) { return a.n_sel ? a.group : (int64_t)a.m
 
 // Which kernel. Dense: up to two mma.sync tiles of shared rows this file's (32 heads over one kv head,
 // 64 x 8192 keys: 60 us against 64; 3000 keys of one sequence: 10.1 against 14.5), more the
-// tensor-memory one (64 heads: 74 against 96). Lists, whose keys are gathered for each tile: up to one (32 heads,
+// tensor-memory one (64 heads: 74 against 96, with one join for both that takes a CTA per row). Lists, whose keys are gathered for each tile: up to one (32 heads,
 // 4096 queries x 1024 keys: 434 us in two tiles, 386 in tensor memory).
 struct Choice {
     bool tile;
@@ -590,12 +590,12 @@ int64_t attn_plan(AttnArgs& a, int64_t bytes) {
     const int64_t per_split = a.T * a.q_heads * (a.head_dim + 2) * 4;
     // Splits. Units that fill the resident CTAs (three or two to an SM) by themselves are cut until there are
     // about four rounds of them, in pieces of 1024 keys at least (64 sequences of 8192 keys, 8
-    // kv heads: 203 / 196 / 188 / 194 us with 1 / 2 / 4 / 7 splits); fewer units are cut until they fill one
+    // kv heads: 202 / 190 / 184 / 191 us with 1 / 2 / 4 / 7 splits); fewer units are cut until they fill one
     // round, in pieces of 512 keys at least (two sequences of 131071 keys, 4 kv heads: 36 / 32 / 31
     // / 43 us with 32 / 38 / 57 / 64, the last one round and a bit), or of 256 where those are fewer
     // than the SMs (one sequence of 4000 keys: 20.7 / 13.6 / 10.6 / 9.2 us with 2 / 4 / 8 / 16).
     // The tensor-memory kernel's units hold up to 128 rows, whose partial results cost more than a
-    // second round: they are cut to fill one (64 x 8192 keys, 64 heads over 1: 83 / 79 / 67 / 76 us with 2 /
+    // second round: they are cut to fill one (64 x 8192 keys, 64 heads over 1: 75 / 73 / 63 / 71 us with 2 /
     // 3 / 4 / 8; 512 queries on 8192 keys: 133 / 107 / 118 with 1 / 2 / 4) and not at all where
     // they do by themselves (prompts of 1024 and 2048: 34 and 81 us whole, 56 and 116 in 2). max_q_len only
     // bounds the number of queries, so the units that have rows are counted from T; where chunks are

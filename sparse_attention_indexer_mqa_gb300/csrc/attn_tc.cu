@@ -19,16 +19,16 @@
 // (tensor memory 2 x 256 columns, shared memory 2 x 107 KB): one's products run under the other's
 // softmax.
 //
-// What bounds it. That prompt takes 626 us, 878 TFLOP/s of its visible pairs (45 % of a large bf16 product's measured
+// What bounds it. That prompt takes 622 us, 884 TFLOP/s of its visible pairs (46 % of a large bf16 product's measured
 // rate). Eight MMAs of 128 x 128 x 16 take 736 cycles (both operands in shared memory) or 679
 // (P in tensor memory) with nothing else on the SM, so a step needs 1415 cycles of the tensor pipe;
 // a CTA's step takes 4400: S 740, softmax 1950, O += P V 700, and 200 to 500 from each to
 // the next. Measured and no faster: 64-key steps with two S (S of the next step under this step's softmax;
-// an N = 64 MMA takes as long as an N = 128 one: 600 us, and 548 instead of 443 us with lists),
+// an N = 64 MMA takes as long as an N = 128 one: 600 us, and 548 with lists, which were at 443 then),
 // with K's and V's converters apart (645, 518); two tiles to a CTA that share converted K and V (698, and
 // 685 with the tiles' MMAs in turn); the softmax in one pass over S with P kept in registers
-// (665). With lists (4096 queries x 1024 keys, 64 heads over 1: 443 us) half of a tile's rows are
-// empty and a unit is only eight steps long; the order of the keys hardly matters (441 in order).
+// (665). With lists (4096 queries x 1024 keys, 64 heads over 1: 453 us) half of a tile's rows are
+// empty and a unit is only eight steps long; the order of the keys hardly matters (441 in order, 448 at random).
 #include "attn_tc.cuh"
 
 namespace idx {
