@@ -473,7 +473,8 @@ int idx_kv_store(const void* k, const void* v, int32_t ftype, int64_t n_rows, in
  * max_q_len and max_seq_len_k as in idx_mqa_logits_paged) and, when sel_idx is given, that
  * sel_idx[t*sel_stride .. + n_sel - 1] lists (int32 key positions in the sequence, any order:
  * the output of idx_topk, idx_mqa_topk_paged or idx_mqa_topk_cand_paged). Entries that are
- * negative or not visible are ignored; a position listed twice counts twice.
+ * negative or not visible are ignored; a position listed twice counts twice. n_sel >= 1 with a list, 0
+ * without one.
  *   q: [T][Hq][D] at q + t*q_row_stride + h*q_head_stride; out alike with its own strides (elements; 16-byte
  *     aligned, strides multiples of 8; out strides >= D); both of type ftype. Query head h reads kv
  *     head h / (Hq / kv_heads); Hq is a multiple of kv_heads. lse: fp32 [T][Hq], may be NULL.

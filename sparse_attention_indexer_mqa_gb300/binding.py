@@ -423,7 +423,7 @@ def idx_attn_paged(q, pool, num_pages, page_size, page_stride, kv_heads, page_ta
                    causal, max_q_len, max_seq_len_k, softmax_scale, out, lse=None, sel_idx=None, workspace=None,
                    dev_status=None, stream=None):
     """q, out: bf16 or fp16 [T, q_heads, head_dim], last dimension dense, the others strided;
-    sel_idx: int32 [T, n_sel], rows strided (the top-k's output), or None for every visible key."""
+    sel_idx: int32 [T, n_sel], n_sel >= 1, rows strided (the top-k's output), or None for every visible key."""
     fn, dev = "idx_attn_paged", _device()
     i32 = _torch.int32
     ft = _ftype(fn, q)
@@ -463,8 +463,9 @@ def idx_attn_paged(q, pool, num_pages, page_size, page_stride, kv_heads, page_ta
         n, n_sel = sel_idx.shape
         s0, s1 = sel_idx.stride()
         sel_stride = max(s0, n_sel)
-        if n != T or (T > 0 and n_sel > 1 and s1 != 1) or (T > 1 and s0 < n_sel):
-            raise ValueError(f"{fn}: sel_idx {tuple(sel_idx.shape)} with strides {sel_idx.stride()}")
+        # without columns its pointer may be null, which the library takes for no list
+        if n != T or (T > 0 and (n_sel < 1 or (n_sel > 1 and s1 != 1))) or (T > 1 and s0 < n_sel):
+            raise ValueError(f"{fn}: sel_idx {tuple(sel_idx.shape)} with strides {sel_idx.stride()} for {T} rows")
         sel_p = sel_idx.data_ptr()
     if workspace is not None:
         if workspace.get_device() != dev:
