@@ -377,9 +377,16 @@ def idx_kv_layout(kv_heads: int, head_dim: int, page_size: int) -> IdxKvLayout:
     return out
 
 
+def _bytes_behind(x):
+    """Bytes from a tensor's first element to the end of its memory: more than its own where it is a view with
+    gaps, fewer where it repeats elements."""
+    return x.untyped_storage().nbytes() - x.storage_offset() * x.element_size()
+
+
 def _pool_bytes(fn, pool, num_pages, page_stride, page_bytes, dev):
     """The pool holds its pages: the library only sees a pointer."""
-    if pool.get_device() != dev or (num_pages > 0 and pool.nbytes < (num_pages - 1) * page_stride + page_bytes):
+    have = pool.nbytes if pool.is_contiguous() else _bytes_behind(pool)
+    if pool.get_device() != dev or (num_pages > 0 and have < (num_pages - 1) * page_stride + page_bytes):
         raise ValueError(f"{fn}: the pool ({tuple(pool.shape)}, {pool.dtype}, {pool.device}) does not hold {num_pages} pages "
                          f"{page_stride} bytes apart on the current CUDA device")
 
@@ -468,8 +475,9 @@ def idx_attn_paged(q, pool, num_pages, page_size, page_stride, kv_heads, page_ta
             raise ValueError(f"{fn}: sel_idx {tuple(sel_idx.shape)} with strides {sel_idx.stride()} for {T} rows")
         sel_p = sel_idx.data_ptr()
     if workspace is not None:
-        if workspace.get_device() != dev:
-            raise ValueError(f"{fn}: the workspace is on {workspace.device}, not on the current CUDA device")
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError(f"{fn}: the workspace has to be contiguous, on the current CUDA device; got "
+                             f"{tuple(workspace.shape)}, strides {workspace.stride()}, {workspace.device}")
         wsb, ws_p = workspace.nbytes, workspace.data_ptr()
     st = (_lib or load()).idx_attn_paged(
         q.data_ptr(), ft, T, H, kv_heads, D, qr, qh, pool.data_ptr(), num_pages, page_size, page_stride,

@@ -55,3 +55,41 @@ def test_lists_reach_the_library(calls):
     assert got[0] == [sel.data_ptr(), 9, 7]
     assert got[1] == [None, 0, 0]
     assert got[3][0] in (None, 0)
+
+
+def store(pool, pages, stride, H=1, D=64, P=64):
+    k = torch.zeros(1, H, D, dtype=torch.float16)
+    Bn.idx_kv_store(k, k.clone(), torch.zeros(1, dtype=torch.int64), pool, pages, P, stride, stream=0)
+
+
+PAGE = 2 * 64 * 64 + 16
+
+
+@pytest.mark.parametrize("use", [lambda pool, pages, stride: store(pool, pages, stride),
+                                 lambda pool, pages, stride: attend(pool=pool, pages=pages, stride=stride)])
+def test_pool_is_measured_by_the_memory_behind_it(calls, use):
+    """A view of a wider pool holds its pages though its own elements are fewer than the strides span; one
+    that repeats its elements does not."""
+    wide = torch.zeros(3, PAGE + 64, dtype=torch.uint8)
+    use(wide[:, :PAGE], 3, wide.stride(0))
+    use(wide[1:, 16:16 + PAGE], 2, wide.stride(0))
+    use(wide[0], 1, wide.stride(0))
+    use(wide.view(-1)[:2 * wide.stride(0) + PAGE], 3, wide.stride(0))
+    assert len(calls) == 4
+    bad = [(wide[:, :PAGE], 4, wide.stride(0)), (wide[1:], 3, wide.stride(0)),
+           (wide[2, 65:], 1, PAGE), (wide[0, :PAGE].expand(9, PAGE), 9, PAGE)]
+    for pool, pages, stride in bad:
+        with pytest.raises(ValueError, match="pool"):
+            use(pool, pages, stride)
+    assert len(calls) == 4
+
+
+def test_workspace_without_memory_of_its_own_is_refused(calls):
+    """A view that repeats or skips elements claims bytes that are not its own."""
+    room = torch.zeros(1 << 16, dtype=torch.uint8)
+    attend(workspace=room[256:])
+    assert calls[0][1][29] == (1 << 16) - 256
+    for ws in (room[:1].expand(1 << 20), room[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            attend(workspace=ws)
+    assert len(calls) == 1
