@@ -42,7 +42,7 @@ int idx_step_meta(const int32_t* ctx_lens, const int32_t* q_lens, int32_t B, int
     Range r("idx_step_meta");
     if (B < 0 || pt_stride < 0 || max_seq_len_k < 0 || free_cap < 0 || num_pages < 0 || T_cap < 0) return IDX_EINVAL;
     if (page_size != 64 && page_size != 128) return IDX_EUNSUPPORTED;
-    if (B > 16384 || T_cap > INT32_MAX) return IDX_EUNSUPPORTED;
+    if (B > idx::kMetaMaxRequests || T_cap > INT32_MAX) return IDX_EUNSUPPORTED;
     if (max_seq_len_k > (int64_t)pt_stride * page_size) return IDX_EINVAL;
     if (!free_span || !cu_seqlens_q || !free_next || (free_cap > 0 && !free_pages)) return IDX_EINVAL;
     if (B > 0 && (!ctx_lens || !q_lens || !seq_lens_k || (!page_table && pt_stride > 0))) return IDX_EINVAL;

@@ -145,6 +145,7 @@ int prefill_queries_per_block(int32_t H);
 int device_sm_count();
 
 // Step metadata (idx_step_meta).
+constexpr int32_t kMetaMaxRequests = 16384;  // 8 bytes each in shared memory
 struct MetaArgs {
     const int32_t* ctx_lens;
     const int32_t* q_lens;

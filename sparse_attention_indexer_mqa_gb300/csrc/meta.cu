@@ -185,10 +185,10 @@ cudaError_t launch_step_meta(const MetaArgs& a, cudaStream_t st) {
     const int rows = threads;
     const int64_t ctas = a.T_cap > rows ? (a.T_cap + rows - 1) / rows : 1;
     const size_t smem = (2 * (size_t)a.B + 1) * sizeof(int32_t);
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(step_meta_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   (int)smem);
-        if (e != cudaSuccess) return e;
+    if (smem > 48 * 1024) {  // raised to the most that any call needs: another thread's call may come in between
+        static std::atomic<uint64_t> allowed{0};
+        const cudaError_t s = allow_smem(allowed, step_meta_kernel, (2 * kMetaMaxRequests + 1) * (int)sizeof(int32_t));
+        if (s != cudaSuccess) return s;
     }
     const cudaError_t e = launch_k(false, step_meta_kernel, dim3((unsigned)ctas), dim3(threads), smem, st, a, rows);
     if (e == cudaSuccess) {
