@@ -405,10 +405,9 @@ int idx_debug_wait_timeout(int32_t limit_us, int32_t* dev_status, cudaStream_t s
  *   gives slot -1; so does a free_span outside [0, free_cap], which is taken as empty.
  * max_seq_len_k <= pt_stride * P. B <= 16384 (IDX_EUNSUPPORTED above). B = 0 or T_cap = 0 is
  *   allowed. The outputs may not overlap the inputs or one another (IDX_EINVAL where the
- *   base addresses are equal). The library's next call on the stream (a replayed graph's next node
- *   likewise) starts when the outputs are visible: the library remembers that this call was the
- *   stream's last. A step whose next call goes to another stream orders the two by an event,
- *   as ever.
+ *   base addresses are equal). What follows on the stream (or in a replayed graph), other calls of the
+ *   library among them, starts when the outputs are visible. A step whose next call goes to another
+ *   stream orders the two by an event, as ever.
  */
 int idx_step_meta(const int32_t* ctx_lens, const int32_t* q_lens, int32_t B, int32_t* page_table,
                   int32_t pt_stride, int32_t page_size, int32_t max_seq_len_k,

@@ -34,17 +34,12 @@ __device__ __forceinline__ void report(int32_t* status, int32_t bit) {
 // overlaps the kernel before them. Either way every CTA of a kernel is resident before its
 // dependent launches (no dependent can hold the resources a CTA of it still needs), and a
 // kernel's pdl_wait() returning means its predecessor, and everything that one waited for,
-// has completed.
+// has completed. idx_step_meta, which writes what the others read before they wait, ends with a
+// kernel that only waits (meta.cu).
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
-
-// idx_step_meta writes what the kernels read before pdl_wait(), so the call behind it on its
-// stream is launched without programmatic serialization: it starts when the metadata are
-// visible, and what follows it starts no earlier. The metadata call leaves a mark (meta.cu).
-extern std::atomic<int> g_order_marks;     // streams with a mark
-bool take_order_mark(cudaStream_t st);     // true, once, if st has one
 
 // Launch with programmatic stream serialization (the kernel calls pdl_wait()) when pdl is
 // true, else as an ordinary stream-ordered launch (the previous kernel has finished, and its
@@ -52,7 +47,6 @@ bool take_order_mark(cudaStream_t st);     // true, once, if st has one
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_k(bool pdl, void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                             cudaStream_t st, Args&&... args) {
-    if (g_order_marks.load(std::memory_order_relaxed) > 0 && take_order_mark(st)) pdl = false;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;

@@ -9,34 +9,15 @@
 // request by binary search in the sums, which stay in shared memory (8 bytes a request).
 // Reads and writes of the page table never meet: a row reads entries below ceil(ctx/P) or
 // the free list, and only entries from ceil(ctx/P) on are written.
-// Measured: 64 requests of one token 5.6 us, 512 requests with 66173 rows 7.8 us (0.8 MB): launch,
-// two sums with four barriers, and per row a binary search and two dependent loads.
-#include <algorithm>
-#include <mutex>
-#include <thread>
-#include <tuple>
-#include <vector>
-
+// Measured in a replayed graph: 64 requests of one token 6.0 us, 512 requests with 66173 rows 8.5 us (0.8 MB): launch,
+// two sums with four barriers, and per row a binary search and two dependent loads; 0.4 and 0.7 us of it are the
+// waiting kernel behind. A call from the host takes 10.6 and 11.0 us, 1.8 of them for the second launch.
 #include "common.cuh"
 #include "kernels.h"
 
 namespace idx {
 
-std::atomic<int> g_order_marks{0};
-
 namespace {
-
-// Streams whose last library call was idx_step_meta. A per-thread default stream has one handle in every
-// thread, and a device's legacy stream has the handle of every other's.
-using StreamKey = std::tuple<cudaStream_t, int, std::thread::id>;
-std::mutex order_mutex;
-std::vector<StreamKey> ordered;
-
-StreamKey key_of(cudaStream_t st) {
-    int dev = 0;
-    cudaGetDevice(&dev);
-    return {st, dev, st == cudaStreamPerThread ? std::this_thread::get_id() : std::thread::id()};
-}
 
 // Exclusive sum over the CTA of one value per thread, and the total.
 __device__ __forceinline__ int64_t cta_scan(int64_t v, int64_t* warp_sums, int64_t& total) {
@@ -70,6 +51,7 @@ __global__ void step_meta_kernel(const MetaArgs a, int rows_per_cta) {
     const int per = (a.B + nt - 1) / nt;  // consecutive requests of a thread
     const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
     const int64_t P = a.page_size;
+    pdl_launch_dependents();  // step_meta_done_kernel
 
     int64_t head = a.free_span[0], tail = a.free_span[1];
     if (head < 0 || tail < head || tail > a.free_cap) {
@@ -167,20 +149,18 @@ __global__ void step_meta_kernel(const MetaArgs a, int rows_per_cta) {
     }
 }
 
-}  // namespace
+// Behind the metadata: returns when they are visible. The library's kernels read lengths and page tables before they
+// wait for the kernel in front of them, and a kernel launched with programmatic serialization may start as
+// soon as the CTAs of that one have ended. In front of them is this one, whose CTA ends behind its wait: whatever
+// is launched next, eagerly, captured or replayed, starts when the metadata are there. It is resident while the
+// metadata kernel runs.
+__global__ void step_meta_done_kernel() { pdl_wait(); }
 
-bool take_order_mark(cudaStream_t st) {
-    std::lock_guard<std::mutex> lock(order_mutex);
-    const auto it = std::find(ordered.begin(), ordered.end(), key_of(st));
-    if (it == ordered.end()) return false;
-    ordered.erase(it);
-    g_order_marks.store((int)ordered.size(), std::memory_order_relaxed);
-    return true;
-}
+}  // namespace
 
 cudaError_t launch_step_meta(const MetaArgs& a, cudaStream_t st) {
     // a thread per request for the sums where that fits, and a thread per row (512 requests, 66173 rows: 7.8 us, 11.8
-    // with four rows a thread)
+    // with four rows a thread, the waiting kernel not counted)
     const int threads = a.B <= 256 ? 256 : 1024;
     const int rows = threads;
     const int64_t ctas = a.T_cap > rows ? (a.T_cap + rows - 1) / rows : 1;
@@ -191,13 +171,7 @@ cudaError_t launch_step_meta(const MetaArgs& a, cudaStream_t st) {
         if (s != cudaSuccess) return s;
     }
     const cudaError_t e = launch_k(false, step_meta_kernel, dim3((unsigned)ctas), dim3(threads), smem, st, a, rows);
-    if (e == cudaSuccess) {
-        std::lock_guard<std::mutex> lock(order_mutex);
-        const StreamKey k = key_of(st);
-        if (std::find(ordered.begin(), ordered.end(), k) == ordered.end()) ordered.push_back(k);
-        g_order_marks.store((int)ordered.size(), std::memory_order_relaxed);
-    }
-    return e;
+    return e == cudaSuccess ? launch_pdl(step_meta_done_kernel, dim3(1), dim3(32), 0, st) : e;
 }
 
 }  // namespace idx

@@ -56,3 +56,91 @@ def test_meta_of_unlike_batches_from_threads(torch, Bn):
     for x in threads:
         x.join()
     assert not errors, errors
+
+
+@pytest.mark.parametrize("between", ["nothing", "capture", "refused", "names"])
+def test_lengths_reach_the_next_call_whatever_lies_between(torch, Bn, between):
+    """The top-k reads lengths before it waits for the kernel in front of it. Eager metadata and top-k with a
+    capture on the same stream between them, a refused call, or another name of the same stream."""
+    t, call, _ = decode_step(torch, Bn, 512)
+    L, k = 256, 4
+    logits = torch.arange(L, device="cuda").float().repeat(512, 1).contiguous()
+    got = [torch.zeros(512, k, dtype=torch.int32, device="cuda") for _ in range(40)]
+    ctx = torch.randint(4, 200, (len(got), 512), dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    first, second = (0, 1) if between == "names" else (side, side)  # 1: cudaStreamLegacy
+    torch.cuda.synchronize()
+    graphs = []
+    for i, out in enumerate(got):
+        with torch.cuda.stream(torch.cuda.default_stream() if between == "names" else side):
+            t["ctx"].copy_(ctx[i])
+            call(stream=first)
+            if between == "capture":
+                graphs.append(torch.cuda.CUDAGraph())
+                graphs[-1].capture_begin()
+                Bn.idx_topk(logits, t["lens"], t["cu"], 0, L, k, torch.zeros_like(out), stream=side)
+                graphs[-1].capture_end()
+            elif between == "refused":
+                with pytest.raises(Bn.IdxError):
+                    Bn.idx_topk(logits, t["lens"], t["cu"], 0, L, 0, out, stream=side)
+            Bn.idx_topk(logits, t["lens"], t["cu"], 0, L, k, out, stream=second)
+    torch.cuda.synchronize()
+    n = ctx.long() + 1
+    want = torch.stack([n - 3, n - 2, n - 1, n - 4], -1).int()  # above the k-th in index order, then the k-th
+    wrong = (torch.stack(got) != want).any(-1).nonzero()
+    assert len(wrong) == 0, (len(wrong), [(n[i, b].item(), got[i][b].tolist()) for i, b in wrong[:4].tolist()])
+
+
+def test_two_streams_in_turns(torch, Bn):
+    """Metadata, store and attention of two batches on two streams, call by call in turn: the bits of one
+    after the other."""
+    P, H, D = 64, 1, 128
+
+    def batch(seed):
+        B = 300 + 100 * seed
+        t, call, want = decode_step(torch, Bn, B, 5, seed)
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        kv = torch.randn(B + 5, 2, H, D, device="cuda", generator=g).bfloat16()
+        q = torch.randn(B + 5, 16 + 48 * seed, D, device="cuda", generator=g).bfloat16()
+        pool = torch.zeros(6 * B, 2 * P * D + 16, dtype=torch.uint8, device="cuda")
+        out = torch.zeros_like(q)
+
+        def attend(stream):
+            Bn.idx_attn_paged(q, pool, 6 * B, P, pool.stride(0), H, t["table"], t["lens"], t["cu"], 1, 1, 4 * P, 0.1, out,
+                              stream=stream)
+        steps = [lambda s: call(stream=s),
+                 lambda s: Bn.idx_kv_store(kv[:, 0], kv[:, 1], t["slots"], pool, 6 * B, P, pool.stride(0), stream=s),
+                 attend, lambda s: (t["ctx"].copy_(t["lens"]), t["span"][:1].copy_(t["nxt"]))]
+        ctx = t["ctx"].clone()
+
+        def reset():
+            t["ctx"].copy_(ctx)
+            t["span"][:1].zero_()
+            t["table"].copy_(torch.arange(4 * B, dtype=torch.int32, device="cuda").reshape(B, 4))
+            pool.zero_()
+            out.zero_()
+        return steps, reset, (out, pool, t["slots"], t["lens"], t["table"]), want
+
+    both = [batch(0), batch(1)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    alone = []
+    for (steps, reset, outs, want), s in zip(both, streams):
+        with torch.cuda.stream(s):
+            reset()
+            steps[0](s)
+            assert torch.equal(outs[2].cpu(), want)
+            reset()
+            for _ in range(30):
+                for step in steps:
+                    step(s)
+            alone.append([x.clone() for x in outs])
+            reset()
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for i in range(4):
+            for (steps, _, _, _), s in zip(both, streams):
+                with torch.cuda.stream(s):
+                    steps[i](s)
+    torch.cuda.synchronize()
+    for (_, _, outs, _), want in zip(both, alone):
+        assert all(torch.equal(x, y) for x, y in zip(outs, want))
