@@ -139,6 +139,7 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
         const int64_t tok = kSel ? tok0 : tok0 + row / G;
         const int hq = head * G + (kSel ? row : row % G);
         const int vis = (int)visible_keys(s.len, s.nq, tok - s.t0, a.causal);
+        // < 0: an infinity or a NaN in q; the row is scored as zeros, and is NaN at the end if any key counted
         const float rc = write_q_row<D, kHalf>(sm + S::kQ, a.q + tok * a.q_row_stride + (int64_t)hq * a.q_head_stride,
                                                real, tid, a.scale);
         tc::fence_proxy_async();
@@ -325,6 +326,7 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
         if (ok && n > 0 && !idle) ok = warp_wait<kNsSoft>(o_done, (n - 1) & 1);
         if (ok && !idle) {
             tc::tc_fence_after();
+            if (rc < 0.0f && l != 0.0f) l = __int_as_float(0x7fc00000);
             store_rows<D, kHalf>(a, tm_o + lanes, n > 0, real, tok, hq, z, m, l);
         }
     } else {

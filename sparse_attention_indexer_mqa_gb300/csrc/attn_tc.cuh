@@ -95,8 +95,8 @@ __device__ __forceinline__ void write_v_block(uint8_t* tile, const uint4 (&rv)[8
     }
 }
 
-// A thread's row of q as fp16 into row `row` of the Q tile (zeros if it does not exist); returns the row's
-// factor: softmax_scale * log2(e) * (the power of two taken out), NaN for a row that is not finite.
+// A thread's row of q as fp16 into row `row` of the Q tile (zeros if it does not exist or is not finite); returns the
+// row's factor: softmax_scale * log2(e) * (the power of two taken out), -1 for a row that is not finite.
 template <int D, bool kHalf>
 __device__ __forceinline__ float write_q_row(uint8_t* tile, const uint16_t* src, bool real, int row, float scale) {
     const uint4* q = reinterpret_cast<const uint4*>(src);
@@ -117,7 +117,7 @@ __device__ __forceinline__ float write_q_row(uint8_t* tile, const uint16_t* src,
     const float up = pow2f(-e);
 #pragma unroll 4
     for (int i = 0; i < D / 8; ++i) {  // again, from L1
-        const uint4 w = real ? q[i] : make_uint4(0, 0, 0, 0);
+        const uint4 w = real && !odd ? q[i] : make_uint4(0, 0, 0, 0);
         uint32_t u[4] = {w.x, w.y, w.z, w.w};
         if constexpr (!kHalf) {
 #pragma unroll
@@ -129,7 +129,7 @@ __device__ __forceinline__ float write_q_row(uint8_t* tile, const uint16_t* src,
         *reinterpret_cast<uint4*>(tile + dims_sub<D>(i) * (kRowsT * 128) + row * 128 +
                                   ((dims_chunk<D>(i) ^ (row & 7)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
     }
-    return odd ? __int_as_float(0x7fc00000) : scale * kLog2e * pow2f(e);
+    return odd ? -1.0f : scale * kLog2e * pow2f(e);
 }
 
 // S = Q K^T and O (+)= P V of a step, by one lane of the (converged) warp that calls. P lies in the

@@ -1,11 +1,46 @@
 """Calls of the step metadata and the paged attention at the borders of what include/idx.h allows, on the GPU."""
+import math
 import threading
 
 import pytest
 
-from test_gpu_attn import Bn, torch  # noqa: F401  (fixtures)
+from test_gpu_attn import Att, Bn, torch  # noqa: F401  (fixtures and inputs)
 
 pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------------------ rows without keys
+
+@pytest.mark.parametrize("Hq,nq", [(8, 1), (64, 1), (64, 3), (17, 1)])
+@pytest.mark.parametrize("k", [5, 700, 1500])
+@pytest.mark.parametrize("split", [False, True])
+def test_non_finite_query_without_keys(torch, Bn, Hq, nq, k, split):
+    """A row whose list holds nothing that counts has out 0 and lse -inf whatever its query holds; one key makes it
+    NaN."""
+    a = Att(torch, [100, 90, 80], [nq] * 3, Hq, 1, 128, 64, torch.bfloat16)
+    sel = torch.full((a.T, k), -1, dtype=torch.int32, device="cuda")
+    sel[:, 1::2] = 100
+    sel[2 * nq:, k - 1] = 0
+    for value in (math.nan, math.inf):
+        a.q[:, ::2, 3] = value
+        a.out.fill_(77)
+        a.lse.fill_(77)
+        a.call(Bn, 1, sel, a.workspace(Bn, k) if split else None)
+        assert int(a.status) == 0
+        assert (a.out[:2 * nq] == 0).all() and (a.lse[:2 * nq] == -math.inf).all()
+        assert a.out[2 * nq:, ::2].isnan().all() and a.lse[2 * nq:, ::2].isnan().all()
+        assert a.out[2 * nq:, 1::2].isfinite().all() and a.lse[2 * nq:, 1::2].isfinite().all()
+
+
+@pytest.mark.parametrize("Hq,nq", [(8, 1), (64, 1), (4, 40)])
+def test_non_finite_query_on_pages_outside_the_pool(torch, Bn, Hq, nq):
+    a = Att(torch, [130, 90], [nq, nq], Hq, 1, 64, 64, torch.float16)
+    a.table[0] = a.pages
+    a.q[:, 1] = math.inf
+    a.call(Bn, 1)
+    assert int(a.status) == Bn.IDX_STATUS_BAD_PAGE
+    assert (a.out[:nq] == 0).all() and (a.lse[:nq] == -math.inf).all()
+    assert a.out[nq:, 1].isnan().all() and a.out[nq:, 0].isfinite().all()
 
 
 # ------------------------------------------------------------------------------ step metadata
