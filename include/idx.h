@@ -481,8 +481,9 @@ int idx_kv_store(const void* k, const void* v, int32_t ftype, int64_t n_rows, in
  * A row that sees no key gets out 0 and lse -inf. Rows of no sequence (behind cu_seqlens_q[B]) are
  *   left as they were, and so are the rows of a sequence that breaks its length bounds
  *   (IDX_STATUS_BAD_LEN). Keys of a page outside the pool are skipped (IDX_STATUS_BAD_PAGE). A query
- *   row that holds an infinity or a NaN gives NaN in that row (out and lse) if it sees a key. What the cache holds in slots that a row
- *   does not see (NaN codes too) does not reach it.
+ *   row that holds an infinity or a NaN gives NaN in that row (out and lse) if it sees a key. What the
+ *   cache holds in slots that a row does not see (NaN codes too) does not reach it. A NaN code that a row does see
+ *   (idx_kv_store writes none) gives NaN: one of K in all of out and in lse, one of V in its dim of out at least.
  * Arithmetic: q is scaled by a power of two per row and held in fp16 (exact for fp16 and, but for
  *   values below 2^-28 of the row's largest, for bf16), products and sums in fp32; the softmax
  *   weights are rounded to fp16 (2^-11 relative, half a step) for the product with v.

@@ -61,11 +61,14 @@ struct Ring {
 };
 __device__ __forceinline__ constexpr int swizzle(int t) { return (((t >> 1) & 3) << 1) ^ ((t & 1) << 2); }
 
-template <int D, bool kHalf, bool kSel>
+// kDiag: rows of a unit may see unlike numbers of keys (dense, causal, several queries to a sequence). The ring starts on
+// a 128-byte line: 16 bytes past one, 64 x 8192 keys took 205 us.
+template <int D, bool kHalf, bool kSel, bool kDiag>
 __global__ void __launch_bounds__(kWarps * 32, 3) attn_rows_kernel(const AttnArgs a) {
     using R = Ring<D>;
-    extern __shared__ __align__(16) uint8_t sm[];
+    extern __shared__ __align__(128) uint8_t sm[];
     __shared__ float2 ml[kWarps][16];
+    __shared__ int nan_key[kDiag ? kWarps : 1];  // lowest key whose V held a NaN code that was taken out
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, c = lane & 3;
     pdl_wait();
     pdl_launch_dependents();
@@ -369,16 +372,37 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attn_rows_kernel(const AttnArg
         }
     };
 
+    // V's NaN codes taken out of a step's keys that some row does not see.
+    [[maybe_unused]] auto clear_v = [&](int it) {
+        constexpr int kVPieces = D / 16;
+        uint8_t* sp = ring + (it & (kStages - 1)) * R::kStage + R::kVAt;
+        const int kb = kw + kStep * it, t0 = max(vis_lo - kb, 0), t1 = min(k1 - kb, kKeys);
+#pragma unroll 1
+        for (int x = t0 * kVPieces + lane; x < t1 * kVPieces; x += 32) {
+            const int t = x / kVPieces, chunk = x % kVPieces + (D == 128 ? 0 : kVPieces);
+            uint4* at = reinterpret_cast<uint4*>(sp + t * 128 + ((chunk ^ swizzle(t)) << 4));
+            uint4 w = *at;
+            if (clear_nan_codes(w.x) | clear_nan_codes(w.y) | clear_nan_codes(w.z) | clear_nan_codes(w.w)) {
+                *at = w;
+                atomicMin(&nan_key[warp], kb + t);
+            }
+        }
+        __syncwarp();
+    };
+
+    if (kDiag && lane == 0) nan_key[warp] = INT32_MAX;
     if (n_it > 0) {
         if constexpr (kSel) {
             ent = load_entry(0);
             ent_n = load_entry(1);
         }
         page = load_page(0);
-#pragma unroll 1
-        for (int it = -1; it < n_it; ++it) {
-            const uint32_t scales = scales_n;
-            const bool page_ok = page_ok_n;
+        // A round: the copies of step it + 1 go out, the ones of step it have arrived.
+        uint32_t scales = 0;
+        bool page_ok = false;
+        auto next = [&](int it) {
+            scales = scales_n;
+            page_ok = page_ok_n;
             __syncwarp();  // the stage that comes next has been read by every lane
             issue(it + 1);
             if constexpr (kSel) {
@@ -386,16 +410,29 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attn_rows_kernel(const AttnArg
                 ent_n = load_entry(it + 3);
             }
             page = load_page(it + 2);
-            if (it < 0) continue;
             cp_async_wait<kStages - 1>();
             __syncwarp();  // every lane's copies have arrived
-            if constexpr (kSel) {
+        };
+        next(-1);
+        if constexpr (kSel) {
+#pragma unroll 1
+            for (int it = 0; it < n_it; ++it) {
+                next(it);
                 compute(it, scales, std::true_type{});
-            } else if (page_ok) {  // else none of these keys exists
-                if (kw + kStep * it + kKeys <= vis_lo)
-                    compute(it, scales, std::false_type{});
-                else
-                    compute(it, scales, std::true_type{});
+            }
+        } else {
+            // A unit's rows see at most 15 keys more the one than the other, and a warp's steps are 128 keys
+            // apart: only its last one can hold a key that some row does not see. Keys of a page outside the
+            // pool do not exist.
+#pragma unroll 1
+            for (int it = 0; it < n_it - 1; ++it) {
+                next(it);
+                if (page_ok) compute(it, scales, std::false_type{});
+            }
+            next(n_it - 1);
+            if (page_ok) {
+                if constexpr (kDiag) clear_v(n_it - 1);
+                compute(n_it - 1, scales, std::true_type{});
             }
         }
         cp_async_wait<0>();
@@ -443,6 +480,13 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attn_rows_kernel(const AttnArg
             v.z = fmaf(g, y.z, v.z); v.w = fmaf(g, y.w, v.w);
         }
         const int at = row0 + row;
+        if constexpr (kDiag) {
+            int least = INT32_MAX;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) least = min(least, nan_key[w]);
+            if (least < INT32_MAX && least < (int)visible_keys(s.len, s.nq, at / G, a.causal))
+                v.x = v.y = v.z = v.w = __int_as_float(0x7fc00000);
+        }
         const int64_t tok = kSel ? tok0 : tok0 + at / G;
         const int hq = head * G + (kSel ? at : at % G);
         if (a.n_split > 1) {
@@ -556,10 +600,10 @@ Choice choose(const AttnArgs& a) {
     return {true, times * ((rows + 127) / 128), 2};
 }
 
-template <int D, bool kHalf, bool kSel>
+template <int D, bool kHalf, bool kSel, bool kDiag>
 cudaError_t launch_rows(const AttnArgs& a, cudaStream_t st) {
     constexpr int smem = Ring<D>::kBytes;
-    auto* kernel = attn_rows_kernel<D, kHalf, kSel>;
+    auto* kernel = attn_rows_kernel<D, kHalf, kSel, kDiag>;
     static std::atomic<uint64_t> allowed{0};
     const cudaError_t e = allow_smem(allowed, kernel, smem);
     if (e != cudaSuccess) return e;
@@ -571,9 +615,10 @@ cudaError_t launch_rows(const AttnArgs& a, cudaStream_t st) {
 
 template <int D, bool kHalf>
 cudaError_t launch_d(const AttnArgs& a, cudaStream_t st) {
-    cudaError_t e = choose(a).tile ? launch_attn_tile(a, st)
-                    : a.sel        ? launch_rows<D, kHalf, true>(a, st)
-                                   : launch_rows<D, kHalf, false>(a, st);
+    cudaError_t e = choose(a).tile                   ? launch_attn_tile(a, st)
+                    : a.sel                          ? launch_rows<D, kHalf, true, false>(a, st)
+                    : a.causal && a.max_q_len > 1    ? launch_rows<D, kHalf, false, true>(a, st)
+                                                     : launch_rows<D, kHalf, false, false>(a, st);
     if (e != cudaSuccess || a.n_split <= 1) return e;
     const int64_t many = (int64_t)kJoinAlone * device_sm_count();
     return a.T * a.q_heads < many ? launch_join<D, kHalf, kJoinWarps>(a, st) : launch_join<D, kHalf, 1>(a, st);

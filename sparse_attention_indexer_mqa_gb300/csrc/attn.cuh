@@ -13,6 +13,12 @@
 //     out = O / l,   lse = ln 2 * (m - kShift + log2 l).
 // |Ev| <= 48, so that p' and p' * 2^-Ev can only underflow where the weight is below 2^-46 of
 // the row's largest.
+//
+// A NaN code. Of K it makes the scores of its key NaN, which a row that does not see the key drops with the
+// score. Of V it would come through the product at weight 0 too, so where a unit's rows see unlike numbers of
+// keys (the diagonal of a causal unit) V's NaN codes are taken out of the steps that some row does not see whole, the
+// lowest such key is kept, and rows that see it are NaN at the end. Everywhere else all rows see what was loaded and
+// the product does it.
 #pragma once
 
 #include <cuda_bf16.h>

@@ -70,6 +70,7 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + S::kBar);
     uint64_t *q_full = bars, *k_full = bars + 1, *v_full = bars + 2, *s_full = bars + 3, *p_full = bars + 4,
              *o_done = bars + 5, *drain = bars + 6;
+    int* nan_key = reinterpret_cast<int*>(bars + 7);  // lowest key whose V held a NaN code that was taken out
     float4* scales = reinterpret_cast<float4*>(sm + S::kScale);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
@@ -116,6 +117,7 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
         tc::mbar_init(p_full, (rows + 31) / 32);  // a warp without rows takes no part
         tc::mbar_init(o_done, 1);
         tc::mbar_init(drain, 1);
+        *nan_key = INT32_MAX;
         tc::fence_mbar_init();
     }
     __syncwarp();
@@ -323,11 +325,12 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
             ok = warp_wait<kNsIssue>(drain, 0) && ok;
         }
         // ---- the row's result -------------------------------------------------------------------------
-        if (ok && n > 0 && !idle) ok = warp_wait<kNsSoft>(o_done, (n - 1) & 1);
+        // V's barrier too, long complete: it orders nan_key
+        if (ok && n > 0 && !idle) ok = warp_wait<kNsSoft>(o_done, (n - 1) & 1) && warp_wait<kNsSoft>(v_full, (n - 1) & 1);
         if (ok && !idle) {
             tc::tc_fence_after();
             if (rc < 0.0f && l != 0.0f) l = __int_as_float(0x7fc00000);
-            store_rows<D, kHalf>(a, tm_o + lanes, n > 0, real, tok, hq, z, m, l);
+            store_rows<D, kHalf>(a, tm_o + lanes, n > 0, real, tok, hq, z, m, l, !kSel && *nan_key < vis);
         }
     } else {
         // ---- converters --------------------------------------------------------------------------------
@@ -341,6 +344,8 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
         const int32_t* pt = a.page_table + (int64_t)b * a.pt_stride;
         int64_t* offs = reinterpret_cast<int64_t*>(sm + S::kOff);
         const int vis_sel = kSel ? (int)visible_keys(s.len, s.nq, tok0 - s.t0, a.causal) : 0;
+        // keys that the tile's first row does not see though another does begin here
+        const int vis_first = kSel ? 0 : (int)visible_keys(s.len, s.nq, row0 / G, a.causal);
         uint4 rk[kPieces], rv[8];
         uint32_t my_scale = 0;  // the key's or block's two scale bytes, bit 16 set; 0: not to be used
         bool bad = false;
@@ -494,6 +499,17 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
                     for (int i = 0; i < 4; ++i) {
                         const uint2 two = *reinterpret_cast<const uint2*>(key_scales + (j & 1) * kKeysT + 8 * my.kg + 2 * i);
                         f[i] = down(v_top - (int)scale_byte(two.x >> 8)) | down(v_top - (int)scale_byte(two.y >> 8)) << 16;
+                    }
+                }
+            }
+            if constexpr (!kSel) {
+                const int end = k0 + (j + 1) * kKeysT;
+                if (end > vis_first && vis_first < kv_end) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        bool hit = clear_nan_codes(rv[i].x) | clear_nan_codes(rv[i].y);
+                        if constexpr (D == 128) hit |= clear_nan_codes(rv[i].z) | clear_nan_codes(rv[i].w);
+                        if (hit) atomicMin(nan_key, end - kKeysT + 8 * my.kg + i);
                     }
                 }
             }

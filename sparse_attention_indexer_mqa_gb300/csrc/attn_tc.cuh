@@ -164,11 +164,11 @@ __device__ __forceinline__ void issue_outputs(uint32_t tm_o, uint32_t tm_p, uint
 }
 
 // A warp's rows out of tensor memory (tm_o: the warp's lanes): the result, or the split's part of it. some: O was
-// written at all. Column 8y + x of O is dim (D/8) * x + y, so 32 columns are 4 dims of each x.
+// written at all. nan: a NaN code of V among the row's keys. Column 8y + x of O is dim (D/8) * x + y, so 32 columns are 4 dims of each x.
 template <int D, bool kHalf>
 __device__ __forceinline__ void store_rows(const AttnArgs& a, uint32_t tm_o, bool some, bool real, int64_t tok, int hq,
-                                           int z, float m, float l) {
-    const float g = a.n_split > 1 ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
+                                           int z, float m, float l, bool nan) {
+    const float g = nan ? __int_as_float(0x7fc00000) : a.n_split > 1 ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
     const int64_t pr = ((int64_t)z * a.T + tok) * a.q_heads + hq;
     uint16_t* out = a.out + tok * a.out_row_stride + (int64_t)hq * a.out_head_stride;
 #pragma unroll 1

@@ -26,6 +26,12 @@ __device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t four, uint32_t& lo, uin
         : "=r"(lo), "=r"(hi)
         : "r"(four));
 }
+// NaN codes (0x7f, 0xff) among four replaced by 0; whether there was one
+__device__ __forceinline__ bool clear_nan_codes(uint32_t& four) {
+    const uint32_t hit = ((four & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;  // 0x7f + 1 carries into bit 7
+    four &= ~((hit >> 7) * 255u);
+    return hit != 0;
+}
 // two fp32 -> two e4m3 codes (a in the low byte), nearest even, saturating
 __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float a, float b) {
     uint16_t d;

@@ -4,9 +4,76 @@ import threading
 
 import pytest
 
+import attn_ref as ref
 from test_gpu_attn import Att, Bn, torch  # noqa: F401  (fixtures and inputs)
 
 pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------------------ NaN codes
+
+def plant(a, b, pos, side, dim, head=0):
+    """A NaN code in the cache: sequence b, key pos, K (0) or V (1)."""
+    codes, _ = ref.kv_views(a.pool, a.Hkv, a.P, a.D)
+    codes[int(a.table[b, pos // a.P]), head, pos % a.P, side, dim] = 0x7F if dim % 2 else 0xFF
+
+
+NAN_SHAPES = [(8, 1, 2, 128, 64, "bfloat16"), (4, 2, 7, 64, 64, "float16"), (16, 1, 2, 64, 128, "bfloat16"),
+              (64, 1, 2, 128, 128, "float16"), (24, 2, 3, 64, 64, "bfloat16"), (8, 1, 70, 128, 64, "bfloat16"),
+              (1, 1, 150, 64, 128, "float16"), (3, 1, 300, 128, 128, "bfloat16")]
+
+
+@pytest.mark.parametrize("Hq,Hkv,nq,D,P,dt", NAN_SHAPES)
+@pytest.mark.parametrize("split", [False, True])
+def test_nan_codes_stay_with_the_rows_that_see_them(torch, Bn, Hq, Hkv, nq, D, P, dt, split):
+    """Slots that hold NaN codes before they are stored to: a causal row that does not see such a key has the
+    result of the cache without it, though the row behind it in the same tile sees it."""
+    extra = 9000 if split else 0
+    a = Att(torch, [nq + 61 + extra, nq, nq + 127 + extra, nq + 3], [nq] * 4, Hq, Hkv, D, P, getattr(torch, dt), nq + D)
+    n = a.lens
+    clean, cl = torch.zeros_like(a.out), torch.zeros_like(a.lse)
+    a.call(Bn, 1, ws=a.workspace(Bn) if split else None)
+    clean.copy_(a.out), cl.copy_(a.lse)
+    marks = [(0, n[0] - 1, 1, 5), (1, n[1] - 1, 1, D - 1), (1, n[1] - nq // 2, 1, 0), (2, n[2] - 1, 0, 7), (3, 1, 1, 33),
+             (3, n[3] - 1, 1, 2)]
+    for m in marks:
+        plant(a, *m, head=Hkv - 1)
+    a.call(Bn, 1, ws=a.workspace(Bn) if split else None)
+    G = Hq // Hkv
+    hit = torch.zeros(a.T, Hq, D, dtype=torch.bool, device="cuda")   # NaN by the definition
+    seen = torch.zeros(a.T, Hq, dtype=torch.bool, device="cuda")     # a NaN code is among the row's keys
+    hit_lse = torch.zeros(a.T, Hq, dtype=torch.bool, device="cuda")
+    for b, pos, side, dim in marks:
+        for i, v in enumerate(ref.visible(n[b], nq, 1)):
+            if v > pos:
+                hs = slice((Hkv - 1) * G, Hkv * G)
+                seen[a.cu[b] + i, hs] = True
+                if side:
+                    hit[a.cu[b] + i, hs, dim] = True
+                else:
+                    hit[a.cu[b] + i, hs] = hit_lse[a.cu[b] + i, hs] = True
+    assert int(a.status) == 0
+    assert torch.equal(a.out[~seen], clean[~seen]) and torch.equal(a.lse[~hit_lse], cl[~hit_lse])
+    assert torch.isnan(a.out[hit]).all() and torch.isnan(a.lse[hit_lse]).all()
+    # the other dims of a row that sees a NaN code of V: NaN, or what they are without it
+    left = seen[..., None] & ~hit & ~torch.isnan(a.out)
+    assert torch.equal(a.out[left], clean[left])
+
+
+@pytest.mark.parametrize("Hq", [8, 64])
+def test_nan_codes_behind_every_row(torch, Bn, Hq):
+    """Not causal, every row sees the same keys: a NaN code of V is NaN in its dim alone."""
+    a = Att(torch, [70, 200], [2, 2], Hq, 1, 128, 64, torch.bfloat16)
+    a.call(Bn, 0)
+    clean = a.out.clone()
+    plant(a, 0, 69, 1, 9)
+    plant(a, 1, 3, 1, 10)
+    a.call(Bn, 0)
+    want = clean.clone()
+    want[:2, :, 9] = math.nan
+    want[2:, :, 10] = math.nan
+    assert torch.equal(a.out.isnan(), want.isnan())
+    assert torch.equal(a.out.nan_to_num(), want.nan_to_num())
 
 
 # ------------------------------------------------------------------------------ rows without keys
