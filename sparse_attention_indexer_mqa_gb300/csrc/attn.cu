@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attn_rows_kernel(const AttnArg
     __shared__ int nan_key[kDiag ? kWarps : 1];  // lowest key whose V held a NaN code that was taken out
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, c = lane & 3;
     pdl_wait();
-    pdl_launch_dependents();
+    if (a.n_split > 1) pdl_launch_dependents();  // the join
 
     // ---- the unit: sequence, rows, keys --------------------------------------------------------
     const int G = a.group, head = blockIdx.y, z = blockIdx.z;
@@ -508,6 +508,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attn_rows_kernel(const AttnArg
 // take splits in turn where rows are few, so that their loads are in flight together, and sum in
 // shared memory (64 rows of 38 splits: 33 us with the attention against 39); enough rows to fill the GPU
 // take a warp each (4096 rows of 4 splits: 184 against 188 us with the attention, 32768 of 2: 56 against 80).
+// The call's last kernel, this one or a sole attention kernel, lets nothing start beside it: out may be what the
+// next call reads before its wait (q or k of the pre-processing).
 constexpr int kJoinWarps = 4;
 constexpr int kJoinAlone = 8;  // rows per SM from which a warp joins one
 template <int D, bool kHalf, int kPerRow>
@@ -518,7 +520,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const AttnAr
     const int64_t row = (int64_t)blockIdx.x * (kJoinWarps / kPerRow) + warp / kPerRow, t = row / a.q_heads;
     const int hq = (int)(row % a.q_heads);
     pdl_wait();
-    pdl_launch_dependents();
     if (row >= step) return;  // a whole warp, with kPerRow = kJoinWarps never
     const int b = warp_seq_of_query(a, t);
     if (b < 0 || seq_rows(a, b).nq < 0) return;  // the same for all warps of a row

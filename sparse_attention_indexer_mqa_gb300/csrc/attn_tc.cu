@@ -105,10 +105,7 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
         rows = 0;
     }
     // uniform: nothing has been allocated yet
-    if (rows <= 0) {
-        pdl_launch_dependents();
-        return;
-    }
+    if (rows <= 0) return;
     if (tid == 0) {
         tc::mbar_init(q_full, kRowsT);
         tc::mbar_init(k_full, 128);
@@ -128,7 +125,7 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
-    pdl_launch_dependents();  // with the tensor memory in hand: a dependent may allocate its own
+    if (a.n_split > 1) pdl_launch_dependents();  // the join
     const uint32_t tm_s = tmem_slot, tm_o = tm_s + 128;
     const int k0 = z * a.chunk, k1 = min(kv_end, k0 + a.chunk);
     const int n = k1 > k0 ? (k1 - k0 + kKeysT - 1) / kKeysT : 0;

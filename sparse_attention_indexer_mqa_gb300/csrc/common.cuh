@@ -35,7 +35,8 @@ __device__ __forceinline__ void report(int32_t* status, int32_t bit) {
 // dependent launches (no dependent can hold the resources a CTA of it still needs), and a
 // kernel's pdl_wait() returning means its predecessor, and everything that one waited for,
 // has completed. idx_step_meta, which writes what the others read before they wait, ends with a
-// kernel that only waits (meta.cu).
+// kernel that only waits (meta.cu), and the attention's last kernel, whose output may be such a bf16
+// input, never issues pdl_launch_dependents(): its dependent starts when it has completed.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -246,3 +246,36 @@ def test_two_streams_in_turns(torch, Bn):
     torch.cuda.synchronize()
     for (_, _, outs, _), want in zip(both, alone):
         assert all(torch.equal(x, y) for x, y in zip(outs, want))
+
+
+@pytest.mark.parametrize("nq,Hq,keys", [(2000, 8, 2000), (1, 8, 30000), (1, 64, 30000), (40, 1, 9000), (1, 16, 500)])
+@pytest.mark.parametrize("split", [False, True])
+def test_output_as_the_next_calls_query(torch, Bn, nq, Hq, keys, split):
+    """The Q quantisation reads q before it waits for the kernel in front of it: here the attention's output."""
+    a = Att(torch, [keys, keys - 7], [nq, nq], Hq, 1, 128, 128, torch.bfloat16)
+    ws = a.workspace(Bn) if split else None
+    w = torch.ones(a.T, Hq, device="cuda")
+    outs = [(torch.zeros(a.T, Hq + -Hq % 8, 64, dtype=torch.uint8, device="cuda"),
+             torch.zeros(a.T, 512, dtype=torch.uint8, device="cuda"), torch.zeros_like(w)) for _ in range(8)]
+    other = torch.randn(a.q.shape, device="cuda").bfloat16()
+    qs = [a.q, other]
+
+    def quant(o):
+        Bn.idx_q_quant(a.out.view(torch.int16), None, None, Bn.IDX_ROPE_NONE, w, 1.0, 1.0, Bn.IDX_MXFP4, *o)
+    want = []
+    for i in range(2):
+        a.q = qs[i]
+        a.call(Bn, 1, ws=ws)
+        torch.cuda.synchronize()
+        o = tuple(torch.zeros_like(x) for x in outs[0])
+        quant(o)
+        torch.cuda.synchronize()
+        want.append(o)
+    assert not torch.equal(want[0][0], want[1][0])
+    for i, o in enumerate(outs):
+        a.q = qs[i % 2]
+        a.call(Bn, 1, ws=ws)
+        quant(o)
+    torch.cuda.synchronize()
+    for i, o in enumerate(outs):
+        assert all(torch.equal(x, y) for x, y in zip(o, want[i % 2])), i
