@@ -369,10 +369,11 @@ int idx_debug_mma_rate(int32_t dtype, int32_t iters, int32_t* dev_status, double
                        cudaStream_t stream);
 
 /*
- * Test hook for the bounded waits: one CTA whose thread waits, with the wait helper every
- * kernel of the library uses, for an mbarrier phase that nothing completes, gives up after
- * limit_us microseconds (1 .. 1000000) of global time, sets IDX_STATUS_TIMEOUT in *dev_status
- * and returns; the context stays usable. *dev_status: a device int32 (required).
+ * Test hook for the bounded waits: one CTA whose thread waits, with each of the two wait helpers
+ * that the library's kernels use in turn, for an mbarrier phase that nothing completes, gives up
+ * after limit_us microseconds (1 .. 1000000; the second helper: limit_us / 4 tests of 1 to 4 us) each, sets
+ * IDX_STATUS_TIMEOUT in *dev_status if it gave up both times, and returns; the context stays usable. The
+ * kernels' own limit is 1000000. *dev_status: a device int32 (required).
  */
 int idx_debug_wait_timeout(int32_t limit_us, int32_t* dev_status, cudaStream_t stream);
 

@@ -69,14 +69,16 @@ __global__ void __launch_bounds__(128, 1) mma_rate_kernel(int iters, int32_t* st
 }
 
 // One thread waits for phase 0 of an mbarrier whose arrival count is never reached (nothing
-// arrives on it), gives up at the deadline and reports the timeout.
+// arrives on it), gives up at the deadline and reports the timeout; first with the indexer kernels' helper, then with the
+// attention kernels', which counts tests of 1 to 4 us.
 __global__ void wait_timeout_kernel(int64_t limit_ns, int32_t* status) {
     __shared__ uint64_t bar;
     if (threadIdx.x != 0) return;
     tc::mbar_init(&bar, 1);
     tc::fence_mbar_init();
     const uint64_t deadline = tc::global_ns() + (uint64_t)limit_ns;
-    if (!tc::mbar_wait_until(&bar, 0, deadline)) report(status, IDX_STATUS_TIMEOUT);
+    const bool first = tc::mbar_wait_until(&bar, 0, deadline);
+    if (!tc::mbar_spin<0>(&bar, 0, (uint32_t)(limit_ns / 4000)) && !first) report(status, IDX_STATUS_TIMEOUT);
 }
 
 }  // namespace

@@ -59,14 +59,14 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
     }
 }
 
-// The same, bounded by a number of tests (each takes tens of cycles: seconds in all) instead of the
-// global timer. kNs > 0: sleeps that long between tests. A warp that tests without a pause takes
-// shared-memory cycles from the tensor core's operand reads.
-constexpr uint32_t kWaitTests = 1u << 24;
+// The same, bounded by a number of tests, for kernels without a register to spare for the clock (with one, the attention's
+// 8192-token prompt took 663 us instead of 608). A test that fails suspends its thread for 1 to 4.1 us
+// (measured), so that the limit is a second at most. kNs > 0: sleeps that long between tests.
+constexpr uint32_t kWaitTests = 250000;
 template <int kNs>
-__device__ __forceinline__ bool mbar_spin(uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ bool mbar_spin(uint64_t* bar, uint32_t parity, uint32_t tests = kWaitTests) {
 #pragma unroll 1
-    for (uint32_t i = 0; i < kWaitTests; ++i) {
+    for (uint32_t i = 0; i < tests; ++i) {
         if (mbar_try_wait(bar, parity)) return true;
         if (kNs > 0) __nanosleep(kNs);
     }

@@ -1,6 +1,7 @@
 """Calls of the step metadata and the paged attention at the borders of what include/idx.h allows, on the GPU."""
 import math
 import threading
+import time
 
 import pytest
 
@@ -279,3 +280,19 @@ def test_output_as_the_next_calls_query(torch, Bn, nq, Hq, keys, split):
     torch.cuda.synchronize()
     for i, o in enumerate(outs):
         assert all(torch.equal(x, y) for x, y in zip(o, want[i % 2])), i
+
+
+def test_attention_waits_give_up_in_time(torch, Bn):
+    """Both wait helpers at the kernels' own limit of a second each, on a barrier that nothing completes; an attention
+    call right after runs."""
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    t0 = time.perf_counter()
+    Bn.idx_debug_wait_timeout(1000000, status)
+    torch.cuda.synchronize()
+    took = time.perf_counter() - t0
+    assert int(status) == Bn.IDX_STATUS_TIMEOUT
+    assert 1.2 < took < 2.6  # 1 s by the clock, then 250000 tests of 1 to 4.1 us
+    a = Att(torch, [200, 100], [3, 2], 64, 1, 128, 64, torch.bfloat16)
+    a.call(Bn, 1)
+    a.check(1)
