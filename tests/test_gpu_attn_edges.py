@@ -6,7 +6,7 @@ import time
 import pytest
 
 import attn_ref as ref
-from test_gpu_attn import Att, Bn, torch  # noqa: F401  (fixtures and inputs)
+from test_gpu_attn import Att, Bn, empty_pool, make_rows, run_meta, run_store, torch  # noqa: F401  (fixtures, inputs)
 
 pytestmark = pytest.mark.gpu
 
@@ -111,6 +111,124 @@ def test_non_finite_query_on_pages_outside_the_pool(torch, Bn, Hq, nq):
     assert a.out[nq:, 1].isnan().all() and a.out[nq:, 0].isfinite().all()
 
 
+# ------------------------------------------------------------------------------ long lists
+
+def graded(torch, a):
+    """K and V scales of a's blocks over 17 exponents, the same in every head; the exponents by position."""
+    _, scales = ref.kv_views(a.pool, a.Hkv, a.P, a.D)
+    grade = []
+    for b, n in enumerate(a.lens):
+        block = torch.arange(-(-n // 16), device="cuda")
+        g = block % 17
+        page = a.table[b, block * 16 // a.P].long()
+        e = torch.stack([104 + g, 122 - g], -1).to(torch.uint8)
+        scales[page, :, block * 16 % a.P // 16] = e[:, None]
+        grade.append(g.repeat_interleave(16)[:n].cpu())
+    return grade
+
+
+def stepped(torch, a, k, seed):
+    """Lists whose steps of 128 entries are of unlike kinds: scales all alike, 2^15 apart (the most that is folded
+    into the operands), 2^16 apart, with one entry that does not count, of such entries alone, random."""
+    grade = graded(torch, a)
+    g = torch.Generator().manual_seed(seed)
+    sel = torch.full((a.T, k), -1, dtype=torch.int32)
+
+    def some(ids, count):
+        return ids[torch.randint(len(ids), (count,), generator=g)]
+    for b, n in enumerate(a.lens):
+        at = torch.arange(n)
+        kinds = [lambda c: some(at[grade[b] == 4], c), lambda c: some(at[grade[b] <= 15], c),
+                 lambda c: some(at, c), lambda c: some(at[grade[b] <= 1], c),
+                 lambda c: torch.full((c,), n), lambda c: some(at[grade[b] > 0], c)]
+        for t in range(a.cu[b], a.cu[b + 1]):
+            for i, start in enumerate(range(0, k, 128)):
+                count = min(128, k - start)
+                part = kinds[(i + t) % len(kinds)](count)
+                if (i + t) % len(kinds) == 3:
+                    part[int(torch.randint(count, (1,), generator=g))] = -1
+                sel[t, start:start + count] = part.int()
+    return sel.cuda()
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,dt", [(8, 1, 128, "bfloat16"), (16, 1, 64, "float16"), (64, 1, 128, "float16"),
+                                         (130, 1, 64, "bfloat16"), (40, 2, 128, "bfloat16"), (34, 2, 128, "float16")])
+@pytest.mark.parametrize("k", [1024, 2048, 1500])
+@pytest.mark.parametrize("split", [False, True])
+def test_long_lists(torch, Bn, Hq, Hkv, D, dt, k, split):
+    """Lists of many steps, split and joined or whole, folded steps and others in one row; full lists of distinct keys
+    and lists of steps of unlike kinds."""
+    a = Att(torch, [5000, 2100, 3333], [1, 2, 1], Hq, Hkv, D, 64, getattr(torch, dt), k + Hq)
+    g = torch.Generator().manual_seed(k)
+    full = torch.stack([torch.randperm(2100, generator=g)[:k] for _ in range(a.T)]).int()
+    full = torch.nn.functional.pad(full, (0, k - full.shape[1]), value=-1).cuda()
+    ws = a.workspace(Bn, k) if split else None
+    if split:
+        assert ws.numel() > 256
+    a.call(Bn, 0, full, ws)
+    a.check(0, full)
+    sel = stepped(torch, a, k, k + Hq)
+    a.scale = 2.0 ** -4 / D
+    a.out.fill_(77), a.lse.fill_(77)
+    a.call(Bn, 0, sel, ws)
+    a.check(0, sel)
+
+
+# ------------------------------------------------------------------------------ batches of unlike requests
+
+@pytest.mark.parametrize("Hq,Hkv,D,dt", [(8, 1, 128, "bfloat16"), (16, 2, 64, "float16"), (64, 1, 128, "float16"),
+                                         (1, 1, 64, "bfloat16"), (32, 8, 128, "bfloat16")])
+@pytest.mark.parametrize("split", [False, True])
+def test_decodes_beside_a_chunk(torch, Bn, Hq, Hkv, D, dt, split):
+    """Single tokens on caches of unlike lengths, a chunk of a prompt, requests without tokens, in one call."""
+    nq = [1] * 20 + [0, 170, 0] + [1] * 13 + [3]
+    lens = [1 + 97 * i for i in range(20)] + [40, 1234, 0] + [2000 + 31 * i for i in range(13)] + [3]
+    a = Att(torch, lens, nq, Hq, Hkv, D, 128, getattr(torch, dt), Hq, pad=5)
+    a.call(Bn, 1, ws=a.workspace(Bn) if split else None)
+    a.check(1)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(2, 2), (40, 1), (6, 3)])
+def test_many_short_requests(torch, Bn, Hq, Hkv):
+    a = Att(torch, [1 + (i * 37) % 150 for i in range(500)], [1] * 500, Hq, Hkv, 64, 64, torch.float16, Hq, pad=1)
+    a.call(Bn, 1, ws=a.workspace(Bn))
+    a.check(1)
+
+
+# ------------------------------------------------------------------------------ stores of many rows
+
+@pytest.mark.parametrize("H,D,P,dt", [(1, 64, 64, "float16"), (5, 128, 128, "bfloat16")])
+@pytest.mark.parametrize("case", ["prompt", "tokens", "gaps", "flagged"])
+def test_store_many_rows(torch, Bn, H, D, P, dt, case):
+    """1024 rows and more, of which a CTA looks at 16: runs that cross its rows, single tokens of many requests, rows
+    that are skipped or refused at its borders."""
+    n, status = 1300, 0
+    perm = torch.randperm(1400, generator=torch.Generator().manual_seed(3)).tolist()
+    if case == "prompt":      # two prompts that begin inside a block
+        slots = list(range(5, 705))
+        first = (705 // P + 1) * P
+        slots += [first + 9 + i for i in range(n - 700)]
+        pages = slots[-1] // P + 1
+    elif case == "tokens":    # one token of each of 1300 requests, at any offset of a block of its own
+        slots = [16 * b + b % 16 for b in perm[:n]]
+        pages = 1400 * 16 // P + 1
+    else:
+        slots = list(range(3, 3 + n))
+        pages = n // P + 2
+        if case == "gaps":    # whole blocks left out, among them some at the borders of 16 rows
+            slots = [-1 if s // 16 % 5 == 2 else s for s in slots]
+        else:
+            status = 1
+            for r in (16, 32, 47, 255, 256, 1299):   # a slot twice: it and the block's rows behind it are skipped
+                slots[r] = slots[r - 1]
+            slots[600] = pages * P                   # past the pool
+            for r in range(601, 603 + 16):           # the rest of that row's block: apart from its first rows
+                if slots[r] // 16 == slots[599] // 16:
+                    slots[r] = -1
+    pool = empty_pool(torch, pages, H, D, P, 5)
+    run_store(torch, Bn, pool, make_rows(torch, n, H, D, getattr(torch, dt), 6), slots, P, status)
+
+
 # ------------------------------------------------------------------------------ step metadata
 
 def decode_step(torch, Bn, B, T_extra=0, seed=0):
@@ -159,6 +277,16 @@ def test_meta_of_unlike_batches_from_threads(torch, Bn):
     for x in threads:
         x.join()
     assert not errors, errors
+
+
+@pytest.mark.parametrize("new,P", [([60000], 64), ([1, 0, 33333, 5], 128), ([0, 1, 20000, 20000], 64)])
+def test_meta_of_long_prompts(torch, Bn, new, P):
+    """Hundreds of pages to a request, on shuffled pages, beside single tokens."""
+    ctx = [(7 * i) % 130 for i in range(len(new))]
+    longest = max(x + y for x, y in zip(ctx, new))
+    need = sum(-(-(x + y) // P) - -(-x // P) for x, y in zip(ctx, new))
+    free = torch.randperm(need + 50, generator=torch.Generator().manual_seed(1)).tolist()
+    run_meta(torch, Bn, ctx, new, P, longest, free, [2, 2 + need], need + 50, sum(new) + 3, -(-longest // P) + 1, 1, 0)
 
 
 @pytest.mark.parametrize("between", ["nothing", "capture", "refused", "names"])
