@@ -343,6 +343,15 @@ def _ftype(fn, x):
     raise ValueError(f"{fn}: {x.dtype} is neither bfloat16 nor float16")
 
 
+def _status(fn, x, dev):
+    """The status word's pointer (the kernels write to it), from a tensor or as a number."""
+    if x is None or isinstance(x, int):
+        return x
+    if x.dtype is not _torch.int32 or x.get_device() != dev or x.numel() < 1:
+        _refuse(fn, "dev_status", x, _torch.int32, 1, False)
+    return x.data_ptr()
+
+
 def idx_step_meta(ctx_lens, q_lens, page_table, page_size, max_seq_len_k, free_pages, free_span, num_pages,
                   cu_seqlens_q, seq_lens_k, positions, slot_mapping, free_next, dev_status=None,
                   stream=None):
@@ -366,7 +375,7 @@ def idx_step_meta(ctx_lens, q_lens, page_table, page_size, max_seq_len_k, free_p
         ctx_lens.data_ptr(), q_lens.data_ptr(), B, page_table.data_ptr(), width, page_size, max_seq_len_k,
         free_pages.data_ptr(), free_pages.numel(), free_span.data_ptr(), num_pages, cu_seqlens_q.data_ptr(),
         seq_lens_k.data_ptr(), positions.data_ptr(), slot_mapping.data_ptr(), T, free_next.data_ptr(),
-        _ptr(dev_status), _stream(stream))
+        _status(fn, dev_status, dev), _stream(stream))
     if st:
         _check(fn, st)
 
@@ -414,7 +423,7 @@ def idx_kv_store(k, v, slot_mapping, pool, num_pages, page_size, page_stride, de
     _pool_bytes(fn, pool, num_pages, page_stride, H * (2 * page_size * D + 16), dev)
     st = (_lib or load()).idx_kv_store(
         k.data_ptr(), v.data_ptr(), ft, n, H, D, kr, kh, vr, vh, slot_mapping.data_ptr(), pool.data_ptr(), num_pages,
-        page_size, page_stride, _ptr(dev_status), _stream(stream))
+        page_size, page_stride, _status(fn, dev_status, dev), _stream(stream))
     if st:
         _check(fn, st)
 
@@ -483,6 +492,6 @@ def idx_attn_paged(q, pool, num_pages, page_size, page_stride, kv_heads, page_ta
         q.data_ptr(), ft, T, H, kv_heads, D, qr, qh, pool.data_ptr(), num_pages, page_size, page_stride,
         page_table.data_ptr(), width, seq_lens_k.data_ptr(), cu_seqlens_q.data_ptr(), B, 1 if causal else 0, max_q_len,
         max_seq_len_k, sel_p, sel_stride, n_sel, softmax_scale, out.data_ptr(), orow, oh, lse_p, ws_p, wsb,
-        _ptr(dev_status), _stream(stream))
+        _status(fn, dev_status, dev), _stream(stream))
     if st:
         _check(fn, st)

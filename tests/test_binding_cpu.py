@@ -93,3 +93,38 @@ def test_workspace_without_memory_of_its_own_is_refused(calls):
         with pytest.raises(ValueError, match="workspace"):
             attend(workspace=ws)
     assert len(calls) == 1
+
+
+class Elsewhere:
+    """An int32 that is not on the current device (a host tensor, as the fixture has it)."""
+    dtype, device, shape, nbytes = torch.int32, "elsewhere", (1,), 4
+    is_contiguous = lambda self: True
+    get_device = lambda self: 3
+    numel = dim = lambda self: 1
+    stride = lambda self: (1,)
+    data_ptr = lambda self: 4096
+
+
+def meta(**kw):
+    z = lambda n, dt=torch.int32: torch.zeros(n, dtype=dt)
+    Bn.idx_step_meta(z(1), z(1), z(2).view(1, 2), 64, 128, z(4), z(2), 8, z(2), z(1), z(3), z(3, torch.int64), z(1), stream=0,
+                     **kw)
+
+
+def store_one(**kw):
+    k = torch.zeros(1, 1, 64, dtype=torch.float16)
+    Bn.idx_kv_store(k, k.clone(), torch.zeros(1, dtype=torch.int64), torch.zeros(PAGE, dtype=torch.uint8), 1, 64, PAGE,
+                    stream=0, **kw)
+
+
+@pytest.mark.parametrize("use", [meta, store_one, attend])
+def test_status_word_has_to_be_on_the_device(calls, use):
+    """The kernels write to it: a pointer that is not the device's would fault there."""
+    word = torch.zeros(1, dtype=torch.int32)
+    for status in (word, word.data_ptr(), None):
+        use(dev_status=status)
+    assert [args[-2] for _, args in calls] == [word.data_ptr(), word.data_ptr(), None]
+    for bad in (Elsewhere(), torch.zeros(1, dtype=torch.int64), torch.zeros(1), torch.zeros(0, dtype=torch.int32)):
+        with pytest.raises(ValueError, match="dev_status"):
+            use(dev_status=bad)
+    assert len(calls) == 3
