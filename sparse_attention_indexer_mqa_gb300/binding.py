@@ -347,9 +347,10 @@ def _status(fn, x, dev):
     """The status word's pointer (the kernels write to it), from a tensor or as a number."""
     if x is None or isinstance(x, int):
         return x
-    if x.dtype is not _torch.int32 or x.get_device() != dev or x.numel() < 1:
+    p = x.data_ptr()
+    if x.dtype is not _torch.int32 or x.get_device() != dev or not p:  # null: no elements
         _refuse(fn, "dev_status", x, _torch.int32, 1, False)
-    return x.data_ptr()
+    return p
 
 
 def idx_step_meta(ctx_lens, q_lens, page_table, page_size, max_seq_len_k, free_pages, free_span, num_pages,
