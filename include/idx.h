@@ -486,8 +486,11 @@ int idx_kv_store(const void* k, const void* v, int32_t ftype, int64_t n_rows, in
  *   cache holds in slots that a row does not see (NaN codes too) does not reach it. A NaN code that a row does see
  *   (idx_kv_store writes none) gives NaN: one of K in all of out and in lse, one of V in its dim of out at least.
  * Arithmetic: q is scaled by a power of two per row and held in fp16 (exact for fp16 and, but for
- *   values below 2^-28 of the row's largest, for bf16), products and sums in fp32; the softmax
- *   weights are rounded to fp16 (2^-11 relative, half a step) for the product with v.
+ *   values below 2^-28 of the row's largest, for bf16), products and sums in fp32. For the product with v the
+ *   softmax weights, times their V block's 2^E, are rounded to fp16: 2^-11 relative (half a step) down to 2^-21 of the
+ *   row's largest such product, below that an absolute 2^-32 of it. lse does not have that rounding. Scores, and
+ *   softmax_scale * log2(e) * 2^E of a K block (for bf16 q also times 2^-14 of the row's largest |q|), have to stay
+ *   within fp32's range.
  * workspace: optional device memory, 256-byte aligned, no starting value needed: partial results of a key axis
  *   that is split over CTAs when the rows alone do not fill the GPU. idx_attn_workspace_bytes
  *   gives the size that the splitting would like; with less (or NULL) it splits less. One

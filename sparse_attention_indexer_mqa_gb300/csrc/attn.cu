@@ -13,11 +13,11 @@
 //   O = P V: S's accumulator is P's A operand as it stands: rows r, r + 8, keys 2c, 2c+1, 8+2c,
 //     9+2c. The thread holds those four keys' dims r*D/8 .. and pairs their bytes by prmt;
 //     column n of step j is dim n*D/8 + j, so a thread ends with D/4 consecutive dims of a row.
-// Measured (bf16): 64 sequences of 8192 keys, 64 heads over 8, D = 128: 183 us, 5.9 TB/s of cache, 87 % of
-// the measured copy rate (236 us with lanes' pieces of 16 bytes scattered over lines); two of 131071
-// keys, 32 heads over 4, D = 64: 32 us with the join, 4.2 TB/s. Eleven warps on an SM, each a chain of
-// loads, 64 mma.sync, two shuffles, exponentials and 64 mma.sync a step, do not hide all of it: DRAM
-// 62 %, issue 39 % busy.
+// Measured in replayed graphs (bf16): 64 sequences of 8192 keys, 64 heads over 8, D = 128: 181 us, 5.9 TB/s of cache,
+// 88 % of the measured copy rate (236 us with lanes' pieces of 16 bytes scattered over lines); two of 131071
+// keys, 32 heads over 4, D = 64: 32 us with the join, 4.2 TB/s; one of 256 keys, 8 heads over one: 6.5 us, 11 to 12 with
+// the host's call. Eleven warps on an SM, each a chain of loads, 64 mma.sync, two shuffles, exponentials and 64
+// mma.sync a step, do not hide all of it: DRAM 65 %, issue 40 % busy.
 #include "attn.cuh"
 
 namespace idx {
@@ -506,8 +506,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attn_rows_kernel(const AttnArg
 
 // Joins the splits of a key axis. A (query row, head) is joined by kPerRow of a CTA's four warps: all four
 // take splits in turn where rows are few, so that their loads are in flight together, and sum in
-// shared memory (64 rows of 38 splits: 33 us with the attention against 39); enough rows to fill the GPU
-// take a warp each (4096 rows of 4 splits: 184 against 188 us with the attention, 32768 of 2: 56 against 80).
+// shared memory (64 rows of 38 splits: 32 us with the attention against 39); enough rows to fill the GPU
+// take a warp each (4096 rows of 4 splits: 180 against 182 us with the attention, 32768 of 2: 56 against 78).
 // The call's last kernel, this one or a sole attention kernel, lets nothing start beside it: out may be what the
 // next call reads before its wait (q or k of the pre-processing).
 constexpr int kJoinWarps = 4;
@@ -586,10 +586,10 @@ cudaError_t launch_join(const AttnArgs& a, cudaStream_t st) {
 // Rows that share their keys: those of a sequence and a kv head, or with a list those of a query's group.
 int64_t shared_rows(const AttnArgs& a) { return a.n_sel ? a.group : (int64_t)a.max_q_len * a.group; }
 
-// Which kernel. Dense: up to two mma.sync tiles of shared rows this file's (32 heads over one kv head,
-// 64 x 8192 keys: 60 us against 64; 3000 keys of one sequence: 10.1 against 14.5), more the
-// tensor-memory one (64 heads: 74 against 96, with one join for both that takes a CTA per row). Lists, whose keys are gathered for each tile: up to one (32 heads,
-// 4096 queries x 1024 keys: 434 us in two tiles, 386 in tensor memory).
+// Which kernel. Dense: up to two mma.sync tiles of shared rows this file's (32 heads over one kv head, 3000 keys of
+// one sequence: 10.1 us against 14.8; 64 x 8192 keys: 59 against 58), more the tensor-memory one (64 heads, 64 x 8192
+// keys: 62 against 93). Lists, whose keys are gathered for each tile: up to one (4096 queries x 1024 keys, 16 heads:
+// 207 us against 380; 32 heads in two tiles 413 against 389).
 struct Choice {
     bool tile;
     int64_t units;
@@ -636,17 +636,17 @@ int64_t attn_plan(AttnArgs& a, int64_t bytes) {
     const int64_t per_split = a.T * a.q_heads * (a.head_dim + 2) * 4;
     // Splits. Units that fill the resident CTAs (three or two to an SM) by themselves are cut until there are
     // about four rounds of them, in pieces of 1024 keys at least (64 sequences of 8192 keys, 8
-    // kv heads: 202 / 190 / 184 / 191 us with 1 / 2 / 4 / 7 splits); fewer units are cut until they fill one
-    // round, in pieces of 512 keys at least (two sequences of 131071 keys, 4 kv heads: 36 / 32 / 31
-    // / 43 us with 32 / 38 / 57 / 64, the last one round and a bit), or of 256 where those are fewer
-    // than the SMs (one sequence of 4000 keys: 20.7 / 13.6 / 10.6 / 9.2 us with 2 / 4 / 8 / 16).
+    // kv heads: 205 / 180 / 180 / 186 us with 1 / 2 / 4 / 7 splits); fewer units are cut until they fill one
+    // round, in pieces of 512 keys at least (two sequences of 131071 keys, 4 kv heads: 35 / 32 / 32
+    // / 44 us with 32 / 38 / 57 / 64, the last one round and a bit), or of 256 where those are fewer
+    // than the SMs (one sequence of 4000 keys: 20.3 / 13.9 / 10.4 / 8.9 us with 2 / 4 / 8 / 16).
     // The tensor-memory kernel's units hold up to 128 rows, whose partial results cost more than a
-    // second round: they are cut to fill one (64 x 8192 keys, 64 heads over 1: 75 / 73 / 63 / 71 us with 2 /
-    // 3 / 4 / 8; 512 queries on 8192 keys: 133 / 107 / 118 with 1 / 2 / 4) and not at all where
-    // they do by themselves (prompts of 1024 and 2048: 34 and 81 us whole, 56 and 116 in 2). max_q_len only
+    // second round: they are cut to fill one (64 x 8192 keys, 64 heads over 1: 75 / 73 / 62 / 72 us with 2 /
+    // 3 / 4 / 8; 512 queries on 8192 keys: 124 / 99 / 112 with 1 / 2 / 4) and not at all where
+    // they do by themselves (prompts of 1024 and 2048: 34 and 80 us whole, 56 and 114 in 2). max_q_len only
     // bounds the number of queries, so the units that have rows are counted from T; where chunks are
-    // uneven they are cut to fill three rounds (8 of 3 to 301 queries on up to 3300 keys: 48 / 32 / 27 /
-    // 24 / 29 us with 1 / 2 / 4 / 6 / 8).
+    // uneven they are cut to fill three rounds (8 of 3 to 301 queries on up to 3300 keys: 48 / 31 / 27 /
+    // 24 / 29 us with 1 / 2 / 4 / 6 / 8; no other batch of uneven chunks was measured).
     const int64_t slots = (int64_t)sms * choice.per_sm;
     int64_t want = 1;
     if (units > 0) {

@@ -8,11 +8,12 @@
 // scaled element by element. m follows the largest u; it is raised only when a u passes it by more than
 // kLazy, since raising it means rescaling O and l (with 3 some row of a warp's 32 was raised in every
 // second step of 128 keys, by the counter of O's loads in a 4096-token prompt; with 8 in few). p' <=
-// 2^(kShift + kLazy) = 2^15 stays in fp16's range; weights down to 2^-21 of the largest keep fp16's full
-// 11 bits, and below that an absolute 2^-32 of it.
+// 2^(kShift + kLazy) = 2^15 stays in fp16's range. What is rounded to fp16 is the weight times 2^Ev: down to 2^-21 of
+// the row's largest such product it keeps fp16's full 11 bits, below that an absolute 2^-32 of it (so a key of large
+// weight in a block of small V can lose its V beside a block of large V).
 //     out = O / l,   lse = ln 2 * (m - kShift + log2 l).
-// |Ev| <= 48, so that p' and p' * 2^-Ev can only underflow where the weight is below 2^-46 of
-// the row's largest.
+// -32 <= Ev <= 48, so that in fp32, in which l is summed, p' and p' * 2^-Ev can only underflow where the weight is
+// below 2^-46 of the row's largest.
 //
 // A NaN code. Of K it makes the scores of its key NaN, which a row that does not see the key drops with the
 // score. Of V it would come through the product at weight 0 too, so where a unit's rows see unlike numbers of

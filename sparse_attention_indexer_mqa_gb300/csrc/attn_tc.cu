@@ -8,7 +8,7 @@
 // operand from there. Roles of a CTA's two warpgroups:
 //   0  softmax: thread = row. Q to shared memory at the start, S -> P per tile, O out at the end; warp
 //      0 issues the MMAs, which it would wait for anyway (in a converter warp each step waited for that
-//      warp's other work, 674 us for a causal prompt of 8192 tokens, 32 heads over 8, against 630; in a
+//      warp's other work, 674 us for a causal prompt of 8192 tokens, 32 heads over 8, against 630 then; in a
 //      warp of its own every thread had a quarter fewer registers and spilled, 898 us);
 //   1  converters: e4m3 from memory to fp16 operand tiles in shared memory (exact). The loads of a
 //      tile go out one tile ahead into registers, so any row order costs the same: pages and
@@ -19,7 +19,7 @@
 // (tensor memory 2 x 256 columns, shared memory 2 x 107 KB): one's products run under the other's
 // softmax.
 //
-// What bounds it. That prompt takes 622 us, 884 TFLOP/s of its visible pairs (46 % of a large bf16 product's measured
+// What bounds it. That prompt takes 609 us, 903 TFLOP/s of its visible pairs (47 % of a large bf16 product's measured
 // rate). Eight MMAs of 128 x 128 x 16 take 736 cycles (both operands in shared memory) or 679
 // (P in tensor memory) with nothing else on the SM, so a step needs 1415 cycles of the tensor pipe;
 // a CTA's step takes 4400: S 740, softmax 1950, O += P V 700, and 200 to 500 from each to
@@ -27,8 +27,8 @@
 // an N = 64 MMA takes as long as an N = 128 one: 600 us, and 548 with lists, which were at 443 then),
 // with K's and V's converters apart (645, 518); two tiles to a CTA that share converted K and V (698, and
 // 685 with the tiles' MMAs in turn); the softmax in one pass over S with P kept in registers
-// (665). With lists (4096 queries x 1024 keys, 64 heads over 1: 453 us) half of a tile's rows are
-// empty and a unit is only eight steps long; the order of the keys hardly matters (441 in order, 448 at random).
+// (665). With lists (4096 queries x 1024 keys, 64 heads over 1: 450 us) half of a tile's rows are
+// empty and a unit is only eight steps long; the order of the keys hardly matters (447 in order, 453 at random).
 #include "attn_tc.cuh"
 
 namespace idx {

@@ -10,8 +10,9 @@
 // One warp owns what a call writes into one block of one head: a run of at most 16 adjacent rows.
 // It holds them in registers (16-byte loads, 16 or 8 lanes a row), so that the rows are read
 // once: maximum, scale, codes.
-// Measured (bf16, 8 heads, D = 128): 8192 rows of a prompt 11.1 us, 4.5 TB/s of rows read and codes written (floor 7.4 us at
-// the measured copy rate); 64 single rows 3.3 us, launch and one chain of loads.
+// Measured in replayed graphs (bf16, 8 heads, D = 128): 8192 rows of a prompt 11.2 us, 4.5 TB/s of rows read and codes
+// written (floor 7.4 us at the measured copy rate); 64 single rows 3.4 us, launch and one chain of loads (a call from the
+// host takes 10 us more).
 #include "kernels.h"
 #include "kv.cuh"
 

@@ -5,7 +5,7 @@
 // first row) and of the new pages (its first entry of the free list). The pages' sum runs over
 // the requests that passed the first one's checks. Every CTA takes both sums over all requests
 // itself (8 bytes a request from L2, at most 16384 of them) and then writes its own rows and
-// requests, so that one launch without a wait between CTAs does the step. A row finds its
+// requests, so that no CTA waits for another. A row finds its
 // request by binary search in the sums, which stay in shared memory (8 bytes a request).
 // Reads and writes of the page table never meet: a row reads entries below ceil(ctx/P) or
 // the free list, and only entries from ceil(ctx/P) on are written.
