@@ -174,6 +174,45 @@ def test_long_lists(torch, Bn, Hq, Hkv, D, dt, k, split):
     a.check(0, sel)
 
 
+# ------------------------------------------------------------------------------ ends of the ranges
+
+@pytest.mark.parametrize("Hq,nq,k", [(8, 1, 0), (64, 1, 0), (8, 3, 0), (8, 40, 0), (8, 1, 300), (64, 1, 300), (17, 2, 129)])
+@pytest.mark.parametrize("split", [False, True])
+def test_scales_at_the_ends_of_their_range(torch, Bn, Hq, nq, k, split):
+    """Scale exponents -32 and 48 side by side, V's in every row, K's with logits that stay small; bytes that the store
+    does not write are read as the nearest that it does."""
+    a = Att(torch, [2100, 260], [nq, nq], Hq, 1, 128, 64, torch.bfloat16, k + Hq)
+    _, scales = ref.kv_views(a.pool, 1, 64, 128)
+    g = torch.Generator().manual_seed(1)
+    ends = torch.tensor([95, 175, 121], dtype=torch.uint8)
+    scales[..., 1] = ends[torch.randint(3, scales.shape[:-1], generator=g)].cuda()
+    scales[..., 0] = torch.tensor([95, 100], dtype=torch.uint8)[torch.randint(2, scales.shape[:-1], generator=g)].cuda()
+    a.scale = 2.0 ** 16
+    sel = None
+    if k:
+        sel = torch.stack([torch.randperm(260 - nq, generator=g)[:k] if k < 250 else torch.randint(260 - nq, (k,), generator=g)
+                           for _ in range(a.T)]).int().cuda()
+    ws = a.workspace(Bn, k) if split else None
+    a.call(Bn, 1, sel, ws)
+    a.check(1, sel)
+    kept = a.out.clone(), a.lse.clone()
+    scales[..., 1] = torch.where(scales[..., 1] == 95, 0, torch.where(scales[..., 1] == 175, 255, scales[..., 1]))
+    scales[..., 0] = torch.where(scales[..., 0] == 95, 7, scales[..., 0])
+    a.call(Bn, 1, sel, ws)
+    assert torch.equal(a.out, kept[0]) and torch.equal(a.lse, kept[1])
+
+
+@pytest.mark.parametrize("Hq,nq", [(4, 1), (64, 1), (4, 70)])
+def test_small_and_large_fp16_queries(torch, Bn, Hq, nq):
+    """Rows of q in fp16's subnormal range, zeros, and rows near its largest value."""
+    a = Att(torch, [200], [nq], Hq, 1, 64, 64, torch.float16)
+    a.scale = 2.0 ** -10
+    for i, f in enumerate([0.0, 2.0 ** -20, 2.0 ** -14, 2.0 ** 13]):
+        a.q[:, i] = (a.q[:, i].float().clamp(-4, 4) * f).half()
+    a.call(Bn, 1)
+    a.check(1)
+
+
 # ------------------------------------------------------------------------------ batches of unlike requests
 
 @pytest.mark.parametrize("Hq,Hkv,D,dt", [(8, 1, 128, "bfloat16"), (16, 2, 64, "float16"), (64, 1, 128, "float16"),
