@@ -435,7 +435,8 @@ typedef struct {
     int32_t page_size, kv_heads, head_dim;
 } idx_kv_layout_t;
 
-typedef enum { IDX_BF16 = 0, IDX_FP16 = 1 } idx_ftype; /* element type of q, k, v and out */
+/* Element type of q, k, v and out (bf16 or fp16), and of probabilities (any). */
+typedef enum { IDX_BF16 = 0, IDX_FP16 = 1, IDX_FP32 = 2 } idx_ftype;
 
 int idx_kv_layout(int32_t kv_heads, int32_t head_dim, int32_t page_size, idx_kv_layout_t* out);
 
@@ -511,6 +512,143 @@ int idx_attn_paged(const void* q, int32_t ftype, int64_t T, int32_t q_heads, int
                    int32_t n_sel, float softmax_scale, void* out, int64_t out_row_stride,
                    int64_t out_head_stride, float* lse, void* workspace, size_t workspace_bytes,
                    int32_t* dev_status, cudaStream_t stream);
+
+/*
+ * Attention of a tree of drafted tokens over the 8-bit paged KV cache: idx_attn_paged with a mask among a
+ * step's own tokens in place of causal order. A sequence's n query rows (cu_seqlens_q) are nodes, whose keys are its
+ * last n: node j's is key front + j, front = seq_lens_k[b] - n. A row sees every key in front of the tree,
+ * and node j where bit j of its mask is set (its own bit too, or it does not see itself).
+ *   tree_mask: bit j of a row is bit j % 64 of word tree_mask[t*mask_stride + j/64] (uint64, 8-byte aligned);
+ *     mask_words words of a row are read, 64 * mask_words >= min(max_q_len, T). Any mask is allowed: a row
+ *     that sees nothing gets out 0 and lse -inf; bits from n on are ignored, and so are nodes whose key would lie before
+ *     key 0 (front < 0: a request that idx_step_meta refused has rows and no keys).
+ *   With a list (sel_idx, n_sel entries a row, as in idx_attn_paged) a row attends the listed keys in front of the tree
+ *     and the nodes that its mask shows, which are not listed: entries that are negative or front and above are
+ *     ignored. The scorers and the top-k give such lists when they are called with causal = 0 and the lengths in front of the tree.
+ *   max_q_len (after min with T) <= 1024 (IDX_EUNSUPPORTED above).
+ * All else, the arithmetic and the treatment of bad lengths, pages and NaN codes too, as in idx_attn_paged; the
+ * workspace's size by idx_attn_tree_workspace_bytes.
+ */
+int idx_attn_tree_workspace_bytes(int64_t T, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t B,
+                                  int32_t max_q_len, int32_t max_seq_len_k, int32_t n_sel,
+                                  size_t* bytes);
+
+int idx_attn_tree(const void* q, int32_t ftype, int64_t T, int32_t q_heads, int32_t kv_heads,
+                  int32_t head_dim, int64_t q_row_stride, int64_t q_head_stride, const void* pool,
+                  int64_t num_pages, int32_t page_size, int64_t page_stride,
+                  const int32_t* page_table, int32_t pt_stride, const int32_t* seq_lens_k,
+                  const int32_t* cu_seqlens_q, int32_t B, const uint64_t* tree_mask, int64_t mask_stride,
+                  int32_t mask_words, int32_t max_q_len, int32_t max_seq_len_k, const int32_t* sel_idx,
+                  int64_t sel_stride, int32_t n_sel, float softmax_scale, void* out,
+                  int64_t out_row_stride, int64_t out_head_stride, float* lse, void* workspace,
+                  size_t workspace_bytes, int32_t* dev_status, cudaStream_t stream);
+
+/*
+ * Verification of drafted tokens against the target's probabilities, from given random numbers, so that
+ * what is emitted is distributed as if the target had drawn every token itself.
+ * Sequence b's rows t = cu_seqlens_q[b] .. are the nodes of its tree: node 0 is its last accepted token, and
+ *   tokens[t], parents[t] (int32 [T]) are node t - cu_seqlens_q[b]'s drafted token and the node that it follows, a lower
+ *   one (a node whose parent is not lower is never reached). A chain is a tree.
+ * target_probs: [T] rows of V (of type ptype, target_stride elements apart): row t is the target's distribution of
+ *   the token behind node t. draft_probs: the drafter's, from which all children of node t were drawn
+ *   independently; NULL: children were chosen, not drawn. Entries that are negative, infinite or NaN count as 0 and set
+ *   IDX_STATUS_BAD_VALUE where they are read. Rows need not add up to 1 exactly.
+ * The walk starts on node 0 with p = the row of its probabilities, c = 0, S = 1 and tests the children of its
+ *   node in index order. With draft_probs (q): child t with token x is accepted if
+ *     coins[t] * q[x] * S < p[x] - c * q[x];  else c += S, then S = sum_v max(p[v] - c * q[v], 0).
+ *   Without: if coins[t] * S < p[x], x not rejected at this node before; else S = max(S - p[x], 0) and x is out
+ *   of p (p[x] counts 0 once it is). An accepted child becomes the walk's node, with c = 0 and S = 1. A child whose token is outside [0, V) is
+ *   passed over (IDX_STATUS_BAD_VALUE). coins: fp32 [T], uniform in [0, 1); only tested nodes' are used.
+ * Where no child is left, or max_path nodes are accepted, a token is drawn from the weights that are left, w[v] = max(p[v] -
+ *   c * q[v], 0) or p[v] without the rejected: the first v whose sum w[0] + .. + w[v] passes last_coins[b] (fp32 [B],
+ *   in [0, 1); others set IDX_STATUS_BAD_VALUE) times the sum of all. If nothing is left, from p; if that holds nothing either,
+ *   -1 and IDX_STATUS_BAD_VALUE. Products, differences and sums are carried to 2^-44 or better of the sum.
+ * Outputs: n_path int32 [B]: accepted nodes, node 0 among them (0 for a sequence without rows); path int32 [B][max_path]:
+ *   those nodes, increasing; out_tokens int32 [B][max_path]: the tokens of path[1] .. and then the drawn one, n_path of
+ *   them. -1 behind. A sequence whose rows break their bounds (as in idx_attn_paged) gets n_path 0 and sets IDX_STATUS_BAD_LEN.
+ * V <= 2^20 (IDX_EUNSUPPORTED above). Reads the rows of the nodes that the walk stands on, no others.
+ */
+int idx_draft_verify(const void* target_probs, const void* draft_probs, int32_t ptype,
+                     int64_t target_stride, int64_t draft_stride, int64_t T, int32_t V,
+                     const int32_t* tokens, const int32_t* parents, const float* coins,
+                     const float* last_coins, const int32_t* cu_seqlens_q, int32_t B, int32_t max_q_len,
+                     int32_t max_path, int32_t* path, int32_t* n_path, int32_t* out_tokens,
+                     int32_t* dev_status, cudaStream_t stream);
+
+/*
+ * The accepted tokens of a drafting step moved together in the paged caches: of sequence b, whose last n keys are the
+ * nodes of its tree (as in idx_attn_tree), the token at key front + path[b][i] goes to key front + i, i <
+ * n_path[b]. path int32 [B][max_path] and n_path int32 [B] as idx_draft_verify gives them: nodes increase.
+ * new_lens (int32 [B], or NULL) becomes front + n_path, the sequence's keys from now on. Keys behind are no longer
+ * defined; their bytes are left as they were but where they shared a scale with what moved.
+ *   layers: that many caches of one page table, layer l's page p at pool + l*layer_stride + p*page_stride
+ *     (multiples of 16): whole layers one behind the other, or each page's layers; pages may not overlap (IDX_EINVAL).
+ * idx_kv_compact: the 8-bit KV cache. A block of 16 tokens that tokens move into takes the largest scale among the blocks
+ *   that they, and the tokens that it keeps, come from; codes of smaller ones are divided by the power of two and rounded
+ *   to nearest even (exact but for codes that become subnormal).
+ * idx_k_compact: the indexer's K cache (dtype IDX_MXFP4 or IDX_FP8). The tokens' bytes move as they are.
+ * A sequence with fewer keys than rows (idx_step_meta refused it) is left alone, its new length is its seq_lens_k. One whose lengths are
+ *   negative, above pt_stride * page_size, or whose n_path is negative or above max_path or its rows is left alone too and sets
+ *   IDX_STATUS_BAD_LEN; one whose path does not increase or leaves the tree IDX_STATUS_BAD_VALUE (new length: seq_lens_k, at
+ *   least 0). A token whose page, or whose destination's, is outside the pool does not move (IDX_STATUS_BAD_PAGE).
+ * Sequences may share pages in front of their trees only (idx_pages_update keeps it so). new_lens may not be one of the
+ *   inputs. layers <= 65535.
+ */
+int idx_kv_compact(const int32_t* path, int32_t max_path, const int32_t* n_path,
+                   const int32_t* seq_lens_k, const int32_t* cu_seqlens_q, int32_t B,
+                   const int32_t* page_table, int32_t pt_stride, void* pool, int32_t kv_heads,
+                   int32_t head_dim, int32_t layers, int64_t layer_stride, int64_t num_pages,
+                   int32_t page_size, int64_t page_stride, int32_t* new_lens, int32_t* dev_status,
+                   cudaStream_t stream);
+
+int idx_k_compact(const int32_t* path, int32_t max_path, const int32_t* n_path,
+                  const int32_t* seq_lens_k, const int32_t* cu_seqlens_q, int32_t B,
+                  const int32_t* page_table, int32_t pt_stride, int32_t dtype, void* pool,
+                  int32_t layers, int64_t layer_stride, int64_t num_pages, int32_t page_size,
+                  int64_t page_stride, int32_t* new_lens, int32_t* dev_status, cudaStream_t stream);
+
+/*
+ * Next rows of a page table out of the present ones, on the GPU: requests that end, go back to a shorter length (after
+ * rejected drafts), change places, or fork into several that share the pages in front (parallel samples, beams).
+ *   Next row b < n_out continues present row parent[b] with its first keep[b] tokens (int32 [n_out]; 0 <= keep <=
+ *     lens[parent]); parent -1 with keep 0 begins an empty row. Present rows that nothing continues end.
+ *   page_table int32 [B][pt_stride], lens int32 [B] (tokens, so that row i holds ceil(lens/P) pages); new_table int32
+ *     [n_out][new_stride] gets entries 0 .. ceil(keep/P) - 1, others are left as they were; new_lens int32 [n_out] = keep.
+ *   shares int32 [num_pages]: holders of a page beyond the first (0 for a page with one, and for a free one: pages that
+ *     idx_step_meta gives out need no entry). new_shares likewise, behind the call; it may be shares itself.
+ *   A row's last page, if it is not full, will be written by the row. Where it has another holder behind the call, the row
+ *     gets a page of its own from the free list and copies[b] (int32 [n_out][2]) = (old page, new page), for
+ *     idx_pages_copy to carry out in every cache in front of the next step; but the first of rows that all end in
+ *     one page without other holders keeps it. copies[b] = (-1, -1) where nothing is to be copied.
+ *   free_pages [free_cap] and free_span [2] as in idx_step_meta; pages are taken from the front in row order. new_free
+ *     [new_free_cap], new_free_cap >= num_pages, gets what is left of the list, in its order, and behind it the pages that no
+ *     row holds any more, by page number; new_span = (0, how many). Entries behind are left as they were.
+ * A row that breaks its bounds (or whose parent does, or whose pages exceed new_stride) sets IDX_STATUS_BAD_LEN and becomes an empty row; a present
+ *   row with a length outside [0, pt_stride * P] holds nothing. A row for which no free page is left sets IDX_STATUS_NO_PAGE
+ *   and becomes an empty row, and what it would have held is released. A page id outside [0, num_pages) is passed on but not counted
+ *   (IDX_STATUS_BAD_PAGE); a page released more often than it was held becomes free once (IDX_STATUS_BAD_PAGE); a
+ *   free_span outside [0, free_cap] is taken as empty (IDX_STATUS_BAD_PAGE).
+ * B, n_out <= 16384, num_pages <= 2^30 (IDX_EUNSUPPORTED above). Outputs may not be inputs (but new_shares may be shares) nor one another. What
+ *   follows on the stream starts when the outputs are visible.
+ */
+int idx_pages_update(const int32_t* parent, const int32_t* keep, int32_t n_out,
+                     const int32_t* page_table, int32_t pt_stride, const int32_t* lens, int32_t B,
+                     int32_t page_size, int32_t* new_table, int32_t new_stride, int32_t* new_lens,
+                     const int32_t* shares, int32_t* new_shares, int32_t num_pages,
+                     const int32_t* free_pages, int32_t free_cap, const int32_t* free_span,
+                     int32_t* new_free, int32_t new_free_cap, int32_t* new_span, int32_t* copies,
+                     int32_t* dev_status, cudaStream_t stream);
+
+/*
+ * Copies of whole pages in a paged cache of any kind: for each i < n page copies[i][0] to page copies[i][1] (int32
+ * [n][2]), page_bytes bytes (a multiple of 16) in each of `layers` layers (as in idx_kv_compact). A pair with a
+ * negative page, or twice the same, is passed over; one with a page outside the pool sets IDX_STATUS_BAD_PAGE and is passed over.
+ * Pages that are written may not be read, nor written twice, by the same call (their contents are unspecified then).
+ * n, layers <= 65535 (IDX_EUNSUPPORTED above).
+ */
+int idx_pages_copy(const int32_t* copies, int32_t n, void* pool, int32_t layers, int64_t layer_stride,
+                   int64_t num_pages, int64_t page_bytes, int64_t page_stride, int32_t* dev_status,
+                   cudaStream_t stream);
 
 /* Human-readable name of an idx_status value (static string). */
 const char* idx_status_string(int status);

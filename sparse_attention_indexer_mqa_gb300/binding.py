@@ -19,7 +19,7 @@ IDX_ROPE_NONE, IDX_ROPE_NEOX, IDX_ROPE_INTERLEAVED = 0, 1, 2
 IDX_STATUS_BAD_SLOT, IDX_STATUS_BAD_POS, IDX_STATUS_BAD_PAGE = 0x1, 0x2, 0x4
 IDX_STATUS_TIMEOUT, IDX_STATUS_BAD_LEN = 0x8, 0x10
 IDX_STATUS_NO_PAGE, IDX_STATUS_BAD_VALUE = 0x20, 0x40
-IDX_BF16, IDX_FP16 = 0, 1
+IDX_BF16, IDX_FP16, IDX_FP32 = 0, 1, 2
 
 HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include",
                       "idx.h")
@@ -112,12 +112,23 @@ def _declare(L):
     L.idx_attn_paged.argtypes = [vp, i32, i64, i32, i32, i32, i64, i64, vp, i64, i32, i64, vp, i32, vp, vp,
                                  i32, i32, i32, i32, vp, i64, i32, f32, vp, i64, i64, vp, vp, C.c_size_t,
                                  vp, vp]
+    L.idx_attn_tree_workspace_bytes.argtypes = L.idx_attn_workspace_bytes.argtypes
+    L.idx_attn_tree.argtypes = [vp, i32, i64, i32, i32, i32, i64, i64, vp, i64, i32, i64, vp, i32, vp, vp, i32, vp, i64,
+                                i32, i32, i32, vp, i64, i32, f32, vp, i64, i64, vp, vp, C.c_size_t, vp, vp]
+    L.idx_draft_verify.argtypes = [vp, vp, i32, i64, i64, i64, i32, vp, vp, vp, vp, vp, i32, i32, i32, vp, vp, vp, vp, vp]
+    L.idx_kv_compact.argtypes = [vp, i32, vp, vp, vp, i32, vp, i32, vp, i32, i32, i32, i64, i64, i32, i64, vp, vp, vp]
+    L.idx_k_compact.argtypes = [vp, i32, vp, vp, vp, i32, vp, i32, i32, vp, i32, i64, i64, i32, i64, vp, vp, vp]
+    L.idx_pages_update.argtypes = [vp, vp, i32, vp, i32, vp, i32, i32, vp, i32, vp, vp, vp, i32, vp, i32, vp, vp, i32, vp,
+                                   vp, vp, vp]
+    L.idx_pages_copy.argtypes = [vp, i32, vp, i32, i64, i64, i64, i64, vp, vp]
     for n in ("idx_cache_layout", "idx_k_store", "idx_q_quant", "idx_qk_prep", "idx_mqa_logits_paged",
               "idx_topk", "idx_debug_encode", "idx_mqa_topk_workspace_bytes", "idx_mqa_topk_paged",
               "idx_debug_mma_rate", "idx_mqa_topk_paged_noalloc", "idx_compress_k_store",
               "idx_mqa_topk_cand_workspace_bytes", "idx_mqa_topk_cand_paged",
               "idx_mqa_logits_workspace_bytes", "idx_debug_wait_timeout", "idx_step_meta", "idx_kv_layout",
-              "idx_kv_store", "idx_attn_workspace_bytes", "idx_attn_paged"):
+              "idx_kv_store", "idx_attn_workspace_bytes", "idx_attn_paged", "idx_attn_tree_workspace_bytes",
+              "idx_attn_tree", "idx_draft_verify", "idx_kv_compact", "idx_k_compact", "idx_pages_update",
+              "idx_pages_copy"):
         getattr(L, n).restype = C.c_int
 
 
@@ -436,12 +447,10 @@ def idx_attn_workspace_bytes(T, q_heads, kv_heads, head_dim, B, max_q_len, max_s
     return int(n.value)
 
 
-def idx_attn_paged(q, pool, num_pages, page_size, page_stride, kv_heads, page_table, seq_lens_k, cu_seqlens_q,
-                   causal, max_q_len, max_seq_len_k, softmax_scale, out, lse=None, sel_idx=None, workspace=None,
-                   dev_status=None, stream=None):
-    """q, out: bf16 or fp16 [T, q_heads, head_dim], last dimension dense, the others strided;
-    sel_idx: int32 [T, n_sel], n_sel >= 1, rows strided (the top-k's output), or None for every visible key."""
-    fn, dev = "idx_attn_paged", _device()
+def _attention(fn, q, pool, num_pages, page_size, page_stride, kv_heads, page_table, seq_lens_k, cu_seqlens_q, causal,
+               tree_mask, max_q_len, max_seq_len_k, softmax_scale, out, lse, sel_idx, workspace, dev_status, stream):
+    """What both forms of the attention check and hand on; causal is None for a tree."""
+    dev = _device()
     i32 = _torch.int32
     ft = _ftype(fn, q)
     if q.dim() != 3 or q.get_device() != dev:
@@ -489,10 +498,194 @@ def idx_attn_paged(q, pool, num_pages, page_size, page_stride, kv_heads, page_ta
             raise ValueError(f"{fn}: the workspace has to be contiguous, on the current CUDA device; got "
                              f"{tuple(workspace.shape)}, strides {workspace.stride()}, {workspace.device}")
         wsb, ws_p = workspace.nbytes, workspace.data_ptr()
-    st = (_lib or load()).idx_attn_paged(
-        q.data_ptr(), ft, T, H, kv_heads, D, qr, qh, pool.data_ptr(), num_pages, page_size, page_stride,
-        page_table.data_ptr(), width, seq_lens_k.data_ptr(), cu_seqlens_q.data_ptr(), B, 1 if causal else 0, max_q_len,
-        max_seq_len_k, sel_p, sel_stride, n_sel, softmax_scale, out.data_ptr(), orow, oh, lse_p, ws_p, wsb,
+    front = (q.data_ptr(), ft, T, H, kv_heads, D, qr, qh, pool.data_ptr(), num_pages, page_size, page_stride,
+             page_table.data_ptr(), width, seq_lens_k.data_ptr(), cu_seqlens_q.data_ptr(), B)
+    back = (max_q_len, max_seq_len_k, sel_p, sel_stride, n_sel, softmax_scale, out.data_ptr(), orow, oh, lse_p, ws_p, wsb,
+            _status(fn, dev_status, dev), _stream(stream))
+    if causal is not None:
+        st = (_lib or load()).idx_attn_paged(*front, 1 if causal else 0, *back)
+    else:
+        if tree_mask.dtype is not _torch.int64 or tree_mask.dim() != 2 or tree_mask.get_device() != dev:
+            _refuse(fn, "tree_mask", tree_mask, _torch.int64, 2, False)
+        n, words = tree_mask.shape
+        s0, s1 = tree_mask.stride()
+        if n != T or (T > 0 and words > 1 and s1 != 1) or (T > 1 and s0 < words):
+            raise ValueError(f"{fn}: tree_mask {tuple(tree_mask.shape)} with strides {tree_mask.stride()} for {T} rows")
+        st = (_lib or load()).idx_attn_tree(*front, tree_mask.data_ptr(), max(s0, words), words, *back)
+    if st:
+        _check(fn, st)
+
+
+def idx_attn_paged(q, pool, num_pages, page_size, page_stride, kv_heads, page_table, seq_lens_k, cu_seqlens_q,
+                   causal, max_q_len, max_seq_len_k, softmax_scale, out, lse=None, sel_idx=None, workspace=None,
+                   dev_status=None, stream=None):
+    """q, out: bf16 or fp16 [T, q_heads, head_dim], last dimension dense, the others strided;
+    sel_idx: int32 [T, n_sel], n_sel >= 1, rows strided (the top-k's output), or None for every visible key."""
+    _attention("idx_attn_paged", q, pool, num_pages, page_size, page_stride, kv_heads, page_table, seq_lens_k,
+               cu_seqlens_q, 1 if causal else 0, None, max_q_len, max_seq_len_k, softmax_scale, out, lse, sel_idx,
+               workspace, dev_status, stream)
+
+
+def idx_attn_tree_workspace_bytes(T, q_heads, kv_heads, head_dim, B, max_q_len, max_seq_len_k, n_sel=0) -> int:
+    n = C.c_size_t(0)
+    _check("idx_attn_tree_workspace_bytes", load().idx_attn_tree_workspace_bytes(
+        T, q_heads, kv_heads, head_dim, B, max_q_len, max_seq_len_k, n_sel, C.byref(n)))
+    return int(n.value)
+
+
+def idx_attn_tree(q, pool, num_pages, page_size, page_stride, kv_heads, page_table, seq_lens_k, cu_seqlens_q,
+                  tree_mask, max_q_len, max_seq_len_k, softmax_scale, out, lse=None, sel_idx=None, workspace=None,
+                  dev_status=None, stream=None):
+    """As idx_attn_paged, for rows that are nodes of trees: tree_mask int64 [T, words], rows strided, bit j % 64 of
+    word j // 64 set where the row sees its sequence's node j; sel_idx lists keys in front of the tree."""
+    _attention("idx_attn_tree", q, pool, num_pages, page_size, page_stride, kv_heads, page_table, seq_lens_k,
+               cu_seqlens_q, None, tree_mask, max_q_len, max_seq_len_k, softmax_scale, out, lse, sel_idx, workspace,
+               dev_status, stream)
+
+
+def _probs(fn, name, x, dev, T):
+    """Type of a matrix of probabilities, its rows' distance and their length."""
+    torch = _torch
+    ft = {torch.float32: IDX_FP32, torch.bfloat16: IDX_BF16, torch.float16: IDX_FP16}.get(x.dtype)
+    if ft is None:
+        raise ValueError(f"{fn}: {name} of {x.dtype} is neither float32, bfloat16 nor float16")
+    if x.dim() != 2 or x.get_device() != dev:
+        _refuse(fn, name, x, x.dtype, 2, False)
+    n, V = x.shape
+    s0, s1 = x.stride()
+    if n != T or (T > 0 and V > 1 and s1 != 1):
+        raise ValueError(f"{fn}: {name} {tuple(x.shape)} with strides {x.stride()} for {T} rows: its rows have to be dense")
+    return ft, s0 if T > 1 else 0, V
+
+
+def idx_draft_verify(target_probs, draft_probs, tokens, parents, coins, last_coins, cu_seqlens_q, max_q_len, path, n_path,
+                     out_tokens, dev_status=None, stream=None):
+    """target_probs, draft_probs (or None): fp32, bf16 or fp16 [T, V], rows dense, strided; tokens, parents: int32 [T]; coins:
+    fp32 [T]; last_coins: fp32 [B]; path, out_tokens: int32 [B, max_path]; n_path: int32 [B]."""
+    fn, dev = "idx_draft_verify", _device()
+    i32, f32 = _torch.int32, _torch.float32
+    for x in (tokens, parents, cu_seqlens_q, n_path):
+        if x.dtype is not i32 or x.get_device() != dev or not x.is_contiguous():
+            _refuse(fn, "every list of tokens, nodes or rows", x, i32, 1, True)
+    for x in (coins, last_coins):
+        if x.dtype is not f32 or x.get_device() != dev or not x.is_contiguous():
+            _refuse(fn, "coins and last_coins", x, f32, 1, True)
+    for x in (path, out_tokens):
+        if x.dtype is not i32 or x.dim() != 2 or x.get_device() != dev or not x.is_contiguous():
+            _refuse(fn, "path and out_tokens", x, i32, 2, True)
+    T, B = tokens.numel(), n_path.numel()
+    ft, ts, V = _probs(fn, "target_probs", target_probs, dev, T)
+    draft_p, ds = None, 0
+    if draft_probs is not None:
+        fd, ds, vd = _probs(fn, "draft_probs", draft_probs, dev, T)
+        if fd != ft or vd != V:
+            raise ValueError(f"{fn}: target_probs {tuple(target_probs.shape)} of {target_probs.dtype} and draft_probs "
+                             f"{tuple(draft_probs.shape)} of {draft_probs.dtype} do not match")
+        # without rows its pointer may be null, which the library takes for no probabilities: nothing is read then
+        draft_p = draft_probs.data_ptr()
+    if (parents.numel() != T or coins.numel() != T or last_coins.numel() != B or cu_seqlens_q.numel() != B + 1
+            or path.shape[0] != B or out_tokens.shape != path.shape):
+        raise ValueError(f"{fn}: shapes do not belong to {B} sequences and {T} rows")
+    st = (_lib or load()).idx_draft_verify(
+        target_probs.data_ptr(), draft_p, ft, ts, ds, T, V, tokens.data_ptr(), parents.data_ptr(), coins.data_ptr(),
+        last_coins.data_ptr(), cu_seqlens_q.data_ptr(), B, max_q_len, path.shape[1], path.data_ptr(), n_path.data_ptr(),
+        out_tokens.data_ptr(), _status(fn, dev_status, dev), _stream(stream))
+    if st:
+        _check(fn, st)
+
+
+def _layers_bytes(fn, pool, num_pages, page_stride, page_bytes, layers, layer_stride, dev):
+    """The pool holds its layers' pages: the library only sees a pointer."""
+    have = pool.nbytes if pool.is_contiguous() else _bytes_behind(pool)
+    need = (layers - 1) * layer_stride + (num_pages - 1) * page_stride + page_bytes
+    if pool.get_device() != dev or (num_pages > 0 and layers > 0 and have < need):
+        raise ValueError(f"{fn}: the pool ({tuple(pool.shape)}, {pool.dtype}, {pool.device}) does not hold {layers} layers "
+                         f"{layer_stride} bytes apart of {num_pages} pages {page_stride} bytes apart on the current CUDA device")
+
+
+def _compact_lists(fn, path, n_path, seq_lens_k, cu_seqlens_q, page_table, new_lens, dev):
+    """Checks of the lists that both caches' compaction takes, and their part of the library's arguments."""
+    i32 = _torch.int32
+    for x in (n_path, seq_lens_k, cu_seqlens_q):
+        if x.dtype is not i32 or x.get_device() != dev or not x.is_contiguous():
+            _refuse(fn, "n_path, seq_lens_k and cu_seqlens_q", x, i32, 1, True)
+    for x in (path, page_table):
+        if x.dtype is not i32 or x.dim() != 2 or x.get_device() != dev or not x.is_contiguous():
+            _refuse(fn, "path and page_table", x, i32, 2, True)
+    B = n_path.numel()
+    if new_lens is not None and (new_lens.dtype is not i32 or new_lens.numel() != B or new_lens.get_device() != dev
+                                 or not new_lens.is_contiguous()):
+        _refuse(fn, f"new_lens (of {B} sequences)", new_lens, i32, 1, True)
+    if path.shape[0] != B or page_table.shape[0] != B or seq_lens_k.numel() != B or cu_seqlens_q.numel() != B + 1:
+        raise ValueError(f"{fn}: shapes do not belong to {B} sequences")
+    return (path.data_ptr(), path.shape[1], n_path.data_ptr(), seq_lens_k.data_ptr(), cu_seqlens_q.data_ptr(), B,
+            page_table.data_ptr(), page_table.shape[1])
+
+
+def idx_kv_compact(path, n_path, seq_lens_k, cu_seqlens_q, page_table, pool, num_pages, page_size, page_stride, kv_heads,
+                   head_dim, layers=1, layer_stride=0, new_lens=None, dev_status=None, stream=None):
+    """path: int32 [B, max_path]; n_path, new_lens: int32 [B]. Layer l of the pool begins l * layer_stride bytes in."""
+    fn, dev = "idx_kv_compact", _device()
+    lists = _compact_lists(fn, path, n_path, seq_lens_k, cu_seqlens_q, page_table, new_lens, dev)
+    _layers_bytes(fn, pool, num_pages, page_stride, kv_heads * (2 * page_size * head_dim + 16), layers, layer_stride, dev)
+    st = (_lib or load()).idx_kv_compact(
+        *lists, pool.data_ptr(), kv_heads, head_dim, layers, layer_stride, num_pages, page_size, page_stride,
+        None if new_lens is None else new_lens.data_ptr(), _status(fn, dev_status, dev), _stream(stream))
+    if st:
+        _check(fn, st)
+
+
+def idx_k_compact(path, n_path, seq_lens_k, cu_seqlens_q, page_table, dtype, pool, num_pages, page_size, page_stride,
+                  layers=1, layer_stride=0, new_lens=None, dev_status=None, stream=None):
+    """As idx_kv_compact, in the indexer's K cache of type dtype."""
+    fn, dev = "idx_k_compact", _device()
+    lists = _compact_lists(fn, path, n_path, seq_lens_k, cu_seqlens_q, page_table, new_lens, dev)
+    _layers_bytes(fn, pool, num_pages, page_stride, (132 if dtype == IDX_FP8 else 68) * page_size, layers, layer_stride, dev)
+    st = (_lib or load()).idx_k_compact(
+        *lists, dtype, pool.data_ptr(), layers, layer_stride, num_pages, page_size, page_stride,
+        None if new_lens is None else new_lens.data_ptr(), _status(fn, dev_status, dev), _stream(stream))
+    if st:
+        _check(fn, st)
+
+
+def idx_pages_update(parent, keep, page_table, lens, page_size, new_table, new_lens, shares, new_shares, free_pages, free_span,
+                     new_free, new_span, copies, dev_status=None, stream=None):
+    """parent, keep, new_lens: int32 [n_out]; copies: int32 [n_out, 2]; page_table: int32 [B, width]; new_table: int32
+    [n_out, new width]; lens: int32 [B]; shares, new_shares: int32 [num_pages]; new_free: int32 of num_pages at least."""
+    fn, dev = "idx_pages_update", _device()
+    i32 = _torch.int32
+    for x in (parent, keep, lens, new_lens, shares, new_shares, free_pages, free_span, new_free, new_span):
+        if x.dtype is not i32 or x.get_device() != dev or not x.is_contiguous():
+            _refuse(fn, "every list of rows, lengths or pages", x, i32, 1, True)
+    for x in (page_table, new_table, copies):
+        if x.dtype is not i32 or x.dim() != 2 or x.get_device() != dev or not x.is_contiguous():
+            _refuse(fn, "page_table, new_table and copies", x, i32, 2, True)
+    n, B, pages = parent.numel(), lens.numel(), shares.numel()
+    rows, width = page_table.shape
+    new_rows, new_width = new_table.shape
+    if (keep.numel() != n or new_lens.numel() != n or new_rows != n or copies.shape != (n, 2) or rows != B
+            or new_shares.numel() != pages or new_free.numel() < pages or free_span.numel() != 2 or new_span.numel() != 2):
+        raise ValueError(f"{fn}: shapes do not belong to {B} rows, {n} next rows and {pages} pages")
+    st = (_lib or load()).idx_pages_update(
+        parent.data_ptr(), keep.data_ptr(), n, page_table.data_ptr(), width, lens.data_ptr(), B, page_size,
+        new_table.data_ptr(), new_width, new_lens.data_ptr(), shares.data_ptr(), new_shares.data_ptr(), pages,
+        free_pages.data_ptr(), free_pages.numel(), free_span.data_ptr(), new_free.data_ptr(), new_free.numel(),
+        new_span.data_ptr(), copies.data_ptr(), _status(fn, dev_status, dev), _stream(stream))
+    if st:
+        _check(fn, st)
+
+
+def idx_pages_copy(copies, pool, num_pages, page_bytes, page_stride, layers=1, layer_stride=0, dev_status=None, stream=None):
+    """copies: int32 [n, 2] of (from, to), as idx_pages_update gives them. Layers as in idx_kv_compact."""
+    fn, dev = "idx_pages_copy", _device()
+    if copies.dtype is not _torch.int32 or copies.dim() != 2 or copies.get_device() != dev or not copies.is_contiguous():
+        _refuse(fn, "copies", copies, _torch.int32, 2, True)
+    n, two = copies.shape
+    if two != 2:
+        raise ValueError(f"{fn}: copies {tuple(copies.shape)} is no list of pairs")
+    _layers_bytes(fn, pool, num_pages, page_stride, page_bytes, layers, layer_stride, dev)
+    st = (_lib or load()).idx_pages_copy(
+        copies.data_ptr(), n, pool.data_ptr(), layers, layer_stride, num_pages, page_bytes, page_stride,
         _status(fn, dev_status, dev), _stream(stream))
     if st:
         _check(fn, st)

@@ -61,14 +61,15 @@ struct Ring {
 };
 __device__ __forceinline__ constexpr int swizzle(int t) { return (((t >> 1) & 3) << 1) ^ ((t & 1) << 2); }
 
-// kDiag: rows of a unit may see unlike numbers of keys (dense, causal, several queries to a sequence). The ring starts on
-// a 128-byte line: 16 bytes past one, 64 x 8192 keys took 205 us.
-template <int D, bool kHalf, bool kSel, bool kDiag>
+// kDiag: rows of a unit may see unlike numbers of keys (dense, causal, several queries to a sequence). kTree: rows are
+// nodes of a tree of drafted tokens. The ring starts on a 128-byte line: 16 bytes past one, 64 x 8192 keys took 205 us.
+template <int D, bool kHalf, bool kSel, bool kDiag, bool kTree>
 __global__ void __launch_bounds__(kWarps * 32, 3) attn_rows_kernel(const AttnArgs a) {
     using R = Ring<D>;
     extern __shared__ __align__(128) uint8_t sm[];
     __shared__ float2 ml[kWarps][16];
     __shared__ int nan_key[kDiag ? kWarps : 1];  // lowest key whose V held a NaN code that was taken out
+    __shared__ uint32_t nan_nodes[kTree && !kSel ? kTreeMaxNodes / 32 : 1];  // nodes of which that holds
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, c = lane & 3;
     pdl_wait();
     if (a.n_split > 1) pdl_launch_dependents();  // the join
@@ -88,7 +89,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attn_rows_kernel(const AttnArg
         row0 = (int)(blockIdx.x % tiles) * 16;
         tok0 = t;
         rows = min(16, G - row0);
-        kv_end = a.n_sel;
+        kv_end = a.n_sel + (kTree ? max(s.nq, 0) : 0);
     } else {
         const int tiles = (int)(((int64_t)a.max_q_len * G + 15) / 16);
         b = blockIdx.x / tiles;
@@ -112,6 +113,11 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attn_rows_kernel(const AttnArg
     }
     if constexpr (!kSel) kv_end = (int)visible_keys(s.len, s.nq, (row0 + rows - 1) / G, a.causal);
     const int k0 = z * a.chunk, k1 = min(kv_end, k0 + a.chunk);
+    [[maybe_unused]] const int front = s.len - s.nq;  // keys in front of the tree
+    [[maybe_unused]] const uint64_t* mask[2];         // of rows r and r + 8
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        mask[i] = kTree ? a.tree + (kSel ? tok0 : tok0 + (row0 + min(r + 8 * i, rows - 1)) / G) * a.tree_stride : nullptr;
 
     // ---- q: fp16, laid out for the contraction over a thread's 16 consecutive dims ----------------
     uint32_t qa[D / 64][4][4];
@@ -178,7 +184,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attn_rows_kernel(const AttnArg
     constexpr int kStep = kWarps * kKeys;
     const int kw = k0 + kKeys * warp;  // this warp's first key; its next ones are kStep further
     const int n_it = k1 > kw ? (k1 - kw + kStep - 1) / kStep : 0;
-    const int vis_lo = __shfl_sync(kFull, vis[0], 0);  // rows see more and more keys: row 0 the fewest
+    // rows see more and more keys: row 0 the fewest
+    const int vis_lo = kTree ? front : __shfl_sync(kFull, vis[0], 0);
     bool bad_page = false;
 
     // Lookups run ahead: a step's page is loaded one step before its copies are issued and, with a
@@ -186,10 +193,18 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attn_rows_kernel(const AttnArg
     int32_t page = -1, ent = -1, ent_n = -1;
     auto load_entry = [&](int it) -> int32_t {
         const int e = kw + kStep * it + lane;
+        if constexpr (kTree) {  // the nodes that the row sees come behind its list
+            const int j = e - a.n_sel;
+            if (j >= 0) return e < k1 && tree_window(mask[0], a.tree_words, s.nq, j) & 1 ? front + j : -1;
+        }
         return e < k1 ? a.sel[tok0 * a.sel_stride + e] : -1;
     };
+    auto counts = [&](int it) -> bool {  // this lane's entry of step it
+        const int end = kTree && kw + kStep * it + lane < a.n_sel ? front : vis[0];
+        return ent >= 0 && ent < end;
+    };
     auto load_page = [&](int it) -> int32_t {
-        if constexpr (kSel) return (ent >= 0 && ent < vis[0]) ? pt[ent >> lp] : -1;
+        if constexpr (kSel) return counts(it) ? pt[ent >> lp] : -1;
         return it < n_it ? pt[(kw + kStep * it) >> lp] : -1;
     };
     // The scale bytes of a step, loaded with its copies. Dense: K, V of block 0, K, V of block 1, the same in
@@ -200,7 +215,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attn_rows_kernel(const AttnArg
         const uint32_t at = (it & (kStages - 1)) * R::kStage;
         scales_n = 0;
         if constexpr (kSel) {
-            const bool seen = ent >= 0 && ent < vis[0], in = (uint32_t)page < (uint64_t)a.num_pages;
+            const bool seen = counts(it), in = (uint32_t)page < (uint64_t)a.num_pages;
             bad_page |= seen && !in;
             const int pg = seen && in ? page : -1, tok = ent & (P - 1);
             if (pg >= 0)
@@ -273,6 +288,11 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attn_rows_kernel(const AttnArg
                     mma16816(sc[j], qa[d][x], lo, hi);
                 }
             }
+        [[maybe_unused]] uint32_t shown[2] = {~0u, ~0u};  // keys of the step that rows r and r + 8 see
+        if constexpr (kTree && !kSel && kMask) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) shown[i] = (uint32_t)tree_window(mask[i], a.tree_words, s.nq, kb - front);
+        }
         // u = s * c + Ev; masked ones to -inf
         float ev[kKeys / 4], mx[2] = {neg_inf(), neg_inf()};
         [[maybe_unused]] uint32_t use = ~0u;  // bit k: the thread's key 8(k/2) + 2c + k%2 counts
@@ -293,6 +313,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attn_rows_kernel(const AttnArg
                 v = fmaf(v, rc[i] * kc, ev[k]);
                 if constexpr (kSel)
                     v = (use >> k) & 1u ? v : neg_inf();
+                else if constexpr (kTree && kMask)
+                    v = (shown[i] >> ((k >> 1) * 8 + 2 * c + (k & 1))) & 1u ? v : neg_inf();
                 else if constexpr (kMask)
                     v = kb + (k >> 1) * 8 + 2 * c + (k & 1) < vis[i] ? v : neg_inf();
                 mx[i] = fmaxf(mx[i], v);
@@ -384,13 +406,20 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attn_rows_kernel(const AttnArg
             uint4 w = *at;
             if (clear_nan_codes(w.x) | clear_nan_codes(w.y) | clear_nan_codes(w.z) | clear_nan_codes(w.w)) {
                 *at = w;
-                atomicMin(&nan_key[warp], kb + t);
+                if constexpr (kTree)
+                    atomicOr(&nan_nodes[(kb + t - front) >> 5], 1u << ((kb + t - front) & 31));
+                else
+                    atomicMin(&nan_key[warp], kb + t);
             }
         }
         __syncwarp();
     };
 
     if (kDiag && lane == 0) nan_key[warp] = INT32_MAX;
+    if constexpr (kTree && !kSel) {
+        if (tid < kTreeMaxNodes / 32) nan_nodes[tid] = 0;
+        __syncthreads();
+    }
     if (n_it > 0) {
         if constexpr (kSel) {
             ent = load_entry(0);
@@ -419,6 +448,18 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attn_rows_kernel(const AttnArg
             for (int it = 0; it < n_it; ++it) {
                 next(it);
                 compute(it, scales, std::true_type{});
+            }
+        } else if constexpr (kTree) {
+#pragma unroll 1
+            for (int it = 0; it < n_it; ++it) {
+                next(it);
+                if (!page_ok) continue;
+                if (kw + kStep * it + kKeys <= front) {
+                    compute(it, scales, std::false_type{});
+                } else {
+                    clear_v(it);
+                    compute(it, scales, std::true_type{});
+                }
             }
         } else {
             // A unit's rows see at most 15 keys more the one than the other, and a warp's steps are 128 keys
@@ -485,6 +526,10 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attn_rows_kernel(const AttnArg
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) least = min(least, nan_key[w]);
             if (least < INT32_MAX && least < (int)visible_keys(s.len, s.nq, at / G, a.causal))
+                v.x = v.y = v.z = v.w = __int_as_float(0x7fc00000);
+        }
+        if constexpr (kTree && !kSel) {
+            if (tree_sees(a.tree + (tok0 + at / G) * a.tree_stride, a.tree_words, s.nq, nan_nodes))
                 v.x = v.y = v.z = v.w = __int_as_float(0x7fc00000);
         }
         const int64_t tok = kSel ? tok0 : tok0 + at / G;
@@ -601,10 +646,10 @@ Choice choose(const AttnArgs& a) {
     return {true, times * ((rows + 127) / 128), 2};
 }
 
-template <int D, bool kHalf, bool kSel, bool kDiag>
+template <int D, bool kHalf, bool kSel, bool kDiag, bool kTree>
 cudaError_t launch_rows(const AttnArgs& a, cudaStream_t st) {
     constexpr int smem = Ring<D>::kBytes;
-    auto* kernel = attn_rows_kernel<D, kHalf, kSel, kDiag>;
+    auto* kernel = attn_rows_kernel<D, kHalf, kSel, kDiag, kTree>;
     static std::atomic<uint64_t> allowed{0};
     const cudaError_t e = allow_smem(allowed, kernel, smem);
     if (e != cudaSuccess) return e;
@@ -616,10 +661,12 @@ cudaError_t launch_rows(const AttnArgs& a, cudaStream_t st) {
 
 template <int D, bool kHalf>
 cudaError_t launch_d(const AttnArgs& a, cudaStream_t st) {
-    cudaError_t e = choose(a).tile                   ? launch_attn_tile(a, st)
-                    : a.sel                          ? launch_rows<D, kHalf, true, false>(a, st)
-                    : a.causal && a.max_q_len > 1    ? launch_rows<D, kHalf, false, true>(a, st)
-                                                     : launch_rows<D, kHalf, false, false>(a, st);
+    cudaError_t e = choose(a).tile                ? launch_attn_tile(a, st)
+                    : a.tree && a.sel             ? launch_rows<D, kHalf, true, false, true>(a, st)
+                    : a.tree                      ? launch_rows<D, kHalf, false, false, true>(a, st)
+                    : a.sel                       ? launch_rows<D, kHalf, true, false, false>(a, st)
+                    : a.causal && a.max_q_len > 1 ? launch_rows<D, kHalf, false, true, false>(a, st)
+                                                  : launch_rows<D, kHalf, false, false, false>(a, st);
     if (e != cudaSuccess || a.n_split <= 1) return e;
     const int64_t many = (int64_t)kJoinAlone * device_sm_count();
     return a.T * a.q_heads < many ? launch_join<D, kHalf, kJoinWarps>(a, st) : launch_join<D, kHalf, 1>(a, st);
@@ -632,7 +679,7 @@ int64_t attn_plan(AttnArgs& a, int64_t bytes) {
     if (sms <= 0) return -1;
     const Choice choice = choose(a);
     const int64_t units = choice.units;
-    const int64_t keys = a.n_sel ? a.n_sel : a.max_seq_len_k;
+    const int64_t keys = a.n_sel ? a.n_sel + (a.tree ? a.max_q_len : 0) : a.max_seq_len_k;
     const int64_t per_split = a.T * a.q_heads * (a.head_dim + 2) * 4;
     // Splits. Units that fill the resident CTAs (three or two to an SM) by themselves are cut until there are
     // about four rounds of them, in pieces of 1024 keys at least (64 sequences of 8192 keys, 8

@@ -18,8 +18,9 @@
 // A NaN code. Of K it makes the scores of its key NaN, which a row that does not see the key drops with the
 // score. Of V it would come through the product at weight 0 too, so where a unit's rows see unlike numbers of
 // keys (the diagonal of a causal unit) V's NaN codes are taken out of the steps that some row does not see whole, the
-// lowest such key is kept, and rows that see it are NaN at the end. Everywhere else all rows see what was loaded and
-// the product does it.
+// lowest such key is kept, and rows that see it are NaN at the end. Rows of a tree see sets that do not contain one
+// another, so a bit for each of its nodes is kept instead. Everywhere else all rows see what was loaded and the product
+// does it.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -104,6 +105,30 @@ __device__ __forceinline__ int warp_seq_of_query(const AttnArgs& a, int64_t t) {
         if (!in) break;
     }
     return in ? lo : -1;
+}
+
+// A tree of drafted tokens (idx_attn_tree). The last nq keys of a sequence are its nodes, the keys in front of
+// them are seen by every row. Bits of the 64 keys from position `front` + j0 on, set where a row with this mask sees
+// the key: j0 < 0 for keys in front of the tree, nothing behind its end.
+__device__ __forceinline__ uint64_t tree_window(const uint64_t* mask, int words, int nq, int j0) {
+    if (j0 <= -64) return ~0ull;
+    uint64_t w = 0;
+    if (j0 < 0) {
+        w = mask[0] << -j0 | ((1ull << -j0) - 1);
+    } else {
+        const int at = j0 >> 6, by = j0 & 63;
+        if (at < words) w = mask[at] >> by;
+        if (by && at + 1 < words) w |= mask[at + 1] << (64 - by);
+    }
+    const int left = nq - j0;
+    return left >= 64 ? w : left <= 0 ? 0 : w & ((1ull << left) - 1);
+}
+// Whether a row with this mask sees a node whose bit is set in `nodes`.
+__device__ __forceinline__ bool tree_sees(const uint64_t* mask, int words, int nq, const uint32_t* nodes) {
+    bool hit = false;
+    for (int w = 0; w < (nq + 63) / 64; ++w)
+        hit |= (tree_window(mask, words, nq, 64 * w) & (nodes[2 * w] | (uint64_t)nodes[2 * w + 1] << 32)) != 0;
+    return hit;
 }
 
 // Power of two that brings a row of q with the given largest magnitude into fp16's range (its

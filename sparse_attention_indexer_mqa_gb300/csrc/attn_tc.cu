@@ -61,11 +61,13 @@ __device__ __forceinline__ bool conv_all(bool v) {
         : "memory");
     return r != 0;
 }
-template <int D, bool kHalf, bool kSel>
+template <int D, bool kHalf, bool kSel, bool kTree>
 __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs a) {
     using S = SmemT<D>;
     extern __shared__ uint8_t sm_raw[];
     __shared__ uint32_t tmem_slot;
+    // kTree: a bit per node whose V held a NaN code that was taken out, and a word for the keys in front of the tree
+    __shared__ uint32_t nan_nodes[kTree && !kSel ? kTreeMaxNodes / 32 + 1 : 1];
     uint8_t* sm = sm_raw + ((1024u - (tc::smem_u32(sm_raw) & 1023u)) & 1023u);
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + S::kBar);
     uint64_t *q_full = bars, *k_full = bars + 1, *v_full = bars + 2, *s_full = bars + 3, *p_full = bars + 4,
@@ -89,7 +91,7 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
         row0 = (int)(blockIdx.x % tiles) * kRowsT;
         tok0 = t;
         rows = b < 0 ? 0 : min(kRowsT, G - row0);
-        kv_end = a.n_sel;
+        kv_end = a.n_sel + (kTree && b >= 0 ? max(s.nq, 0) : 0);
     } else {
         // the last rows of a sequence see the most keys and go first
         const int tiles = (int)(((int64_t)a.max_q_len * G + kRowsT - 1) / kRowsT);
@@ -117,6 +119,9 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
         *nan_key = INT32_MAX;
         tc::fence_mbar_init();
     }
+    if constexpr (kTree && !kSel) {
+        if (tid <= kTreeMaxNodes / 32) nan_nodes[tid] = 0;
+    }
     __syncwarp();
     if (warp == 0) {
         tc::tmem_alloc(&tmem_slot, 256);
@@ -130,6 +135,7 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
     const int k0 = z * a.chunk, k1 = min(kv_end, k0 + a.chunk);
     const int n = k1 > k0 ? (k1 - k0 + kKeysT - 1) / kKeysT : 0;
     bool ok = true;
+    [[maybe_unused]] const int front = s.len - s.nq;  // keys in front of the tree
 
     if (warp < 4) {
         // ---- softmax: this thread's row --------------------------------------------------------------
@@ -137,7 +143,9 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
         const int row = row0 + min(tid, rows - 1);
         const int64_t tok = kSel ? tok0 : tok0 + row / G;
         const int hq = head * G + (kSel ? row : row % G);
-        const int vis = (int)visible_keys(s.len, s.nq, tok - s.t0, a.causal);
+        // keys that the row sees, of a tree: those in front of it
+        const int vis = kTree && !kSel ? front : (int)visible_keys(s.len, s.nq, tok - s.t0, a.causal);
+        [[maybe_unused]] const uint64_t* mask = kTree ? a.tree + tok * a.tree_stride : nullptr;
         // < 0: an infinity or a NaN in q; the row is scored as zeros, and is NaN at the end if any key counted
         const float rc = write_q_row<D, kHalf>(sm + S::kQ, a.q + tok * a.q_row_stride + (int64_t)hq * a.q_head_stride,
                                                real, tid, a.scale);
@@ -180,6 +188,8 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
             constexpr bool kCut = decltype(cut_tag)::value;
             const float4* sc = scales + (j & 1) * kKeysT;
             [[maybe_unused]] const int left = vis - (k0 + j * kKeysT);  // keys of this step that the row sees
+            // of a tree: which ones of 64
+            [[maybe_unused]] auto window = [&](int from) { return tree_window(mask, a.tree_words, s.nq, from - left); };
             float mx = neg_inf();
 #pragma unroll 1
             for (int c = 0; c < 4; c += 2) {
@@ -187,6 +197,8 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
                 __syncwarp();
                 tc::tmem_ld32(tm_s + lanes + 32 * c, r[0]);
                 tc::tmem_ld32(tm_s + lanes + 32 * c + 32, r[1]);
+                [[maybe_unused]] uint64_t shown = 0;
+                if constexpr (kTree && kCut) shown = window(32 * c);
                 tc::tmem_ld_wait();
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
@@ -195,8 +207,10 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
                     const float4 k = sc[at / 16];
                     float bm = neg_inf();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        bm = fmaxf(bm, !kCut || at + i < left ? __uint_as_float(x[i]) : neg_inf());
+                    for (int i = 0; i < 16; ++i) {
+                        const bool in = !kCut || (kTree ? shown >> (16 * h + i) & 1 : at + i < left);
+                        bm = fmaxf(bm, in ? __uint_as_float(x[i]) : neg_inf());
+                    }
                     // nothing visible: bm is -inf whatever the factor
                     const float u = fmaf(bm, rc * k.x, k.y);
                     mx = fmaxf(mx, kCut && bm == neg_inf() ? bm : u);
@@ -210,6 +224,8 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
                 __syncwarp();
                 tc::tmem_ld32(tm_s + lanes + 32 * c, r[0]);
                 tc::tmem_ld32(tm_s + lanes + 32 * c + 32, r[1]);
+                [[maybe_unused]] uint64_t shown = 0;
+                if constexpr (kTree && kCut) shown = window(32 * c);
                 tc::tmem_ld_wait();
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
@@ -226,8 +242,9 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
                             float2 u = fma2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])),
                                             make_float2(cc, cc), make_float2(sub, sub));
                             if constexpr (kCut) {
-                                u.x = at + i < left ? u.x : neg_inf();
-                                u.y = at + i + 1 < left ? u.y : neg_inf();
+                                const int bit = 32 * g + 16 * h + i;
+                                u.x = (kTree ? shown >> bit & 1 : at + i < left) ? u.x : neg_inf();
+                                u.y = (kTree ? shown >> (bit + 1) & 1 : at + i + 1 < left) ? u.y : neg_inf();
                             }
                             const float2 p = make_float2(ex2(u.x), ex2(u.y));
                             sum = add2(sum, p);
@@ -327,7 +344,10 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
         if (ok && !idle) {
             tc::tc_fence_after();
             if (rc < 0.0f && l != 0.0f) l = __int_as_float(0x7fc00000);
-            store_rows<D, kHalf>(a, tm_o + lanes, n > 0, real, tok, hq, z, m, l, !kSel && *nan_key < vis);
+            bool nan = !kSel && *nan_key < vis;
+            if constexpr (kTree && !kSel)
+                nan = nan_nodes[kTreeMaxNodes / 32] || tree_sees(mask, a.tree_words, s.nq, nan_nodes);
+            store_rows<D, kHalf>(a, tm_o + lanes, n > 0, real, tok, hq, z, m, l, nan);
         }
     } else {
         // ---- converters --------------------------------------------------------------------------------
@@ -342,7 +362,7 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
         int64_t* offs = reinterpret_cast<int64_t*>(sm + S::kOff);
         const int vis_sel = kSel ? (int)visible_keys(s.len, s.nq, tok0 - s.t0, a.causal) : 0;
         // keys that the tile's first row does not see though another does begin here
-        const int vis_first = kSel ? 0 : (int)visible_keys(s.len, s.nq, row0 / G, a.causal);
+        const int vis_first = kSel ? 0 : kTree ? front : (int)visible_keys(s.len, s.nq, row0 / G, a.causal);
         uint4 rk[kPieces], rv[8];
         uint32_t my_scale = 0;  // the key's or block's two scale bytes, bit 16 set; 0: not to be used
         bool bad = false;
@@ -355,11 +375,20 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
         int keys = 0;                                    // of the step
         auto load_entry = [&](int j) -> int32_t {
             const int e = k0 + j * kKeysT + ct;
+            if constexpr (kTree) {  // the nodes that the row sees come behind its list
+                const int node = e - a.n_sel;
+                if (node >= 0)
+                    return e < k1 && tree_window(a.tree + tok0 * a.tree_stride, a.tree_words, s.nq, node) & 1 ? front + node : -1;
+            }
             return e < k1 ? a.sel[tok0 * a.sel_stride + e] : -1;
+        };
+        auto counts = [&](int j) -> bool {  // this thread's entry of step j
+            const int end = kTree && k0 + j * kKeysT + ct < a.n_sel ? front : vis_sel;
+            return ent >= 0 && ent < end;
         };
         auto lookup = [&](int j) {
             if constexpr (kSel) {
-                page[0] = (ent >= 0 && ent < vis_sel) ? pt[ent >> lp] : -1;
+                page[0] = counts(j) ? pt[ent >> lp] : -1;
             } else {
                 const int kt = k0 + j * kKeysT;
                 page[0] = kt < k1 ? pt[kt >> lp] : -1;
@@ -369,7 +398,7 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
         auto place = [&](int j) {
             my_scale = 0;
             if constexpr (kSel) {
-                const bool seen = ent >= 0 && ent < vis_sel, in = (uint32_t)page[0] < (uint64_t)a.num_pages;
+                const bool seen = counts(j), in = (uint32_t)page[0] < (uint64_t)a.num_pages;
                 int64_t at = -1;
                 bad |= seen && !in;
                 if (seen && in) {
@@ -506,7 +535,12 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
                     for (int i = 0; i < 8; ++i) {
                         bool hit = clear_nan_codes(rv[i].x) | clear_nan_codes(rv[i].y);
                         if constexpr (D == 128) hit |= clear_nan_codes(rv[i].z) | clear_nan_codes(rv[i].w);
-                        if (hit) atomicMin(nan_key, end - kKeysT + 8 * my.kg + i);
+                        const int key = end - kKeysT + 8 * my.kg + i;
+                        if constexpr (kTree) {
+                            if (hit) atomicOr(&nan_nodes[key < front ? kTreeMaxNodes / 32 : (key - front) >> 5], 1u << ((key - front) & 31));
+                        } else {
+                            if (hit) atomicMin(nan_key, key);
+                        }
                     }
                 }
             }
@@ -555,10 +589,10 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
     if (warp == 0) tc::tmem_dealloc(tm_s, 256);
 }
 
-template <int D, bool kHalf, bool kSel>
+template <int D, bool kHalf, bool kSel, bool kTree>
 cudaError_t launch_tile(const AttnArgs& a, cudaStream_t st) {
     constexpr int smem = SmemT<D>::kBytes;
-    auto* kernel = attn_tile_kernel<D, kHalf, kSel>;
+    auto* kernel = attn_tile_kernel<D, kHalf, kSel, kTree>;
     static std::atomic<uint64_t> allowed{0};
     const cudaError_t e = allow_smem(allowed, kernel, smem);
     if (e != cudaSuccess) return e;
@@ -568,15 +602,17 @@ cudaError_t launch_tile(const AttnArgs& a, cudaStream_t st) {
                       a);
 }
 
+template <int D, bool kHalf>
+cudaError_t launch_tile_d(const AttnArgs& a, cudaStream_t st) {
+    if (a.tree) return a.sel ? launch_tile<D, kHalf, true, true>(a, st) : launch_tile<D, kHalf, false, true>(a, st);
+    return a.sel ? launch_tile<D, kHalf, true, false>(a, st) : launch_tile<D, kHalf, false, false>(a, st);
+}
+
 }  // namespace
 
 cudaError_t launch_attn_tile(const AttnArgs& a, cudaStream_t st) {
-    if (a.head_dim == 128) {
-        if (a.ftype == IDX_FP16) return a.sel ? launch_tile<128, true, true>(a, st) : launch_tile<128, true, false>(a, st);
-        return a.sel ? launch_tile<128, false, true>(a, st) : launch_tile<128, false, false>(a, st);
-    }
-    if (a.ftype == IDX_FP16) return a.sel ? launch_tile<64, true, true>(a, st) : launch_tile<64, true, false>(a, st);
-    return a.sel ? launch_tile<64, false, true>(a, st) : launch_tile<64, false, false>(a, st);
+    if (a.head_dim == 128) return a.ftype == IDX_FP16 ? launch_tile_d<128, true>(a, st) : launch_tile_d<128, false>(a, st);
+    return a.ftype == IDX_FP16 ? launch_tile_d<64, true>(a, st) : launch_tile_d<64, false>(a, st);
 }
 
 }  // namespace idx

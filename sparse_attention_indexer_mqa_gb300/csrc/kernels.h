@@ -183,7 +183,8 @@ struct KvStoreArgs {
 };
 cudaError_t launch_kv_store(const KvStoreArgs& a, cudaStream_t st);
 
-// Attention over that cache (idx_attn_paged); strides in elements.
+// Attention over that cache (idx_attn_paged, idx_attn_tree); strides in elements.
+constexpr int32_t kTreeMaxNodes = 1024;  // nodes of a sequence: a bit of shared memory each
 struct AttnArgs {
     const uint16_t* q;
     int32_t ftype;
@@ -202,6 +203,10 @@ struct AttnArgs {
     const int32_t* sel;
     int64_t sel_stride;
     int32_t n_sel;
+    // a tree of drafted tokens: row t sees its sequence's node j where bit j of its mask is set (causal is 0 then)
+    const uint64_t* tree;  // [T][tree_stride], or NULL
+    int64_t tree_stride;
+    int32_t tree_words;
     float scale;
     uint16_t* out;
     int64_t out_row_stride, out_head_stride;
@@ -217,6 +222,89 @@ struct AttnArgs {
 int64_t attn_plan(AttnArgs& a, int64_t bytes);
 cudaError_t launch_attn(const AttnArgs& a, cudaStream_t st);
 cudaError_t launch_attn_tile(const AttnArgs& a, cudaStream_t st);  // many rows per kv head (attn_tc.cu)
+
+// Walk through trees of drafted tokens (idx_draft_verify); strides in elements.
+constexpr int32_t kVerifyMaxVocab = 1 << 20;  // a bit per token in shared memory
+struct VerifyArgs {
+    const void* target;  // [T][V]
+    const void* draft;   // [T][V], or NULL
+    int32_t ptype;
+    int64_t target_stride, draft_stride, T;
+    int32_t V;
+    const int32_t* tokens;
+    const int32_t* parents;
+    const float* coins;
+    const float* last;
+    const int32_t* cu_seqlens_q;
+    int32_t B, max_q_len, max_path;
+    int32_t* path;
+    int32_t* n_path;
+    int32_t* out_tokens;
+    int32_t* dev_status;
+};
+cudaError_t launch_draft_verify(const VerifyArgs& a, cudaStream_t st);
+
+// Accepted tokens moved together (idx_kv_compact, idx_k_compact).
+struct CompactArgs {
+    const int32_t* path;
+    int32_t max_path;
+    const int32_t* n_path;
+    const int32_t* seq_lens_k;
+    const int32_t* cu_seqlens_q;
+    int32_t B;
+    const int32_t* page_table;
+    int32_t pt_stride;
+    uint8_t* pool;
+    int32_t layers;
+    int64_t layer_stride, num_pages;
+    int32_t page_size;
+    int64_t page_stride;
+    int32_t kv_heads, head_dim;  // 8-bit KV cache
+    int32_t dtype;               // indexer's cache
+    int32_t* new_lens;
+    int32_t* dev_status;
+};
+cudaError_t launch_kv_compact(const CompactArgs& a, cudaStream_t st);
+cudaError_t launch_k_compact(const CompactArgs& a, cudaStream_t st);
+
+// Next rows of a page table out of the present ones (idx_pages_update), copies of pages (idx_pages_copy).
+constexpr int32_t kPagesMaxRows = 16384;  // 8 bytes each in shared memory
+struct PagesArgs {
+    const int32_t* parent;
+    const int32_t* keep;
+    int32_t n_out;
+    const int32_t* page_table;
+    int32_t pt_stride, B;
+    const int32_t* lens;
+    int32_t page_size;
+    int32_t* new_table;
+    int32_t new_stride;
+    int32_t* new_lens;
+    const int32_t* shares;
+    int32_t* new_shares;
+    int32_t num_pages;
+    const int32_t* free_pages;
+    int32_t free_cap;
+    const int32_t* free_span;
+    int32_t* new_free;
+    int32_t new_free_cap;
+    int32_t* new_span;
+    int32_t* copies;
+    int32_t* dev_status;
+};
+cudaError_t launch_pages_update(const PagesArgs& a, cudaStream_t st);
+struct CopyArgs {
+    const int32_t* copies;
+    int32_t n;
+    uint8_t* pool;
+    int32_t layers;
+    int64_t layer_stride, num_pages, page_bytes, page_stride;
+    int32_t* dev_status;
+};
+cudaError_t launch_pages_copy(const CopyArgs& a, cudaStream_t st);
+
+// Behind a kernel that writes lengths or page tables (meta.cu): returns when its output is visible.
+cudaError_t launch_done(cudaStream_t st);
 
 // Bounded-wait test hook (idx_debug_wait_timeout).
 cudaError_t launch_wait_timeout(int32_t limit_us, int32_t* status, cudaStream_t st);

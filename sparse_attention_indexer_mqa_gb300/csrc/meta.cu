@@ -158,6 +158,8 @@ __global__ void step_meta_done_kernel() { pdl_wait(); }
 
 }  // namespace
 
+cudaError_t launch_done(cudaStream_t st) { return launch_pdl(step_meta_done_kernel, dim3(1), dim3(32), 0, st); }
+
 cudaError_t launch_step_meta(const MetaArgs& a, cudaStream_t st) {
     // a thread per request for the sums where that fits, and a thread per row (512 requests, 66173 rows: 7.8 us, 11.8
     // with four rows a thread, the waiting kernel not counted)
@@ -171,7 +173,7 @@ cudaError_t launch_step_meta(const MetaArgs& a, cudaStream_t st) {
         if (s != cudaSuccess) return s;
     }
     const cudaError_t e = launch_k(false, step_meta_kernel, dim3((unsigned)ctas), dim3(threads), smem, st, a, rows);
-    return e == cudaSuccess ? launch_pdl(step_meta_done_kernel, dim3(1), dim3(32), 0, st) : e;
+    return e == cudaSuccess ? launch_done(st) : e;
 }
 
 }  // namespace idx
