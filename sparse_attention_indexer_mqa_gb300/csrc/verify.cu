@@ -9,9 +9,9 @@
 // running sum passes r times the row's sum. The last rejection's pass has left the sums that the search starts from.
 //
 // Sums. The draw looks for a border among a vocabulary's running sums, and with 2^17 of them an error of 2^-24 in each
-// would move one draw in a hundred. fp64 has a 64th of fp32's rate here, so weights and sums are pairs of fp32 (a
-// value and what its rounding lost, by error-free sums and products), about 2^-46 of the sum; only the few totals
-// and the search inside one warp's part are fp64.
+// would move one draw in a hundred. fp64 has a 64th of fp32's rate here (a few scalar operations of it in every warp
+// were most of a small call's time), so weights, sums and what is compared with them are pairs of fp32: a value and what its
+// rounding lost, by error-free sums and products, about 2^-46 of the sum. Two elements go through one packed instruction.
 //
 // A cluster of eight CTAs per request: the row is cut into eight slices, a slice into the CTA's warps' parts. All
 // threads follow the walk by themselves; a pass ends with one cluster barrier, behind which every CTA adds up the
@@ -32,19 +32,102 @@ namespace {
 
 constexpr int kCtasV = 8, kThreadsV = 256, kWarpsV = kThreadsV / 32;
 constexpr int kNodes = kThreadsV;  // nodes that are staged at once
+constexpr int kAhead = 2;          // vectors of either row that a thread has in flight
 
-// A sum and what its roundings lost.
+// A value and what its roundings lost: hi + lo.
 struct Pair {
     float hi, lo;
 };
 __device__ __forceinline__ void add(Pair& s, float x) {  // s.hi + x exactly, as a sum and its error
     const float t = __fadd_rn(s.hi, x), b = __fsub_rn(t, s.hi);
-    s.lo += __fadd_rn(__fsub_rn(s.hi, __fsub_rn(t, b)), __fsub_rn(x, b));
+    s.lo = __fadd_rn(s.lo, __fadd_rn(__fsub_rn(s.hi, __fsub_rn(t, b)), __fsub_rn(x, b)));
     s.hi = t;
 }
 __device__ __forceinline__ void add(Pair& s, const Pair& x) {
     add(s, x.hi);
-    s.lo += x.lo;
+    s.lo = __fadd_rn(s.lo, x.lo);
+}
+__device__ __forceinline__ Pair tidy(const Pair& x) {  // hi the nearest fp32 of the whole
+    const float t = __fadd_rn(x.hi, x.lo);
+    return Pair{t, __fsub_rn(x.lo, __fsub_rn(t, x.hi))};
+}
+__device__ __forceinline__ Pair times(const Pair& x, float y) {
+    const float t = __fmul_rn(x.hi, y);
+    return Pair{t, __fmaf_rn(x.lo, y, __fmaf_rn(x.hi, y, -t))};
+}
+__device__ __forceinline__ Pair less(const Pair& x, const Pair& y) {  // x - y
+    Pair d = x;
+    add(d, Pair{-y.hi, -y.lo});
+    return d;
+}
+__device__ __forceinline__ bool positive(const Pair& x) { return __fadd_rn(x.hi, x.lo) > 0.0f; }
+
+// The sum of lanes 0 .. n - 1's, the same in every lane (each lane's own would differ in the last bits).
+template <int n>
+__device__ __forceinline__ Pair lane0_sum(Pair x) {
+#pragma unroll
+    for (int o = n / 2; o > 0; o >>= 1) {
+        const Pair y{__shfl_down_sync(kFull, x.hi, o), __shfl_down_sync(kFull, x.lo, o)};
+        add(x, y);
+    }
+    return Pair{__shfl_sync(kFull, x.hi, 0), __shfl_sync(kFull, x.lo, 0)};
+}
+__device__ __forceinline__ Pair running_sum(Pair x) {  // of lanes 0 .. this one
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const Pair y{__shfl_up_sync(kFull, x.hi, o), __shfl_up_sync(kFull, x.lo, o)};
+        if ((threadIdx.x & 31) >= o) add(x, y);
+    }
+    return x;
+}
+
+// Lane i holds the sum of part i. The first part behind whose end the running sum is past the goal, or else the last that
+// holds anything (0 if none does); the goal loses what lies in front of that part. The same in every lane.
+__device__ __forceinline__ int first_past(const Pair& x, Pair& goal) {
+    const Pair upto = running_sum(x);
+    const unsigned some = __ballot_sync(kFull, positive(x));
+    const unsigned past = __ballot_sync(kFull, positive(x) && positive(less(upto, goal)));
+    const int part = past ? __ffs(past) - 1 : some ? 31 - __clz(some) : 0;
+    const Pair front{__shfl_sync(kFull, upto.hi, max(part - 1, 0)), __shfl_sync(kFull, upto.lo, max(part - 1, 0))};
+    if (part) goal = less(goal, front);
+    return part;
+}
+
+// Two values in one instruction, each rounded as by itself.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+        " fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n"
+        " add.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n"
+        " mul.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) { return fma2(b, make_float2(-1.0f, -1.0f), a); }
+
+// Two pairs.
+struct Pair2 {
+    float2 hi, lo;
+};
+__device__ __forceinline__ void add(Pair2& s, const Pair2& x) {
+    const float2 t = add2(s.hi, x.hi), b = sub2(t, s.hi);
+    s.lo = add2(s.lo, add2(add2(sub2(s.hi, sub2(t, b)), sub2(x.hi, b)), x.lo));
+    s.hi = t;
 }
 
 __device__ __forceinline__ float to_float(float x) { return x; }
@@ -66,22 +149,28 @@ struct Row {
     __device__ __forceinline__ int off() const { return (int)((reinterpret_cast<uintptr_t>(at) / sizeof(T)) % kVec); }
 };
 
-// Elements e0 .. e0 + kVec - 1 of a row of V; those outside it are 0. whole: e0 lies on a 16-byte boundary.
+// Element by element, for a vector that the row's end cuts or that lies on no 16-byte boundary.
 template <typename T>
-__device__ __forceinline__ void load(const T* row, int e0, int V, bool whole, bool& bad, float (&x)[16 / sizeof(T)]) {
+__device__ __forceinline__ uint4 gather(const T* row, int e0, int V) {
     constexpr int kVec = 16 / sizeof(T);
-    if (whole && e0 >= 0 && e0 + kVec <= V) {
-        const uint4 w = __ldg(reinterpret_cast<const uint4*>(row + e0));
-        const T* t = reinterpret_cast<const T*>(&w);
+    uint4 w = make_uint4(0, 0, 0, 0);
+    T* t = reinterpret_cast<T*>(&w);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) x[i] = to_float(t[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) x[i] = e0 + i >= 0 && e0 + i < V ? to_float(row[e0 + i]) : 0.0f;
-    }
+    for (int i = 0; i < kVec; ++i)
+        if (e0 + i >= 0 && e0 + i < V) t[i] = row[e0 + i];
+    return w;
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack(const uint4& w, bool& bad, float (&x)[16 / sizeof(T)]) {
+    constexpr int kVec = 16 / sizeof(T);
+    const T* t = reinterpret_cast<const T*>(&w);
     uint32_t worst = 0;  // as bits, what is negative, infinite or NaN is above every other
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) worst = max(worst, __float_as_uint(x[i]));
+    for (int i = 0; i < kVec; ++i) {
+        x[i] = to_float(t[i]);
+        worst = max(worst, __float_as_uint(x[i]));
+    }
     if (worst >= 0x7f800000u) {
 #pragma unroll
         for (int i = 0; i < kVec; ++i) x[i] = clean(x[i], bad);
@@ -89,13 +178,14 @@ __device__ __forceinline__ void load(const T* row, int e0, int V, bool whole, bo
 }
 
 template <typename T, bool kDrafter>
-__global__ void __cluster_dims__(kCtasV, 1, 1) __launch_bounds__(kThreadsV) draft_verify_kernel(const VerifyArgs a) {
+__global__ void __cluster_dims__(kCtasV, 1, 1) __launch_bounds__(kThreadsV, 4) draft_verify_kernel(const VerifyArgs a) {
     constexpr int kVec = Row<T>::kVec;
     extern __shared__ uint32_t gone[];  // without a drafter: a bit for each token of the CTA's slice that was rejected
     __shared__ int node_parent[kNodes], node_token[kNodes];
     __shared__ float node_coin[kNodes], node_p[kNodes], node_q[kNodes];
-    __shared__ double warp_sum[kWarpsV];
-    __shared__ double cta_sum[2];  // of this pass and the last one, which another CTA may still read
+    __shared__ Pair warp_sum[kWarpsV];
+    __shared__ Pair cta_sum[2];  // of this pass and the last one, which another CTA may still read
+    __shared__ int first_thread, last_thread;
     cg::cluster_group cluster = cg::this_cluster();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = (int)cluster.block_rank();
     const int b = blockIdx.x / kCtasV;
@@ -144,9 +234,14 @@ __global__ void __cluster_dims__(kCtasV, 1, 1) __launch_bounds__(kThreadsV) draf
     int cur = 0, pass = 0, from = 0;
     const T* p = target;
     const T* q = draft;
-    // the vectors of the row, this CTA's and this warp's
-    int off = 0, k0 = 0, k1 = 0, e_first = 0;
+    // the row's vectors: this CTA's slice, a warp's part of it
+    int off = 0, s0 = 0, s1 = 0, k0 = 0, k1 = 0;
     bool q_whole = false;
+    auto part_of = [&](int w) {
+        const int part = (s1 - s0 + kWarpsV - 1) / kWarpsV;
+        k0 = min(s0 + w * part, s1);
+        k1 = min(k0 + part, s1);
+    };
     auto place = [&]() {
         p = target + (int64_t)cur * a.target_stride;
         off = Row<T>{p}.off();
@@ -155,78 +250,94 @@ __global__ void __cluster_dims__(kCtasV, 1, 1) __launch_bounds__(kThreadsV) draf
             q_whole = Row<T>{q}.off() == off;
         }
         const int all = (V + off + kVec - 1) / kVec, slice = (all + kCtasV - 1) / kCtasV;
-        const int s0 = min(rank * slice, all), s1 = min(s0 + slice, all), part = (s1 - s0 + kWarpsV - 1) / kWarpsV;
-        k0 = min(s0 + warp * part, s1);
-        k1 = min(k0 + part, s1);
-        e_first = s0 * kVec - off;  // of the CTA
+        s0 = min(rank * slice, all);
+        s1 = min(s0 + slice, all);
+        part_of(warp);
     };
-    // weights of vector k: p, without the rejected tokens (mask) or less cut times q (c_hi + c_lo)
-    auto weights = [&](int k, int how, float c_hi, float c_lo, Pair (&w)[kVec]) {
+    // Vector k of either row, as it is in memory. Only a row's first and last vector may be cut by its ends.
+    auto cut_short = [&](int k) { return k * kVec < off || (k + 1) * kVec - off > V; };
+    auto fetch = [&](int k, int how, uint4& x, uint4& y) {
+        const int e0 = k * kVec - off;
+        const bool cut_off = cut_short(k);
+        x = y = make_uint4(0, 0, 0, 0);
+        if (!cut_off) x = __ldg(reinterpret_cast<const uint4*>(p + e0));
+        if (kDrafter && how && !cut_off && q_whole) y = __ldg(reinterpret_cast<const uint4*>(q + e0));
+    };
+    auto fetch_rest = [&](int k, int how, uint4& x, uint4& y) {
+        const bool cut_off = cut_short(k);
+        if (cut_off) x = gather(p, k * kVec - off, V);
+        if (kDrafter && how && (cut_off || !q_whole)) y = gather(q, k * kVec - off, V);
+    };
+    // its weights, two to a Pair2: p, without the rejected tokens or less cut times q
+    auto weights = [&](int k, int how, const Pair& cut, const uint4& px, const uint4& qx, Pair2 (&w)[kVec / 2]) {
         const int e0 = k * kVec - off;
         float x[kVec];
-        load<T>(p, e0, V, true, bad, x);
+        unpack<T>(px, bad, x);
         if (kDrafter && how) {
             float y[kVec];
-            load<T>(q, e0, V, q_whole, bad, y);
+            unpack<T>(qx, bad, y);
+            const float2 c = make_float2(cut.hi, cut.hi), c_lo = make_float2(cut.lo, cut.lo), nc = make_float2(-cut.hi, -cut.hi);
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) {
-                const float t = __fmul_rn(c_hi, y[i]), te = __fmaf_rn(c_lo, y[i], __fmaf_rn(c_hi, y[i], -t));
-                const float d = __fsub_rn(x[i], t), z = __fsub_rn(d, x[i]);
-                const float e = __fsub_rn(__fsub_rn(__fsub_rn(x[i], __fsub_rn(d, z)), __fadd_rn(t, z)), te);
-                const bool some = __fadd_rn(d, e) > 0.0f;
-                w[i] = Pair{some ? d : 0.0f, some ? e : 0.0f};
+            for (int i = 0; i < kVec / 2; ++i) {
+                const float2 x2 = make_float2(x[2 * i], x[2 * i + 1]), y2 = make_float2(y[2 * i], y[2 * i + 1]);
+                const float2 nt = mul2(nc, y2), te = fma2(c_lo, y2, fma2(c, y2, nt));  // cut * y = te - nt
+                const float2 d = add2(x2, nt), z = sub2(d, x2);
+                const float2 e = sub2(add2(sub2(x2, sub2(d, z)), sub2(nt, z)), te);
+                const float2 s = add2(d, e);
+                w[i].hi = make_float2(s.x > 0.0f ? d.x : 0.0f, s.y > 0.0f ? d.y : 0.0f);
+                w[i].lo = make_float2(s.x > 0.0f ? e.x : 0.0f, s.y > 0.0f ? e.y : 0.0f);
             }
         } else {
+            if (!kDrafter && how) {
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) {
-                if (!kDrafter && how) {
-                    const int v = max(e0 + i, 0) - max(e_first, 0);
+                for (int i = 0; i < kVec; ++i) {
+                    const int v = e0 + i - max(s0 * kVec - off, 0);
                     if (e0 + i >= 0 && e0 + i < V && (gone[v >> 5] >> (v & 31)) & 1u) x[i] = 0.0f;
                 }
-                w[i] = Pair{x[i], 0.0f};
             }
+#pragma unroll
+            for (int i = 0; i < kVec / 2; ++i) w[i] = Pair2{make_float2(x[2 * i], x[2 * i + 1]), make_float2(0.0f, 0.0f)};
         }
     };
-    double before_cta = 0.0;  // sums of the slices in front of this CTA's
-    auto total = [&](int how, double cut) -> double {
-        const float c_hi = (float)cut, c_lo = (float)(cut - (double)c_hi);
-        Pair s[4] = {};
-#pragma unroll 4
-        for (int k = k0 + lane; k < k1; k += 32) {
-            Pair w[kVec];
-            weights(k, how, c_hi, c_lo, w);
+    auto total = [&](int how, const Pair& cut) -> Pair {
+        Pair2 s[2] = {};
+        for (int k = k0 + lane; k < k1; k += 32 * kAhead) {
+            uint4 x[kAhead], y[kAhead];
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) add(s[i & 3], w[i]);
+            for (int u = 0; u < kAhead; ++u) {  // past the part's end its last vector again, which is not counted
+                fetch(min(k + 32 * u, k1 - 1), how, x[u], y[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                if (k + 32 * u >= k1) break;
+                fetch_rest(k + 32 * u, how, x[u], y[u]);
+                Pair2 w[kVec / 2];
+                weights(k + 32 * u, how, cut, x[u], y[u], w);
+#pragma unroll
+                for (int i = 0; i < kVec / 2; ++i) add(s[i & 1], w[i]);
+            }
         }
         add(s[0], s[1]);
-        add(s[2], s[3]);
-        add(s[0], s[2]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const Pair y{__shfl_xor_sync(kFull, s[0].hi, o), __shfl_xor_sync(kFull, s[0].lo, o)};
-            add(s[0], y);
-        }
+        Pair mine{s[0].hi.x, s[0].lo.x};
+        add(mine, Pair{s[0].hi.y, s[0].lo.y});
+        mine = lane0_sum<32>(mine);
         __syncthreads();  // warp_sum has been read
-        if (lane == 0) warp_sum[warp] = (double)s[0].hi + (double)s[0].lo;
+        if (lane == 0) warp_sum[warp] = mine;
         __syncthreads();
-        if (tid == 0) {
-            double t = 0.0;
-            for (int w = 0; w < kWarpsV; ++w) t += warp_sum[w];
-            cta_sum[pass & 1] = t;
+        if (warp == 0) {
+            const Pair x = lane0_sum<kWarpsV>(warp_sum[lane % kWarpsV]);
+            if (lane == 0) cta_sum[pass & 1] = x;
         }
         cluster.sync();
-        double t = 0.0;
-        for (int c = 0; c < kCtasV; ++c) {
-            if (c == rank) before_cta = t;
-            t += *cluster.map_shared_rank(&cta_sum[pass & 1], c);
-        }
+        const Pair x = lane0_sum<kCtasV>(*cluster.map_shared_rank(&cta_sum[pass & 1], lane % kCtasV));
         ++pass;
-        return t;
+        return tidy(x);
     };
 
     // ---- the walk -----------------------------------------------------------------------------------------------
     int length = 1, rejected = 0;
-    double cut = 0.0, mass = 1.0;
+    const Pair zero{0.0f, 0.0f}, one{1.0f, 0.0f};
+    Pair cut = zero, mass = one;
     const bool writes = rank == 0 && tid == 0;
     if (writes) path[0] = 0;
     from = stage(0);
@@ -252,15 +363,20 @@ __global__ void __cluster_dims__(kCtasV, 1, 1) __launch_bounds__(kThreadsV) draf
             bad_token = true;
             continue;
         }
-        const double u = node_coin[child - from];
-        double px = clean(node_p[child - from], bad);
+        const float u = node_coin[child - from];
+        float px = clean(node_p[child - from], bad);
         bool yes;
         if constexpr (kDrafter) {
-            const double qx = clean(node_q[child - from], bad);
-            yes = __dmul_rn(__dmul_rn(u, qx), mass) < __dsub_rn(px, __dmul_rn(cut, qx));
+            const float qx = clean(node_q[child - from], bad);
+            // u q S < p - c q; a coin that is no number rejects
+            const float uq = __fmul_rn(u, qx);
+            Pair need = times(mass, uq);
+            add(need, __fmul_rn(mass.hi, __fmaf_rn(u, qx, -uq)));
+            yes = positive(less(less(Pair{px, 0.0f}, times(cut, qx)), need));
             if (!yes) {
                 if (!rejected) place();
-                cut += mass;
+                add(cut, mass);
+                cut = tidy(cut);
                 mass = total(1, cut);
             }
         } else {
@@ -268,12 +384,15 @@ __global__ void __cluster_dims__(kCtasV, 1, 1) __launch_bounds__(kThreadsV) draf
             for (int i = cur + 1; rejected && i < child; i += 32) {
                 const bool same = i + lane < child && a.parents[c0 + i + lane] == cur && a.tokens[c0 + i + lane] == x;
                 if (__any_sync(kFull, same)) {
-                    px = 0.0;
+                    px = 0.0f;
                     break;
                 }
             }
-            yes = __dmul_rn(u, mass) < px;
-            if (!yes) mass = mass > px ? mass - px : 0.0;
+            yes = positive(less(Pair{px, 0.0f}, times(mass, u)));
+            if (!yes) {
+                add(mass, -px);
+                mass = positive(mass) ? tidy(mass) : zero;
+            }
         }
         if (!yes) {
             ++rejected;
@@ -285,18 +404,18 @@ __global__ void __cluster_dims__(kCtasV, 1, 1) __launch_bounds__(kThreadsV) draf
         }
         ++length;
         cur = child;
-        cut = 0.0;
-        mass = 1.0;
+        cut = zero;
+        mass = one;
         rejected = 0;
     }
 
     // ---- the draw -----------------------------------------------------------------------------------------------
     int how = rejected ? 1 : 0;
-    double all = mass;
+    Pair all = mass;
     if (!kDrafter || !rejected) {
         place();
         if (!kDrafter && rejected) {
-            const int v0 = max(e_first, 0), slice = ((V + off + kVec - 1) / kVec + kCtasV - 1) / kCtasV * kVec;
+            const int v0 = max(s0 * kVec - off, 0), slice = ((V + off + kVec - 1) / kVec + kCtasV - 1) / kCtasV * kVec;
             for (int i = tid; i < (slice + 31) / 32; i += kThreadsV) gone[i] = 0;
             __syncthreads();
             for (int i = cur + 1 + tid; i < n; i += kThreadsV) {
@@ -307,84 +426,73 @@ __global__ void __cluster_dims__(kCtasV, 1, 1) __launch_bounds__(kThreadsV) draf
         }
         all = total(how, cut);
     }
-    if (!(all > 0.0)) {  // nothing is left of p: p itself
+    if (!positive(all)) {  // nothing is left of p: p itself
         how = 0;
-        all = total(0, 0.0);
+        all = total(0, zero);
     }
     float r = a.last[b];
     const bool bad_coin = !(r >= 0.0f && r < 1.0f);
     if (!(r >= 0.0f)) r = 0.0f;
-    const double goal = __dmul_rn((double)r, all);
-    // the CTA, and in it the warp, whose part holds the border; with r >= 1 the last that holds anything
-    int owner = 0;
-    {
-        double t = 0.0;
-        for (int c = 0; c < kCtasV; ++c) {
-            const double x = *cluster.map_shared_rank(&cta_sum[(pass - 1) & 1], c);
-            if (x > 0.0) owner = c;
-            t += x;
-            if (t > goal) break;
-        }
-    }
+    Pair goal = times(all, r);  // passed by a sum that is above it
+    // The border: the CTA's slice that holds it, the warp's part in that, a thread's piece of that, the element. Where
+    // rounding or r >= 1 puts the goal behind everything, the last one that weighs anything.
+    const int owner = first_past(lane < kCtasV ? *cluster.map_shared_rank(&cta_sum[(pass - 1) & 1], lane % kCtasV) : zero, goal);
     if (rank == owner) {
-        int at = 0;
-        double before = before_cta, t = before_cta;
-        for (int w = 0; w < kWarpsV; ++w) {
-            if (warp_sum[w] > 0.0) {
-                at = w;
-                before = t;
+        part_of(first_past(lane < kWarpsV ? warp_sum[lane % kWarpsV] : zero, goal));
+        const int piece = (k1 - k0 + kThreadsV - 1) / kThreadsV, a0 = min(k0 + tid * piece, k1), a1 = min(a0 + piece, k1);
+        auto vector = [&](int k, Pair2 (&x)[kVec / 2]) {
+            uint4 px, qx;
+            fetch(k, how, px, qx);
+            fetch_rest(k, how, px, qx);
+            weights(k, how, cut, px, qx, x);
+        };
+        Pair s = zero;
+        for (int k = a0; k < a1; ++k) {
+            Pair2 x[kVec / 2];
+            vector(k, x);
+#pragma unroll
+            for (int i = 0; i < kVec / 2; ++i) {
+                add(s, Pair{x[i].hi.x, x[i].lo.x});
+                add(s, Pair{x[i].hi.y, x[i].lo.y});
             }
-            t += warp_sum[w];
-            if (t > goal) break;
         }
-        if (warp == at) {
-            const float c_hi = (float)cut, c_lo = (float)(cut - (double)c_hi);
+        const Pair upto = running_sum(s);
+        __syncthreads();  // every warp has read warp_sum
+        if (lane == 31) warp_sum[warp] = upto;
+        if (tid == 0) {
+            first_thread = kThreadsV;
+            last_thread = -1;
+        }
+        __syncthreads();
+        for (int x = 0; x < warp; ++x) goal = less(goal, warp_sum[x]);
+        const unsigned some = __ballot_sync(kFull, positive(s));
+        const unsigned past = __ballot_sync(kFull, positive(s) && positive(less(upto, goal)));
+        if (lane == 0) {
+            if (past) atomicMin(&first_thread, warp * 32 + __ffs(past) - 1);
+            if (some) atomicMax(&last_thread, warp * 32 + 31 - __clz(some));
+        }
+        __syncthreads();
+        const int mine = first_thread < kThreadsV ? first_thread : max(last_thread, 0);
+        if (tid == mine) {
             int found = -1;
-            for (int k = k0; k < k1; k += 32) {
-                Pair w[kVec];
-                double x = 0.0;
-                int last = -1;  // this lane's last element that weighs anything
-                if (k + lane < k1) {
-                    weights(k + lane, how, c_hi, c_lo, w);
+            bool done = false;
+            Pair t = less(upto, s);
+            for (int k = a0; k < a1 && !done; ++k) {
+                Pair2 x[kVec / 2];
+                vector(k, x);
 #pragma unroll
-                    for (int i = 0; i < kVec; ++i) {
-                        x += (double)w[i].hi + (double)w[i].lo;
-                        if (__fadd_rn(w[i].hi, w[i].lo) > 0.0f) last = i;
+                for (int i = 0; i < kVec; ++i) {
+                    const Pair w = i & 1 ? Pair{x[i / 2].hi.y, x[i / 2].lo.y} : Pair{x[i / 2].hi.x, x[i / 2].lo.x};
+                    add(t, w);
+                    if (!done && positive(w)) {
+                        found = k * kVec - off + i;
+                        done = positive(less(t, goal));
                     }
                 }
-                double upto = x;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const double y = __shfl_up_sync(kFull, upto, o);
-                    if (lane >= o) upto += y;
-                }
-                const unsigned passes = __ballot_sync(kFull, last >= 0 && before + upto > goal);
-                const unsigned some = __ballot_sync(kFull, last >= 0);
-                if (!passes) {
-                    if (some) found = (k + 31 - __clz(some)) * kVec - off + __shfl_sync(kFull, last, 31 - __clz(some));
-                    before += __shfl_sync(kFull, upto, 31);
-                    continue;
-                }
-                const int l = __ffs(passes) - 1;
-                if (lane == l) {
-                    double t2 = before + (upto - x);
-                    int hit = last;
-#pragma unroll
-                    for (int i = kVec - 1; i >= 0; --i) {
-                        double s = t2;
-                        for (int m = 0; m <= i; ++m) s += (double)w[m].hi + (double)w[m].lo;
-                        if (__fadd_rn(w[i].hi, w[i].lo) > 0.0f && s > goal) hit = i;
-                    }
-                    found = (k + l) * kVec - off + hit;
-                }
-                found = __shfl_sync(kFull, found, l);
-                break;
             }
-            if (lane == 0) {
-                out[length - 1] = found;
-                a.n_path[b] = length;
-                if (found < 0 || bad_coin || bad_token) report(a.dev_status, IDX_STATUS_BAD_VALUE);
-            }
+            out[length - 1] = found;
+            a.n_path[b] = length;
+            if (found < 0 || bad_coin || bad_token) report(a.dev_status, IDX_STATUS_BAD_VALUE);
         }
     }
     if (rank == 0) {
