@@ -11,15 +11,17 @@
 // Sums. The draw looks for a border among a vocabulary's running sums, and with 2^17 of them an error of 2^-24 in each
 // would move one draw in a hundred. fp64 has a 64th of fp32's rate here (a few scalar operations of it in every warp
 // were most of a small call's time), so weights, sums and what is compared with them are pairs of fp32: a value and what its
-// rounding lost, by error-free sums and products, about 2^-46 of the sum. Two elements go through one packed instruction.
+// rounding lost, by error-free sums and products, about 2^-46 of the sum.
 //
-// A cluster of eight CTAs per request: the row is cut into eight slices, a slice into the CTA's warps' parts. All
+// A cluster of up to eight CTAs per request: the row is cut into a slice for each, a slice into the CTA's warps' parts. All
 // threads follow the walk by themselves; a pass ends with one cluster barrier, behind which every CTA adds up the
-// eight totals in the same order. What the walk asks of each node (its parent, token, number and the two
-// probabilities) is fetched for 256 nodes at once, so that a step between passes is no chain of loads.
+// slices' sums in the same order. What the walk asks of each node (its parent, token, number and the two
+// probabilities) is fetched for 1024 nodes at once, so that a step between passes is no chain of loads.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -30,9 +32,9 @@ namespace idx {
 
 namespace {
 
-constexpr int kCtasV = 8, kThreadsV = 256, kWarpsV = kThreadsV / 32;
+constexpr int kThreadsV = 512, kWarpsV = kThreadsV / 32, kCtasMost = 8;
 constexpr int kNodes = kThreadsV;  // nodes that are staged at once
-constexpr int kAhead = 2;          // vectors of either row that a thread has in flight
+constexpr int kAhead = 4;          // vectors of either row that a thread has on their way
 
 // A value and what its roundings lost: hi + lo.
 struct Pair {
@@ -63,7 +65,7 @@ __device__ __forceinline__ Pair less(const Pair& x, const Pair& y) {  // x - y
 __device__ __forceinline__ bool positive(const Pair& x) { return __fadd_rn(x.hi, x.lo) > 0.0f; }
 
 // The sum of lanes 0 .. n - 1's, the same in every lane (each lane's own would differ in the last bits).
-template <int n>
+template <int n = 32>
 __device__ __forceinline__ Pair lane0_sum(Pair x) {
 #pragma unroll
     for (int o = n / 2; o > 0; o >>= 1) {
@@ -93,43 +95,6 @@ __device__ __forceinline__ int first_past(const Pair& x, Pair& goal) {
     return part;
 }
 
-// Two values in one instruction, each rounded as by itself.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
-        " fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    float2 d;
-    asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n"
-        " add.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 d;
-    asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n"
-        " mul.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-__device__ __forceinline__ float2 sub2(float2 a, float2 b) { return fma2(b, make_float2(-1.0f, -1.0f), a); }
-
-// Two pairs.
-struct Pair2 {
-    float2 hi, lo;
-};
-__device__ __forceinline__ void add(Pair2& s, const Pair2& x) {
-    const float2 t = add2(s.hi, x.hi), b = sub2(t, s.hi);
-    s.lo = add2(s.lo, add2(add2(sub2(s.hi, sub2(t, b)), sub2(x.hi, b)), x.lo));
-    s.hi = t;
-}
-
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
@@ -139,6 +104,17 @@ __device__ __forceinline__ float clean(float x, bool& bad) {
     const bool ok = x >= 0.0f && x < __int_as_float(0x7f800000);
     bad |= !ok;
     return ok ? x : 0.0f;
+}
+// A vector with such an entry: a call, for it is rare and its code would be fetched by every small call.
+template <typename T>
+__device__ __noinline__ uint4 clean_vector(uint4 w, int32_t* status) {
+    constexpr int kVec = 16 / sizeof(T);
+    T* t = reinterpret_cast<T*>(&w);
+    bool bad = false;
+    for (int i = 0; i < kVec; ++i)
+        if (!(clean(to_float(t[i]), bad) > 0.0f)) t[i] = T(0.0f);
+    if (bad) report(status, IDX_STATUS_BAD_VALUE);
+    return w;
 }
 
 // Vectors of a row: 16 bytes each where the row's address allows; vector k holds elements k * kVec - off ..
@@ -151,7 +127,7 @@ struct Row {
 
 // Element by element, for a vector that the row's end cuts or that lies on no 16-byte boundary.
 template <typename T>
-__device__ __forceinline__ uint4 gather(const T* row, int e0, int V) {
+__device__ __noinline__ uint4 gather(const T* row, int e0, int V) {
     constexpr int kVec = 16 / sizeof(T);
     uint4 w = make_uint4(0, 0, 0, 0);
     T* t = reinterpret_cast<T*>(&w);
@@ -162,33 +138,47 @@ __device__ __forceinline__ uint4 gather(const T* row, int e0, int V) {
 }
 
 template <typename T>
-__device__ __forceinline__ void unpack(const uint4& w, bool& bad, float (&x)[16 / sizeof(T)]) {
-    constexpr int kVec = 16 / sizeof(T);
-    const T* t = reinterpret_cast<const T*>(&w);
-    uint32_t worst = 0;  // as bits, what is negative, infinite or NaN is above every other
+__device__ __forceinline__ void unpack(const uint4& w, float (&x)[16 / sizeof(T)]) {
+#pragma unroll
+    for (int i = 0; i < 16 / (int)sizeof(T); ++i) x[i] = to_float(reinterpret_cast<const T*>(&w)[i]);
+}
+
+// How a pass weighs an entry: p as it is, p less q (a node's first pass, the only one of most), p less cut times q,
+// p without the rejected tokens.
+enum { kAll, kLessQ, kLessCutQ, kWithout };
+
+// The weights of a vector's entries, which have to be probabilities; gone: a bit for each that was rejected.
+template <int kHow, int kVec>
+__device__ __forceinline__ void weigh(const Pair& cut, uint32_t gone, const float (&x)[kVec], const float (&y)[kVec], Pair (&w)[kVec]) {
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
-        x[i] = to_float(t[i]);
-        worst = max(worst, __float_as_uint(x[i]));
-    }
-    if (worst >= 0x7f800000u) {
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) x[i] = clean(x[i], bad);
+        if constexpr (kHow == kLessQ) {  // held to x, q leaves no negative difference, and its error takes two operations
+            const float t = fminf(y[i], x[i]), d = __fsub_rn(x[i], t);
+            w[i] = Pair{d, __fsub_rn(__fsub_rn(x[i], d), t)};
+        } else if constexpr (kHow == kLessCutQ) {  // so does this one's where x is larger or nearly so; elsewhere it weighs nothing
+            const float c = __fmul_rn(cut.hi, y[i]), ce = __fmaf_rn(cut.lo, y[i], __fmaf_rn(cut.hi, y[i], -c));
+            const float d = __fsub_rn(x[i], c), e = __fsub_rn(__fsub_rn(__fsub_rn(x[i], d), c), ce);
+            const bool some = __fadd_rn(d, e) > 0.0f;
+            w[i] = Pair{some ? d : 0.0f, some ? e : 0.0f};
+        } else {
+            w[i] = Pair{kHow == kWithout && (gone >> i) & 1u ? 0.0f : x[i], 0.0f};
+        }
     }
 }
 
 template <typename T, bool kDrafter>
-__global__ void __cluster_dims__(kCtasV, 1, 1) __launch_bounds__(kThreadsV, 4) draft_verify_kernel(const VerifyArgs a) {
+__global__ void __launch_bounds__(kThreadsV, 2) draft_verify_kernel(const VerifyArgs a) {
     constexpr int kVec = Row<T>::kVec;
-    extern __shared__ uint32_t gone[];  // without a drafter: a bit for each token of the CTA's slice that was rejected
+    // without a drafter: a bit for each token of the CTA's slice that was rejected, from the slice's first vector on
+    extern __shared__ uint32_t gone[];
     __shared__ int node_parent[kNodes], node_token[kNodes];
     __shared__ float node_coin[kNodes], node_p[kNodes], node_q[kNodes];
     __shared__ Pair warp_sum[kWarpsV];
     __shared__ Pair cta_sum[2];  // of this pass and the last one, which another CTA may still read
     __shared__ int first_thread, last_thread;
     cg::cluster_group cluster = cg::this_cluster();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = (int)cluster.block_rank();
-    const int b = blockIdx.x / kCtasV;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank(), b = blockIdx.x / ctas;
     pdl_wait();
     pdl_launch_dependents();
     const int32_t c0 = a.cu_seqlens_q[b], c1 = a.cu_seqlens_q[b + 1], n = c1 - c0;
@@ -209,6 +199,7 @@ __global__ void __cluster_dims__(kCtasV, 1, 1) __launch_bounds__(kThreadsV, 4) d
     const T* target = static_cast<const T*>(a.target) + (int64_t)c0 * a.target_stride;
     const T* draft = kDrafter ? static_cast<const T*>(a.draft) + (int64_t)c0 * a.draft_stride : nullptr;
     const int V = a.V;
+    const Pair zero{0.0f, 0.0f}, one{1.0f, 0.0f};
     bool bad = false, bad_token = false;
 
     // Nodes from .. from + kNodes - 1, each with what its parent's rows say of its token. Values of nodes that are never
@@ -249,94 +240,123 @@ __global__ void __cluster_dims__(kCtasV, 1, 1) __launch_bounds__(kThreadsV, 4) d
             q = draft + (int64_t)cur * a.draft_stride;
             q_whole = Row<T>{q}.off() == off;
         }
-        const int all = (V + off + kVec - 1) / kVec, slice = (all + kCtasV - 1) / kCtasV;
+        const int all = (V + off + kVec - 1) / kVec, slice = (all + ctas - 1) / ctas;
         s0 = min(rank * slice, all);
         s1 = min(s0 + slice, all);
         part_of(warp);
     };
-    // Vector k of either row, as it is in memory. Only a row's first and last vector may be cut by its ends.
+    // Vector k of either row, as it is in memory; only a row's first and last one may be cut by its ends.
     auto cut_short = [&](int k) { return k * kVec < off || (k + 1) * kVec - off > V; };
-    auto fetch = [&](int k, int how, uint4& x, uint4& y) {
+    auto fetch_p = [&](int k) -> uint4 {
         const int e0 = k * kVec - off;
-        const bool cut_off = cut_short(k);
-        x = y = make_uint4(0, 0, 0, 0);
-        if (!cut_off) x = __ldg(reinterpret_cast<const uint4*>(p + e0));
-        if (kDrafter && how && !cut_off && q_whole) y = __ldg(reinterpret_cast<const uint4*>(q + e0));
+        return cut_short(k) ? gather(p, e0, V) : __ldg(reinterpret_cast<const uint4*>(p + e0));
     };
-    auto fetch_rest = [&](int k, int how, uint4& x, uint4& y) {
-        const bool cut_off = cut_short(k);
-        if (cut_off) x = gather(p, k * kVec - off, V);
-        if (kDrafter && how && (cut_off || !q_whole)) y = gather(q, k * kVec - off, V);
-    };
-    // its weights, two to a Pair2: p, without the rejected tokens or less cut times q
-    auto weights = [&](int k, int how, const Pair& cut, const uint4& px, const uint4& qx, Pair2 (&w)[kVec / 2]) {
+    auto fetch_q = [&](int k) -> uint4 {
         const int e0 = k * kVec - off;
-        float x[kVec];
-        unpack<T>(px, bad, x);
-        if (kDrafter && how) {
-            float y[kVec];
-            unpack<T>(qx, bad, y);
-            const float2 c = make_float2(cut.hi, cut.hi), c_lo = make_float2(cut.lo, cut.lo), nc = make_float2(-cut.hi, -cut.hi);
-#pragma unroll
-            for (int i = 0; i < kVec / 2; ++i) {
-                const float2 x2 = make_float2(x[2 * i], x[2 * i + 1]), y2 = make_float2(y[2 * i], y[2 * i + 1]);
-                const float2 nt = mul2(nc, y2), te = fma2(c_lo, y2, fma2(c, y2, nt));  // cut * y = te - nt
-                const float2 d = add2(x2, nt), z = sub2(d, x2);
-                const float2 e = sub2(add2(sub2(x2, sub2(d, z)), sub2(nt, z)), te);
-                const float2 s = add2(d, e);
-                w[i].hi = make_float2(s.x > 0.0f ? d.x : 0.0f, s.y > 0.0f ? d.y : 0.0f);
-                w[i].lo = make_float2(s.x > 0.0f ? e.x : 0.0f, s.y > 0.0f ? e.y : 0.0f);
-            }
+        return cut_short(k) || !q_whole ? gather(q, e0, V) : __ldg(reinterpret_cast<const uint4*>(q + e0));
+    };
+    auto gone_bits = [&](int k) -> uint32_t { return gone[((k - s0) * kVec) >> 5] >> (((k - s0) * kVec) & 31); };
+    // The weights of a vector of any kind, its entries looked at one by one.
+    auto careful = [&](int how, int k, const Pair& cut, Pair (&w)[kVec]) {
+        float x[kVec], y[kVec];
+        unpack<T>(clean_vector<T>(fetch_p(k), a.dev_status), x);
+        if (how == kAll) {
+            weigh<kAll, kVec>(cut, 0, x, x, w);
+        } else if constexpr (kDrafter) {
+            unpack<T>(clean_vector<T>(fetch_q(k), a.dev_status), y);
+            weigh<kLessCutQ, kVec>(cut, 0, x, y, w);
         } else {
-            if (!kDrafter && how) {
-#pragma unroll
-                for (int i = 0; i < kVec; ++i) {
-                    const int v = e0 + i - max(s0 * kVec - off, 0);
-                    if (e0 + i >= 0 && e0 + i < V && (gone[v >> 5] >> (v & 31)) & 1u) x[i] = 0.0f;
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < kVec / 2; ++i) w[i] = Pair2{make_float2(x[2 * i], x[2 * i + 1]), make_float2(0.0f, 0.0f)};
+            weigh<kWithout, kVec>(cut, gone_bits(k), x, x, w);
         }
     };
     auto total = [&](int how, const Pair& cut) -> Pair {
-        Pair2 s[2] = {};
-        for (int k = k0 + lane; k < k1; k += 32 * kAhead) {
-            uint4 x[kAhead], y[kAhead];
+        Pair s[4] = {};
+        const bool with_q = kDrafter && how != kAll;
+        // Vectors that lie whole in the row, four of each row on their way at once and no test but the loop's: what an
+        // entry's bits are is asked behind it. As bits, what is negative, infinite or NaN is above every other entry; all
+        // entries' bits together are so too, and are else only where one is 2 or more, which is then looked at in vain.
+        const int f0 = max(k0, off > 0), f1 = with_q && !q_whole ? f0 : max(f0, min(k1, (V + off) / kVec));
+        const uint4* pv = reinterpret_cast<const uint4*>(p - off);
+        const uint4* qv = kDrafter ? reinterpret_cast<const uint4*>(q - off) : nullptr;
+        uint32_t bits = 0;
+        auto fast = [&](auto tag) {
+            constexpr int kHow = decltype(tag)::value;
+            constexpr bool kQ = kHow == kLessQ || kHow == kLessCutQ;
+            auto take = [&](int k, const uint4& px, const uint4& qx) {
+                float x[kVec], y[kVec];
+                unpack<T>(px, x);
+                unpack<T>(qx, y);
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) {  // past the part's end its last vector again, which is not counted
-                fetch(min(k + 32 * u, k1 - 1), how, x[u], y[u]);
+                for (int i = 0; i < kVec; ++i) bits |= __float_as_uint(x[i]) | (kQ ? __float_as_uint(y[i]) : 0);
+                Pair w[kVec];
+                weigh<kHow, kVec>(cut, kHow == kWithout ? gone_bits(k) : 0, x, y, w);
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) {
+                    if constexpr (kQ)
+                        add(s[i & 3], w[i]);
+                    else
+                        add(s[i & 3], w[i].hi);
+                }
+            };
+            int k = f0 + lane;
+#pragma unroll 1
+            for (; k + 32 * (kAhead - 1) < f1; k += 32 * kAhead) {
+                uint4 px[kAhead], qx[kAhead];
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    px[u] = __ldg(pv + k + 32 * u);
+                    if constexpr (kQ) qx[u] = __ldg(qv + k + 32 * u);
+                }
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) take(k + 32 * u, px[u], kQ ? qx[u] : px[u]);
             }
-#pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                if (k + 32 * u >= k1) break;
-                fetch_rest(k + 32 * u, how, x[u], y[u]);
-                Pair2 w[kVec / 2];
-                weights(k + 32 * u, how, cut, x[u], y[u], w);
-#pragma unroll
-                for (int i = 0; i < kVec / 2; ++i) add(s[i & 1], w[i]);
+#pragma unroll 1
+            for (; k < f1; k += 32) {
+                const uint4 px = __ldg(pv + k);
+                take(k, px, kQ ? __ldg(qv + k) : px);
             }
+        };
+        if (how == kAll)
+            fast(std::integral_constant<int, kAll>{});
+        else if constexpr (!kDrafter)
+            fast(std::integral_constant<int, kWithout>{});
+        else if (how == kLessQ)
+            fast(std::integral_constant<int, kLessQ>{});
+        else
+            fast(std::integral_constant<int, kLessCutQ>{});
+        const bool again = bits >= 0x7f800000u;  // this thread's once more
+        if (again) s[0] = s[1] = s[2] = s[3] = zero;
+        // what the row's ends cut, or all of it where p and q are not aligned alike
+#pragma unroll 1
+        for (int k = k0 + lane; k < k1; k += 32) {
+            if (!again && k >= f0 && k < f1) {
+                k += (f1 - 1 - k) / 32 * 32;
+                continue;
+            }
+            Pair w[kVec];
+            careful(how, k, cut, w);
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) add(s[i & 3], w[i]);
         }
         add(s[0], s[1]);
-        Pair mine{s[0].hi.x, s[0].lo.x};
-        add(mine, Pair{s[0].hi.y, s[0].lo.y});
-        mine = lane0_sum<32>(mine);
+        add(s[2], s[3]);
+        add(s[0], s[2]);
+        s[0] = lane0_sum(s[0]);
         __syncthreads();  // warp_sum has been read
-        if (lane == 0) warp_sum[warp] = mine;
+        if (lane == 0) warp_sum[warp] = s[0];
         __syncthreads();
         if (warp == 0) {
             const Pair x = lane0_sum<kWarpsV>(warp_sum[lane % kWarpsV]);
             if (lane == 0) cta_sum[pass & 1] = x;
         }
         cluster.sync();
-        const Pair x = lane0_sum<kCtasV>(*cluster.map_shared_rank(&cta_sum[pass & 1], lane % kCtasV));
+        const Pair x = lane0_sum<kCtasMost>(lane < ctas ? *cluster.map_shared_rank(&cta_sum[pass & 1], lane) : zero);
         ++pass;
         return tidy(x);
     };
 
     // ---- the walk -----------------------------------------------------------------------------------------------
     int length = 1, rejected = 0;
-    const Pair zero{0.0f, 0.0f}, one{1.0f, 0.0f};
     Pair cut = zero, mass = one;
     const bool writes = rank == 0 && tid == 0;
     if (writes) path[0] = 0;
@@ -377,7 +397,7 @@ __global__ void __cluster_dims__(kCtasV, 1, 1) __launch_bounds__(kThreadsV, 4) d
                 if (!rejected) place();
                 add(cut, mass);
                 cut = tidy(cut);
-                mass = total(1, cut);
+                mass = total(rejected ? kLessCutQ : kLessQ, cut);
             }
         } else {
             // rejected here before: an earlier child with this token
@@ -410,16 +430,16 @@ __global__ void __cluster_dims__(kCtasV, 1, 1) __launch_bounds__(kThreadsV, 4) d
     }
 
     // ---- the draw -----------------------------------------------------------------------------------------------
-    int how = rejected ? 1 : 0;
+    int how = !rejected ? kAll : !kDrafter ? kWithout : rejected == 1 ? kLessQ : kLessCutQ;
     Pair all = mass;
     if (!kDrafter || !rejected) {
         place();
         if (!kDrafter && rejected) {
-            const int v0 = max(s0 * kVec - off, 0), slice = ((V + off + kVec - 1) / kVec + kCtasV - 1) / kCtasV * kVec;
+            const int slice = (s1 - s0) * kVec;
             for (int i = tid; i < (slice + 31) / 32; i += kThreadsV) gone[i] = 0;
             __syncthreads();
             for (int i = cur + 1 + tid; i < n; i += kThreadsV) {
-                const int x = a.tokens[c0 + i], v = x - v0;
+                const int x = a.tokens[c0 + i], v = x + off - s0 * kVec;
                 if (a.parents[c0 + i] == cur && x >= 0 && x < V && v >= 0 && v < slice) atomicOr(&gone[v >> 5], 1u << (v & 31));
             }
             __syncthreads();
@@ -427,8 +447,8 @@ __global__ void __cluster_dims__(kCtasV, 1, 1) __launch_bounds__(kThreadsV, 4) d
         all = total(how, cut);
     }
     if (!positive(all)) {  // nothing is left of p: p itself
-        how = 0;
-        all = total(0, zero);
+        how = kAll;
+        all = total(kAll, zero);
     }
     float r = a.last[b];
     const bool bad_coin = !(r >= 0.0f && r < 1.0f);
@@ -436,25 +456,16 @@ __global__ void __cluster_dims__(kCtasV, 1, 1) __launch_bounds__(kThreadsV, 4) d
     Pair goal = times(all, r);  // passed by a sum that is above it
     // The border: the CTA's slice that holds it, the warp's part in that, a thread's piece of that, the element. Where
     // rounding or r >= 1 puts the goal behind everything, the last one that weighs anything.
-    const int owner = first_past(lane < kCtasV ? *cluster.map_shared_rank(&cta_sum[(pass - 1) & 1], lane % kCtasV) : zero, goal);
+    const int owner = first_past(lane < ctas ? *cluster.map_shared_rank(&cta_sum[(pass - 1) & 1], lane) : zero, goal);
     if (rank == owner) {
-        part_of(first_past(lane < kWarpsV ? warp_sum[lane % kWarpsV] : zero, goal));
+        part_of(first_past(lane < kWarpsV ? warp_sum[lane] : zero, goal));
         const int piece = (k1 - k0 + kThreadsV - 1) / kThreadsV, a0 = min(k0 + tid * piece, k1), a1 = min(a0 + piece, k1);
-        auto vector = [&](int k, Pair2 (&x)[kVec / 2]) {
-            uint4 px, qx;
-            fetch(k, how, px, qx);
-            fetch_rest(k, how, px, qx);
-            weights(k, how, cut, px, qx, x);
-        };
         Pair s = zero;
         for (int k = a0; k < a1; ++k) {
-            Pair2 x[kVec / 2];
-            vector(k, x);
+            Pair x[kVec];
+            careful(how, k, cut, x);
 #pragma unroll
-            for (int i = 0; i < kVec / 2; ++i) {
-                add(s, Pair{x[i].hi.x, x[i].lo.x});
-                add(s, Pair{x[i].hi.y, x[i].lo.y});
-            }
+            for (int i = 0; i < kVec; ++i) add(s, x[i]);
         }
         const Pair upto = running_sum(s);
         __syncthreads();  // every warp has read warp_sum
@@ -464,7 +475,10 @@ __global__ void __cluster_dims__(kCtasV, 1, 1) __launch_bounds__(kThreadsV, 4) d
             last_thread = -1;
         }
         __syncthreads();
-        for (int x = 0; x < warp; ++x) goal = less(goal, warp_sum[x]);
+        // what the warps in front hold
+        const Pair in_front = running_sum(warp_sum[lane % kWarpsV]);
+        const Pair front{__shfl_sync(kFull, in_front.hi, max(warp - 1, 0)), __shfl_sync(kFull, in_front.lo, max(warp - 1, 0))};
+        if (warp) goal = less(goal, front);
         const unsigned some = __ballot_sync(kFull, positive(s));
         const unsigned past = __ballot_sync(kFull, positive(s) && positive(less(upto, goal)));
         if (lane == 0) {
@@ -478,13 +492,12 @@ __global__ void __cluster_dims__(kCtasV, 1, 1) __launch_bounds__(kThreadsV, 4) d
             bool done = false;
             Pair t = less(upto, s);
             for (int k = a0; k < a1 && !done; ++k) {
-                Pair2 x[kVec / 2];
-                vector(k, x);
+                Pair x[kVec];
+                careful(how, k, cut, x);
 #pragma unroll
                 for (int i = 0; i < kVec; ++i) {
-                    const Pair w = i & 1 ? Pair{x[i / 2].hi.y, x[i / 2].lo.y} : Pair{x[i / 2].hi.x, x[i / 2].lo.x};
-                    add(t, w);
-                    if (!done && positive(w)) {
+                    add(t, x[i]);
+                    if (!done && positive(x[i])) {
                         found = k * kVec - off + i;
                         done = positive(less(t, goal));
                     }
@@ -502,13 +515,26 @@ __global__ void __cluster_dims__(kCtasV, 1, 1) __launch_bounds__(kThreadsV, 4) d
     cluster.sync();  // nobody reads another CTA's sums any more
 }
 
+template <typename T, bool kDrafter>
+cudaError_t launch_form(const VerifyArgs& a, cudaStream_t st) {
+    auto* kernel = draft_verify_kernel<T, kDrafter>;
+    constexpr int kVec = 16 / sizeof(T);
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e = kDrafter ? cudaSuccess : allow_smem(allowed, kernel, kVerifyMaxVocab / 8 + 64);
+    if (e != cudaSuccess) return e;
+    const int sms = device_sm_count();
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    // two CTAs fit on an SM: as many to a request as there is room for
+    int ctas = kCtasMost;
+    while (ctas > 1 && (int64_t)a.B * ctas > 2 * sms) ctas /= 2;
+    const int64_t slice = (((a.V + 2 * kVec - 2) / kVec + ctas - 1) / ctas) * kVec;  // as if no row were aligned
+    const size_t smem = kDrafter ? 0 : (size_t)(slice + 31) / 32 * 4;
+    return launch_cluster(kernel, dim3((unsigned)(a.B * ctas)), dim3(kThreadsV), ctas, smem, st, a);
+}
+
 template <typename T>
 cudaError_t launch(const VerifyArgs& a, cudaStream_t st) {
-    const dim3 grid((unsigned)a.B * kCtasV), block(kThreadsV);
-    if (a.draft) return launch_pdl(draft_verify_kernel<T, true>, grid, block, 0, st, a);
-    const int vec = 16 / (int)sizeof(T);
-    const int slice = (((a.V + 2 * vec - 2) / vec + kCtasV - 1) / kCtasV) * vec;  // as if no row were aligned
-    return launch_pdl(draft_verify_kernel<T, false>, grid, block, (size_t)(slice + 31) / 32 * 4, st, a);
+    return a.draft ? launch_form<T, true>(a, st) : launch_form<T, false>(a, st);
 }
 
 }  // namespace
