@@ -36,6 +36,7 @@ namespace idx {
 namespace {
 
 constexpr int kThreadsT = 256;
+constexpr int kFar = 2;  // see send_for
 
 template <int D>
 struct SmemT {
@@ -395,6 +396,18 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
                 page[1] = kt + 64 < k1 ? pt[(kt + 64) >> lp] : -1;
             }
         };
+        // A tree's context is read by few units, mostly once: its keys are sent for kFar steps ahead, from memory to L2, by two
+        // threads (a page of 64 keys each); the loads into registers come one step ahead and would wait for memory.
+        [[maybe_unused]] auto send_for = [&](int j) {
+            if constexpr (kTree && !kSel) {
+                const int key = k0 + j * kKeysT + ct, n = min(64, k1 - key);
+                if ((ct & 63) == 0 && n > 0) {
+                    const int32_t pg = pt[key >> lp];
+                    if ((uint32_t)pg < (uint64_t)a.num_pages)
+                        tc::bulk_prefetch(pool + (int64_t)pg * a.page_stride + (int64_t)(key & (P - 1)) * 2 * D, n * 2 * D);
+                }
+            }
+        };
         auto place = [&](int j) {
             my_scale = 0;
             if constexpr (kSel) {
@@ -555,6 +568,7 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
                 ent_n = load_entry(1);
             }
             lookup(0);
+            for (int j = 1; j < kFar; ++j) send_for(j);
             // Round j: K of step j + 1 to shared memory (where step j's product has read), loads of step
             // j + 2's K; V of step j + 1 (where O += P V has read), loads of step j + 2's V.
 #pragma unroll 1
@@ -568,6 +582,7 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
                 if (!ok) break;
                 if (j >= -1) write_k(j + 1);
                 if (j + 2 < n) {
+                    send_for(j + 2 + kFar);
                     place(j + 2);
                     load_k(j + 2);
                     if constexpr (kSel) {

@@ -93,6 +93,11 @@ __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t by
         : "memory");
 }
 
+// Bytes sent for, into L2. src 16-byte aligned; bytes a multiple of 16.
+__device__ __forceinline__ void bulk_prefetch(const void* src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+
 // L2 eviction policies: streamed data that is read once (evict first) and small metadata
 // read by every launch (evict last), so that the stream does not push the metadata out.
 __device__ __forceinline__ uint64_t policy_evict_first() {
