@@ -45,30 +45,46 @@ __device__ __forceinline__ int cta_sum(int v, int* warp_sums, int& total) {
     return before + x - v;
 }
 
-__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreadsP) pages_update_kernel(const PagesArgs a) {
+// Dynamic shared memory: three words per next row (heirs and fresh pages take turns, heirs being one per present row), then a
+// bitmap of kSegment pages.
+constexpr int kSegment = 131072;
+inline size_t pages_smem(int32_t n_out, int32_t B) {
+    return (2 * (size_t)n_out + (size_t)(n_out > B ? n_out : B)) * sizeof(int32_t) + kSegment / 8;
+}
+
+// f(0), f(1), .. with all loads of four in flight: get(j) for each, then put(j, value).
+template <typename Get, typename Put>
+__device__ __forceinline__ void by_four(int first, int end, int step, Get get, Put put) {
+    for (int j = first; j < end; j += 4 * step) {
+        int32_t x[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x[u] = j + u * step < end ? get(j + u * step) : 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (j + u * step < end) put(j + u * step, x[u]);
+    }
+}
+
+__global__ void __launch_bounds__(kThreadsP) pages_update_kernel(const PagesArgs a) {
     extern __shared__ int32_t sm[];
-    int32_t* part = sm;            // [n_out] a row's last page, where it is not full; -1
-    int32_t* fresh = sm + a.n_out;  // [n_out] the row's entry of the free list; -1: none wanted, -2: none left
+    uint32_t* freed_bits = reinterpret_cast<uint32_t*>(sm);  // [kSegment / 32]
+    int32_t* keeps = sm + kSegment / 32;                     // [n_out] pages that a next row keeps
+    int32_t* part = keeps + a.n_out;                         // [n_out] a row's last page, where it is not full; -1
+    int32_t* heir = part + a.n_out;                          // [B] the first next row that continues a present one
+    int32_t* fresh = heir;                                   // [n_out] entry of the free list; -1: none wanted, -2: none left
     __shared__ int warp_sums[32];
     __shared__ int freed;
     cg::cluster_group cluster = cg::this_cluster();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = (int)cluster.block_rank();
-    const int all = kCtas * kThreadsP, me = rank * kThreadsP + tid;   // threads of the cluster
-    const int warps = kCtas * kWarpsP, my_warp = warp * kCtas + rank;  // its warps, neighbours on unlike SMs
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int all = ctas * kThreadsP, me = rank * kThreadsP + tid;     // threads of the cluster
+    const int warps = ctas * kWarpsP, my_warp = warp * ctas + rank;    // its warps, neighbours on unlike SMs
     const int P = a.page_size;
     pdl_wait();
     pdl_launch_dependents();  // the kernel that only waits for this one
 
-    auto held = [&](int i) -> int {  // pages of a present row
-        const int32_t len = a.lens[i];
-        return len < 0 || len > (int64_t)a.pt_stride * P ? -1 : (int)(((int64_t)len + P - 1) / P);
-    };
-    auto kept = [&](int b) -> int {  // pages that a next row keeps; -1: an empty row that breaks its bounds
-        const int32_t p = a.parent[b], k = a.keep[b];
-        if (p < 0) return k == 0 ? 0 : -1;
-        if (p >= a.B || k < 0 || held(p) < 0 || k > a.lens[p]) return -1;
-        const int n = (int)(((int64_t)k + P - 1) / P);
-        return n > a.new_stride ? -1 : n;
+    auto pages_of = [&](int32_t len, int32_t width) -> int {  // of a row of len tokens; -1 where that breaks its bounds
+        return len < 0 || len > (int64_t)width * P ? -1 : (int)(((int64_t)len + P - 1) / P);
     };
     auto add = [&](int32_t page, int by) {
         if ((uint32_t)page < (uint32_t)a.num_pages)
@@ -77,29 +93,42 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreadsP) pages
             report(a.dev_status, IDX_STATUS_BAD_PAGE);
     };
 
+    // ---- the rows, in every CTA alike ------------------------------------------------------------------
+    for (int i = tid; i < a.B; i += kThreadsP) heir[i] = INT32_MAX;
+    __syncthreads();
+    for (int b = tid; b < a.n_out; b += kThreadsP) {
+        const int32_t p = a.parent[b], k = a.keep[b];
+        int n = p < 0 && k == 0 ? 0 : -1;
+        int32_t page = -1;
+        if (p >= 0 && p < a.B && k >= 0) {
+            const int32_t len = a.lens[p];
+            if (pages_of(len, a.pt_stride) >= 0 && k <= len) n = pages_of(k, a.new_stride);
+            if (n > 0) {
+                atomicMin(heir + p, b);
+                if (k % P) page = a.page_table[(int64_t)p * a.pt_stride + n - 1];
+            }
+        }
+        if (n < 0 && rank == 0) report(a.dev_status, IDX_STATUS_BAD_LEN);
+        keeps[b] = max(n, 0);
+        part[b] = (uint32_t)page < (uint32_t)a.num_pages ? page : -1;
+    }
     if (a.new_shares != a.shares)
-        for (int p = me; p < a.num_pages; p += all) a.new_shares[p] = a.shares[p];
+        by_four(me, a.num_pages, all, [&](int p) { return a.shares[p]; }, [&](int p, int32_t x) { a.new_shares[p] = x; });
     cluster.sync();
 
-    // ---- 1: holders ----------------------------------------------------------------------------------
+    // ---- 1: holders. What a row's first heir keeps stays held; the rest of it is released, other heirs hold it too ----
     for (int i = my_warp; i < a.B; i += warps) {
-        const int n = held(i);
+        const int n = pages_of(a.lens[i], a.pt_stride);
         if (n < 0 && lane == 0) report(a.dev_status, IDX_STATUS_BAD_LEN);
-        for (int j = lane; j < n; j += 32) add(a.page_table[(int64_t)i * a.pt_stride + j], -1);
+        const int32_t* row = a.page_table + (int64_t)i * a.pt_stride;
+        by_four((heir[i] < INT32_MAX ? keeps[heir[i]] : 0) + lane, n, 32, [&](int j) { return row[j]; },
+                [&](int, int32_t page) { add(page, -1); });
     }
     for (int b = my_warp; b < a.n_out; b += warps) {
-        const int n = kept(b);
-        if (n < 0 && lane == 0) report(a.dev_status, IDX_STATUS_BAD_LEN);
-        for (int j = lane; j < n; j += 32) add(a.page_table[(int64_t)a.parent[b] * a.pt_stride + j], 1);
-    }
-    for (int b = tid; b < a.n_out; b += kThreadsP) {
-        const int n = kept(b);
-        int32_t page = -1;
-        if (n > 0 && a.keep[b] % P) {
-            page = a.page_table[(int64_t)a.parent[b] * a.pt_stride + n - 1];
-            if ((uint32_t)page >= (uint32_t)a.num_pages) page = -1;
-        }
-        part[b] = page;
+        const int n = keeps[b], p = n ? a.parent[b] : 0;
+        if (n == 0 || heir[p] == b) continue;
+        const int32_t* row = a.page_table + (int64_t)p * a.pt_stride;
+        by_four(lane, n, 32, [&](int j) { return row[j]; }, [&](int, int32_t page) { add(page, 1); });
     }
     cluster.sync();
 
@@ -126,32 +155,28 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreadsP) pages
             a.copies[2 * b + 1] = -1;
         }
     }
-    cluster.sync();
-
-    // ---- 3: fresh pages and the rows ------------------------------------------------------------------
     int head = a.free_span[0], tail = a.free_span[1];
     if (head < 0 || tail < head || tail > a.free_cap) {
         if (me == 0) report(a.dev_status, IDX_STATUS_BAD_PAGE);
         head = tail = 0;
     }
-    int taken;
-    {
-        const int per = (a.n_out + kThreadsP - 1) / kThreadsP, b0 = min(tid * per, a.n_out), b1 = min(b0 + per, a.n_out);
-        int n = 0;
-        for (int b = b0; b < b1; ++b) n += __ldcg(a.copies + 2 * b) >= 0;
-        int at = head + cta_sum(n, warp_sums, taken);
-        for (int b = b0; b < b1; ++b) {
-            const bool copy = __ldcg(a.copies + 2 * b) >= 0;
-            fresh[b] = !copy ? -1 : at < tail ? at : -2;
-            at += copy;
-        }
-        taken = min(taken, tail - head);
+    cluster.sync();
+
+    // ---- 3: fresh pages and the rows ------------------------------------------------------------------
+    int taken = 0;
+    for (int b0 = 0; b0 < a.n_out; b0 += kThreadsP) {
+        const int b = b0 + tid;
+        const bool copy = b < a.n_out && __ldcg(a.copies + 2 * b) >= 0;
+        int n;
+        const int at = head + taken + cta_sum(copy, warp_sums, n);
+        if (b < a.n_out) fresh[b] = !copy ? -1 : at < tail ? at : -2;
+        taken += n;
     }
-    if (tid == 0) freed = 0;
+    taken = min(taken, tail - head);
     cluster.sync();  // fresh[] is complete, and every CTA has read the copies
     for (int b = my_warp; b < a.n_out; b += warps) {
-        const int at = fresh[b], n = max(kept(b), 0);
-        const int32_t* row = a.page_table + (int64_t)a.parent[b] * a.pt_stride;
+        const int at = fresh[b], n = keeps[b];
+        const int32_t* row = a.page_table + (int64_t)(n ? a.parent[b] : 0) * a.pt_stride;
         if (at == -2) {
             for (int j = lane; j < n; j += 32) add(row[j], -1);
             if (lane == 0) {
@@ -161,46 +186,83 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreadsP) pages
             }
             continue;
         }
-        const int32_t own = at >= 0 ? a.free_pages[at] : -1;
-        for (int j = lane; j < n; j += 32) a.new_table[(int64_t)b * a.new_stride + j] = at >= 0 && j == n - 1 ? own : row[j];
+        int32_t* to = a.new_table + (int64_t)b * a.new_stride;
         if (lane == 0) {
             a.new_lens[b] = n > 0 ? a.keep[b] : 0;
             if (at >= 0) {
+                const int32_t own = a.free_pages[at];
                 if ((uint32_t)own >= (uint32_t)a.num_pages) report(a.dev_status, IDX_STATUS_BAD_PAGE);
+                to[n - 1] = own;
                 a.copies[2 * b + 1] = own;
                 atomicAdd(a.new_shares + part[b], -1);
             }
         }
+        by_four(lane, at >= 0 ? n - 1 : n, 32, [&](int j) { return row[j]; }, [&](int j, int32_t page) {
+            to[j] = page;
+            if ((uint32_t)page >= (uint32_t)a.num_pages) report(a.dev_status, IDX_STATUS_BAD_PAGE);
+        });
     }
     cluster.sync();
 
     // ---- 4: the free list ------------------------------------------------------------------------------
-    const int per = (a.num_pages + kCtas - 1) / kCtas, p0 = min(rank * per, a.num_pages), p1 = min(p0 + per, a.num_pages);
-    int n = 0;
-    for (int p = p0 + tid; p < p1; p += kThreadsP) n += __ldcg(a.new_shares + p) < 0;
-    int mine;
-    cta_sum(n, warp_sums, mine);
+    // A CTA's pages, as many at a time as the bitmap holds: a warp takes 32 of them, eight loads in flight.
+    const int per = ((a.num_pages + ctas - 1) / ctas + 31) / 32 * 32;
+    const int p0 = min((int64_t)rank * per, (int64_t)a.num_pages), p1 = min((int64_t)p0 + per, (int64_t)a.num_pages);
+    auto find = [&](int from, int end, bool clear) -> int {  // the CTA's count
+        int n = 0;
+        const int words = (end - from + 31) / 32;
+        for (int w = warp; w < words; w += 8 * kWarpsP) {
+            int32_t s[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int p = from + (w + u * kWarpsP) * 32 + lane;
+                s[u] = w + u * kWarpsP < words && p < end ? __ldcg(a.new_shares + p) : 0;
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const unsigned bits = __ballot_sync(kFull, s[u] < 0);
+                if (w + u * kWarpsP < words) {
+                    if (lane == 0) freed_bits[w + u * kWarpsP] = bits;
+                    n += lane == 0 ? __popc(bits) : 0;
+                    if (s[u] < 0 && clear) {
+                        if (s[u] < -1) report(a.dev_status, IDX_STATUS_BAD_PAGE);  // held by more rows than its count says
+                        a.new_shares[from + (w + u * kWarpsP) * 32 + lane] = 0;
+                    }
+                }
+            }
+        }
+        int sum;
+        cta_sum(n, warp_sums, sum);
+        return sum;
+    };
+    const bool once = p1 - p0 <= kSegment;
+    int mine = 0;
+    for (int p = p0; p < p1; p += kSegment) mine += find(p, min(p1 - p, kSegment) + p, once);
     if (tid == 0) freed = mine;
     cluster.sync();
     const int left = tail - head - taken;
     int at = left, total = left;
-    for (int c = 0; c < kCtas; ++c) {
+    for (int c = 0; c < ctas; ++c) {
         const int x = *cluster.map_shared_rank(&freed, c);
         total += x;
         if (c < rank) at += x;
     }
-    for (int p = p0; mine > 0 && p < p1; p += kThreadsP) {
-        const int32_t s = p + tid < p1 ? __ldcg(a.new_shares + p + tid) : 0;
-        int sum;
-        const int before = cta_sum(s < 0, warp_sums, sum);
-        if (s < 0) {
-            if (s < -1) report(a.dev_status, IDX_STATUS_BAD_PAGE);  // held by more rows than its count says
-            if (at + before < a.new_free_cap) a.new_free[at + before] = p + tid;
-            a.new_shares[p + tid] = 0;
-        }
+    for (int p = p0; mine > 0 && p < p1; p += kSegment) {
+        const int end = min(p1 - p, kSegment) + p, words = (end - p + 31) / 32;
+        if (!once) find(p, end, true);
+        const int per_thread = (words + kThreadsP - 1) / kThreadsP;
+        const int w0 = min(tid * per_thread, words), w1 = min(w0 + per_thread, words);
+        int n = 0, sum;
+        for (int w = w0; w < w1; ++w) n += __popc(freed_bits[w]);
+        int to = at + cta_sum(n, warp_sums, sum);
+        for (int w = w0; w < w1; ++w)
+            for (uint32_t bits = freed_bits[w]; bits; bits &= bits - 1, ++to)
+                if (to < a.new_free_cap) a.new_free[to] = p + 32 * w + __ffs(bits) - 1;
         at += sum;
+        __syncthreads();  // the bitmap is used again
     }
-    for (int i = me; i < left && i < a.new_free_cap; i += all) a.new_free[i] = a.free_pages[head + taken + i];
+    by_four(me, min(left, a.new_free_cap), all, [&](int i) { return a.free_pages[head + taken + i]; },
+            [&](int i, int32_t page) { a.new_free[i] = page; });
     if (me == 0) {
         a.new_span[0] = 0;
         a.new_span[1] = min(total, a.new_free_cap);
@@ -236,13 +298,10 @@ __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const CopyArgs
 }  // namespace
 
 cudaError_t launch_pages_update(const PagesArgs& a, cudaStream_t st) {
-    const size_t smem = 2 * (size_t)a.n_out * sizeof(int32_t);
-    if (smem > 48 * 1024) {  // raised to the most that any call needs: another thread's call may come in between
-        static std::atomic<uint64_t> allowed{0};
-        const cudaError_t s = allow_smem(allowed, pages_update_kernel, 2 * kPagesMaxRows * (int)sizeof(int32_t));
-        if (s != cudaSuccess) return s;
-    }
-    const cudaError_t e = launch_pdl(pages_update_kernel, dim3(kCtas), dim3(kThreadsP), smem, st, a);
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t e = allow_smem(allowed, pages_update_kernel, (int)pages_smem(kPagesMaxRows, kPagesMaxRows));
+    if (e != cudaSuccess) return e;
+    e = launch_cluster(pages_update_kernel, dim3(kCtas), dim3(kThreadsP), kCtas, pages_smem(a.n_out, a.B), st, a);
     return e == cudaSuccess ? launch_done(st) : e;  // the library's kernels read lengths and tables before they wait
 }
 
