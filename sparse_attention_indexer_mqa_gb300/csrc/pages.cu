@@ -20,7 +20,7 @@ namespace idx {
 
 namespace {
 
-constexpr int kCtas = 8, kThreadsP = 1024, kWarpsP = kThreadsP / 32;
+constexpr int kCtas = 8, kCtasMost = 16, kThreadsP = 1024, kWarpsP = kThreadsP / 32;
 
 // Exclusive sum over the CTA of one value per thread, and the total.
 __device__ __forceinline__ int cta_sum(int v, int* warp_sums, int& total) {
@@ -48,19 +48,21 @@ __device__ __forceinline__ int cta_sum(int v, int* warp_sums, int& total) {
 // Dynamic shared memory: three words per next row (heirs and fresh pages take turns, heirs being one per present row), then a
 // bitmap of kSegment pages.
 constexpr int kSegment = 131072;
+constexpr int64_t kMany = 100000;  // table entries and pages from which a wide cluster is taken
 inline size_t pages_smem(int32_t n_out, int32_t B) {
     return (2 * (size_t)n_out + (size_t)(n_out > B ? n_out : B)) * sizeof(int32_t) + kSegment / 8;
 }
 
-// f(0), f(1), .. with all loads of four in flight: get(j) for each, then put(j, value).
+// put(j, get(j)) for j = first, first + step, .. below end, kBatch loads at a time in flight.
+constexpr int kBatch = 8;
 template <typename Get, typename Put>
-__device__ __forceinline__ void by_four(int first, int end, int step, Get get, Put put) {
-    for (int j = first; j < end; j += 4 * step) {
-        int32_t x[4];
+__device__ __forceinline__ void in_batches(int first, int end, int step, Get get, Put put) {
+    for (int j = first; j < end; j += kBatch * step) {
+        int32_t x[kBatch];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) x[u] = j + u * step < end ? get(j + u * step) : 0;
+        for (int u = 0; u < kBatch; ++u) x[u] = j + u * step < end ? get(j + u * step) : 0;
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+        for (int u = 0; u < kBatch; ++u)
             if (j + u * step < end) put(j + u * step, x[u]);
     }
 }
@@ -73,7 +75,7 @@ __global__ void __launch_bounds__(kThreadsP) pages_update_kernel(const PagesArgs
     int32_t* heir = part + a.n_out;                          // [B] the first next row that continues a present one
     int32_t* fresh = heir;                                   // [n_out] entry of the free list; -1: none wanted, -2: none left
     __shared__ int warp_sums[32];
-    __shared__ int freed;
+    __shared__ int freed[kCtasMost];  // pages that each CTA has found
     cg::cluster_group cluster = cg::this_cluster();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -113,7 +115,7 @@ __global__ void __launch_bounds__(kThreadsP) pages_update_kernel(const PagesArgs
         part[b] = (uint32_t)page < (uint32_t)a.num_pages ? page : -1;
     }
     if (a.new_shares != a.shares)
-        by_four(me, a.num_pages, all, [&](int p) { return a.shares[p]; }, [&](int p, int32_t x) { a.new_shares[p] = x; });
+        in_batches(me, a.num_pages, all, [&](int p) { return a.shares[p]; }, [&](int p, int32_t x) { a.new_shares[p] = x; });
     cluster.sync();
 
     // ---- 1: holders. What a row's first heir keeps stays held; the rest of it is released, other heirs hold it too ----
@@ -121,14 +123,14 @@ __global__ void __launch_bounds__(kThreadsP) pages_update_kernel(const PagesArgs
         const int n = pages_of(a.lens[i], a.pt_stride);
         if (n < 0 && lane == 0) report(a.dev_status, IDX_STATUS_BAD_LEN);
         const int32_t* row = a.page_table + (int64_t)i * a.pt_stride;
-        by_four((heir[i] < INT32_MAX ? keeps[heir[i]] : 0) + lane, n, 32, [&](int j) { return row[j]; },
+        in_batches((heir[i] < INT32_MAX ? keeps[heir[i]] : 0) + lane, n, 32, [&](int j) { return row[j]; },
                 [&](int, int32_t page) { add(page, -1); });
     }
     for (int b = my_warp; b < a.n_out; b += warps) {
         const int n = keeps[b], p = n ? a.parent[b] : 0;
         if (n == 0 || heir[p] == b) continue;
         const int32_t* row = a.page_table + (int64_t)p * a.pt_stride;
-        by_four(lane, n, 32, [&](int j) { return row[j]; }, [&](int, int32_t page) { add(page, 1); });
+        in_batches(lane, n, 32, [&](int j) { return row[j]; }, [&](int, int32_t page) { add(page, 1); });
     }
     cluster.sync();
 
@@ -173,7 +175,7 @@ __global__ void __launch_bounds__(kThreadsP) pages_update_kernel(const PagesArgs
         taken += n;
     }
     taken = min(taken, tail - head);
-    cluster.sync();  // fresh[] is complete, and every CTA has read the copies
+    __syncthreads();  // fresh[] is complete
     for (int b = my_warp; b < a.n_out; b += warps) {
         const int at = fresh[b], n = keeps[b];
         const int32_t* row = a.page_table + (int64_t)(n ? a.parent[b] : 0) * a.pt_stride;
@@ -182,7 +184,6 @@ __global__ void __launch_bounds__(kThreadsP) pages_update_kernel(const PagesArgs
             if (lane == 0) {
                 report(a.dev_status, IDX_STATUS_NO_PAGE);
                 a.new_lens[b] = 0;
-                a.copies[2 * b] = -1;
             }
             continue;
         }
@@ -197,12 +198,17 @@ __global__ void __launch_bounds__(kThreadsP) pages_update_kernel(const PagesArgs
                 atomicAdd(a.new_shares + part[b], -1);
             }
         }
-        by_four(lane, at >= 0 ? n - 1 : n, 32, [&](int j) { return row[j]; }, [&](int j, int32_t page) {
+        in_batches(lane, at >= 0 ? n - 1 : n, 32, [&](int j) { return row[j]; }, [&](int j, int32_t page) {
             to[j] = page;
             if ((uint32_t)page >= (uint32_t)a.num_pages) report(a.dev_status, IDX_STATUS_BAD_PAGE);
         });
     }
+    const int left = tail - head - taken;
+    in_batches(me, min(left, a.new_free_cap), all, [&](int i) { return a.free_pages[head + taken + i]; },
+               [&](int i, int32_t page) { a.new_free[i] = page; });
     cluster.sync();
+    for (int b = my_warp; b < a.n_out; b += warps)  // every CTA has read the copies
+        if (lane == 0 && fresh[b] == -2) a.copies[2 * b] = -1;
 
     // ---- 4: the free list ------------------------------------------------------------------------------
     // A CTA's pages, as many at a time as the bitmap holds: a warp takes 32 of them, eight loads in flight.
@@ -238,14 +244,12 @@ __global__ void __launch_bounds__(kThreadsP) pages_update_kernel(const PagesArgs
     const bool once = p1 - p0 <= kSegment;
     int mine = 0;
     for (int p = p0; p < p1; p += kSegment) mine += find(p, min(p1 - p, kSegment) + p, once);
-    if (tid == 0) freed = mine;
+    if (tid < ctas) *cluster.map_shared_rank(&freed[rank], tid) = mine;
     cluster.sync();
-    const int left = tail - head - taken;
     int at = left, total = left;
     for (int c = 0; c < ctas; ++c) {
-        const int x = *cluster.map_shared_rank(&freed, c);
-        total += x;
-        if (c < rank) at += x;
+        total += freed[c];
+        if (c < rank) at += freed[c];
     }
     for (int p = p0; mine > 0 && p < p1; p += kSegment) {
         const int end = min(p1 - p, kSegment) + p, words = (end - p + 31) / 32;
@@ -261,13 +265,10 @@ __global__ void __launch_bounds__(kThreadsP) pages_update_kernel(const PagesArgs
         at += sum;
         __syncthreads();  // the bitmap is used again
     }
-    by_four(me, min(left, a.new_free_cap), all, [&](int i) { return a.free_pages[head + taken + i]; },
-            [&](int i, int32_t page) { a.new_free[i] = page; });
     if (me == 0) {
         a.new_span[0] = 0;
         a.new_span[1] = min(total, a.new_free_cap);
     }
-    cluster.sync();  // nobody reads another CTA's count any more
 }
 
 // 16 bytes a thread, eight of them in flight.
@@ -301,7 +302,15 @@ cudaError_t launch_pages_update(const PagesArgs& a, cudaStream_t st) {
     static std::atomic<uint64_t> allowed{0};
     cudaError_t e = allow_smem(allowed, pages_update_kernel, (int)pages_smem(kPagesMaxRows, kPagesMaxRows));
     if (e != cudaSuccess) return e;
-    e = launch_cluster(pages_update_kernel, dim3(kCtas), dim3(kThreadsP), kCtas, pages_smem(a.n_out, a.B), st, a);
+    // Eight CTAs, sixteen (more than every GPU has to offer, so it is asked for) where there is much to go through.
+    const int64_t entries = (int64_t)a.B * a.pt_stride + (int64_t)a.n_out * a.new_stride + a.num_pages;
+    const int ctas = entries > kMany ? kCtasMost : kCtas;
+    if (ctas > kCtas) {
+        static std::atomic<uint64_t> wide{0};
+        e = allow_wide_cluster(wide, pages_update_kernel);
+        if (e != cudaSuccess) return e;
+    }
+    e = launch_cluster(pages_update_kernel, dim3(ctas), dim3(kThreadsP), ctas, pages_smem(a.n_out, a.B), st, a);
     return e == cudaSuccess ? launch_done(st) : e;  // the library's kernels read lengths and tables before they wait
 }
 
