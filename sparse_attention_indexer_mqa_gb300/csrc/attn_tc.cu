@@ -49,6 +49,7 @@ struct SmemT {
     static constexpr int kRange = kKey + 2 * kKeysT * 4;    // [2][4] their ranges, a word per warp
     static constexpr int kBar = kRange + 32;
     static constexpr int kBytes = kBar + 64 + 1024;         // 1024: alignment of the operand tiles
+    static_assert(kK + kRowsT * kOutRow<D> <= kBar, "results are staged from K's tile on");
 };
 
 // Barriers of the four converter warps, one of them with a vote.
@@ -148,8 +149,8 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
         const int vis = kTree && !kSel ? front : (int)visible_keys(s.len, s.nq, tok - s.t0, a.causal);
         [[maybe_unused]] const uint64_t* mask = kTree ? a.tree + tok * a.tree_stride : nullptr;
         // < 0: an infinity or a NaN in q; the row is scored as zeros, and is NaN at the end if any key counted
-        const float rc = write_q_row<D, kHalf>(sm + S::kQ, a.q + tok * a.q_row_stride + (int64_t)hq * a.q_head_stride,
-                                               real, tid, a.scale);
+        const float rc = write_q_rows<D, kHalf>(sm + S::kQ, a.q + tok * a.q_row_stride + (int64_t)hq * a.q_head_stride,
+                                                real, 32 * warp, a.scale);
         tc::fence_proxy_async();
         tc::mbar_arrive(q_full);
         const uint32_t lanes = (uint32_t)(warp * 32) << 16;
@@ -348,7 +349,7 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
             bool nan = !kSel && *nan_key < vis;
             if constexpr (kTree && !kSel)
                 nan = nan_nodes[kTreeMaxNodes / 32] || tree_sees(mask, a.tree_words, s.nq, nan_nodes);
-            store_rows<D, kHalf>(a, tm_o + lanes, n > 0, real, tok, hq, z, m, l, nan);
+            store_rows<D, kHalf>(a, tm_o + lanes, sm + S::kK + warp * 32 * kOutRow<D>, n > 0, real, tok, hq, z, m, l, nan);
         }
     } else {
         // ---- converters --------------------------------------------------------------------------------
@@ -398,14 +399,19 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
         };
         // A tree's context is read by few units, mostly once: its keys are sent for kFar steps ahead, from memory to L2, by two
         // threads (a page of 64 keys each); the loads into registers come one step ahead and would wait for memory.
+        int32_t far_page = -1;  // of the step that is sent for next
+        [[maybe_unused]] auto far_lookup = [&](int j) {
+            if constexpr (kTree && !kSel) {
+                const int key = k0 + j * kKeysT + ct;
+                far_page = (ct & 63) == 0 && key < k1 ? pt[key >> lp] : -1;
+            }
+        };
         [[maybe_unused]] auto send_for = [&](int j) {
             if constexpr (kTree && !kSel) {
-                const int key = k0 + j * kKeysT + ct, n = min(64, k1 - key);
-                if ((ct & 63) == 0 && n > 0) {
-                    const int32_t pg = pt[key >> lp];
-                    if ((uint32_t)pg < (uint64_t)a.num_pages)
-                        tc::bulk_prefetch(pool + (int64_t)pg * a.page_stride + (int64_t)(key & (P - 1)) * 2 * D, n * 2 * D);
-                }
+                const int key = k0 + j * kKeysT + ct;
+                if ((uint32_t)far_page < (uint64_t)a.num_pages)
+                    tc::bulk_prefetch(pool + (int64_t)far_page * a.page_stride + (int64_t)(key & (P - 1)) * 2 * D,
+                                      min(64, k1 - key) * 2 * D);
             }
         };
         auto place = [&](int j) {
@@ -568,7 +574,11 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
                 ent_n = load_entry(1);
             }
             lookup(0);
-            for (int j = 1; j < kFar; ++j) send_for(j);
+            for (int j = 1; j < kFar; ++j) {
+                far_lookup(j);
+                send_for(j);
+            }
+            far_lookup(kFar);
             // Round j: K of step j + 1 to shared memory (where step j's product has read), loads of step
             // j + 2's K; V of step j + 1 (where O += P V has read), loads of step j + 2's V.
 #pragma unroll 1
@@ -583,6 +593,7 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
                 if (j >= -1) write_k(j + 1);
                 if (j + 2 < n) {
                     send_for(j + 2 + kFar);
+                    far_lookup(j + 3 + kFar);
                     place(j + 2);
                     load_k(j + 2);
                     if constexpr (kSel) {

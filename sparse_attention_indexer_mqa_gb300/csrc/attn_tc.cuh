@@ -12,6 +12,9 @@ namespace idx {
 constexpr int kRowsT = 128;   // rows of a tile
 constexpr int kKeysT = 128;   // keys of a step
 
+template <int D>
+constexpr int kOutRow = 4 * D + 16;  // bytes of a staged row of results
+
 // Pauses between tests of a barrier (ns). None was measurably better or worse from 0 to 200.
 constexpr int kNsIssue = 0, kNsSoft = 0, kNsConv = 20;
 
@@ -95,41 +98,63 @@ __device__ __forceinline__ void write_v_block(uint8_t* tile, const uint4 (&rv)[8
     }
 }
 
-// A thread's row of q as fp16 into row `row` of the Q tile (zeros if it does not exist or is not finite); returns the
-// row's factor: softmax_scale * log2(e) * (the power of two taken out), -1 for a row that is not finite.
+// A warp's 32 rows of q as fp16 into rows first .. first + 31 of the Q tile (zeros where a row does not exist or is not
+// finite); src: each lane's row. Returns the lane's row's factor: softmax_scale * log2(e) * (the power of two taken
+// out), -1 for a row that is not finite. D/8 lanes take a row, so that a request touches whole lines; with a row to a thread
+// a unit's start took 8 us where every SM was loading.
 template <int D, bool kHalf>
-__device__ __forceinline__ float write_q_row(uint8_t* tile, const uint16_t* src, bool real, int row, float scale) {
-    const uint4* q = reinterpret_cast<const uint4*>(src);
-    float amax = 0.0f;
-    bool odd = false;
-#pragma unroll 4
-    for (int i = 0; i < D / 8; ++i) {
-        const uint4 w = real ? q[i] : make_uint4(0, 0, 0, 0);
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+__device__ __forceinline__ float write_q_rows(uint8_t* tile, const uint16_t* src, bool real, int first, float scale) {
+    constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kBatch = 4;
+    const int lane = threadIdx.x & 31, i = lane % kLanes, sub = lane / kLanes;
+    const unsigned exist = __ballot_sync(kFull, real);
+    const uint32_t lo = (uint32_t)reinterpret_cast<uintptr_t>(src), hi = (uint32_t)(reinterpret_cast<uintptr_t>(src) >> 32);
+    float mine = 0.0f;
+#pragma unroll 1
+    for (int s0 = 0; s0 < kLanes; s0 += kBatch) {
+        uint4 w[kBatch];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const float2 f = load_pair<kHalf>(u[x]);
-            odd |= !(fabsf(f.x) < __int_as_float(0x7f800000)) || !(fabsf(f.y) < __int_as_float(0x7f800000));
-            amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+        for (int s = 0; s < kBatch; ++s) {
+            const int r = (s0 + s) * kAtOnce + sub;
+            const uint32_t l = __shfl_sync(kFull, lo, r), h = __shfl_sync(kFull, hi, r);
+            const uint4* row = reinterpret_cast<const uint4*>((uintptr_t)h << 32 | l);
+            w[s] = make_uint4(0, 0, 0, 0);
+            if (exist >> r & 1u) w[s] = row[i];
         }
-    }
-    const int e = odd ? 0 : q_exponent<kHalf>(amax);
-    const float up = pow2f(-e);
-#pragma unroll 4
-    for (int i = 0; i < D / 8; ++i) {  // again, from L1
-        const uint4 w = real && !odd ? q[i] : make_uint4(0, 0, 0, 0);
-        uint32_t u[4] = {w.x, w.y, w.z, w.w};
-        if constexpr (!kHalf) {
+#pragma unroll
+        for (int s = 0; s < kBatch; ++s) {
+            const int r = (s0 + s) * kAtOnce + sub, row = first + r;
+            uint32_t u[4] = {w[s].x, w[s].y, w[s].z, w[s].w};
+            float amax = 0.0f;
+            bool odd = false;
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 const float2 f = load_pair<kHalf>(u[x]);
-                u[x] = half2_bits(f.x * up, f.y * up);
+                odd |= !(fabsf(f.x) < __int_as_float(0x7f800000)) || !(fabsf(f.y) < __int_as_float(0x7f800000));
+                amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
             }
+            const unsigned odds = __ballot_sync(kFull, odd);
+            odd = (odds >> (sub * kLanes) & (kLanes == 32 ? ~0u : (1u << kLanes) - 1)) != 0;
+            if constexpr (!kHalf) {
+#pragma unroll
+                for (int o = kLanes / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
+            }
+            const int e = odd ? 0 : q_exponent<kHalf>(amax);
+            const float up = pow2f(-e);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                if (odd) u[x] = 0;
+                if constexpr (!kHalf) {
+                    const float2 f = load_pair<kHalf>(u[x]);
+                    u[x] = half2_bits(f.x * up, f.y * up);
+                }
+            }
+            *reinterpret_cast<uint4*>(tile + dims_sub<D>(i) * (kRowsT * 128) + row * 128 + ((dims_chunk<D>(i) ^ (row & 7)) << 4)) =
+                make_uint4(u[0], u[1], u[2], u[3]);
+            const float f = __shfl_sync(kFull, odd ? -1.0f : scale * kLog2e * pow2f(e), lane % kAtOnce * kLanes);
+            if (lane / kAtOnce == s0 + s) mine = f;
         }
-        *reinterpret_cast<uint4*>(tile + dims_sub<D>(i) * (kRowsT * 128) + row * 128 +
-                                  ((dims_chunk<D>(i) ^ (row & 7)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
     }
-    return odd ? -1.0f : scale * kLog2e * pow2f(e);
+    return mine;
 }
 
 // S = Q K^T and O (+)= P V of a step, by one lane of the (converged) warp that calls. P lies in the
@@ -165,12 +190,16 @@ __device__ __forceinline__ void issue_outputs(uint32_t tm_o, uint32_t tm_p, uint
 
 // A warp's rows out of tensor memory (tm_o: the warp's lanes): the result, or the split's part of it. some: O was
 // written at all. nan: a NaN code of V among the row's keys. Column 8y + x of O is dim (D/8) * x + y, so 32 columns are 4 dims of each x.
+// The rows pass through shared memory (32 * kOutRow<D> bytes of the warp's own, from K's tile on: the last product has
+// read it, and without keys nothing writes there), so that a request writes whole rows: 8 bytes of each of 32 rows a request took 4 us where every SM was writing.
 template <int D, bool kHalf>
-__device__ __forceinline__ void store_rows(const AttnArgs& a, uint32_t tm_o, bool some, bool real, int64_t tok, int hq,
+__device__ __forceinline__ void store_rows(const AttnArgs& a, uint32_t tm_o, uint8_t* stage, bool some, bool real, int64_t tok, int hq,
                                            int z, float m, float l, bool nan) {
-    const float g = nan ? __int_as_float(0x7fc00000) : a.n_split > 1 ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
+    const bool part = a.n_split > 1;
+    const float g = nan ? __int_as_float(0x7fc00000) : part ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
     const int64_t pr = ((int64_t)z * a.T + tok) * a.q_heads + hq;
-    uint16_t* out = a.out + tok * a.out_row_stride + (int64_t)hq * a.out_head_stride;
+    const int lane = threadIdx.x & 31;
+    uint8_t* own = stage + lane * kOutRow<D>;
 #pragma unroll 1
     for (int c = 0; c < D / 32; ++c) {
         uint32_t r[32];
@@ -189,15 +218,28 @@ __device__ __forceinline__ void store_rows(const AttnArgs& a, uint32_t tm_o, boo
 #pragma unroll
             for (int y = 0; y < 4; ++y) v[y] = __uint_as_float(r[8 * y + x]) * g;
             const int dim = D / 8 * x + 4 * c;
-            if (real && a.n_split > 1) {
-                if (l != 0.0f) *reinterpret_cast<float4*>(a.part_o + pr * D + dim) = make_float4(v[0], v[1], v[2], v[3]);
-            } else if (real) {
-                *reinterpret_cast<uint2*>(out + dim) = make_uint2(store_pair<kHalf>(v[0], v[1]), store_pair<kHalf>(v[2], v[3]));
-            }
+            if (part)
+                *reinterpret_cast<float4*>(own + 4 * dim) = make_float4(v[0], v[1], v[2], v[3]);
+            else
+                *reinterpret_cast<uint2*>(own + 2 * dim) = make_uint2(store_pair<kHalf>(v[0], v[1]), store_pair<kHalf>(v[2], v[3]));
         }
     }
+    // where each lane's row goes; a part without keys is not written
+    uint8_t* to = part ? reinterpret_cast<uint8_t*>(a.part_o + pr * D)
+                       : reinterpret_cast<uint8_t*>(a.out + tok * a.out_row_stride + (int64_t)hq * a.out_head_stride);
+    const unsigned go = __ballot_sync(kFull, real && (!part || l != 0.0f));
+    __syncwarp();  // every lane has staged its row
+    const uint32_t lo = (uint32_t)reinterpret_cast<uintptr_t>(to), hi = (uint32_t)(reinterpret_cast<uintptr_t>(to) >> 32);
+    const int pieces = part ? D / 4 : D / 8, at_once = 32 / pieces, i = lane % pieces;
+#pragma unroll 4
+    for (int r0 = 0; r0 < 32; r0 += at_once) {
+        const int r = r0 + lane / pieces;
+        const uint32_t ll = __shfl_sync(kFull, lo, r), hh = __shfl_sync(kFull, hi, r);
+        if (go >> r & 1u)
+            reinterpret_cast<uint4*>((uintptr_t)hh << 32 | ll)[i] = *reinterpret_cast<const uint4*>(stage + r * kOutRow<D> + 16 * i);
+    }
     if (real) {
-        if (a.n_split > 1)
+        if (part)
             a.part_ml[pr] = make_float2(m, l);
         else if (a.lse)
             a.lse[tok * a.q_heads + hq] = lse_of(m, l);
