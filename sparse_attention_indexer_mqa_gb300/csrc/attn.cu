@@ -640,9 +640,19 @@ struct Choice {
     int64_t units;
     int per_sm;  // resident CTAs
 };
+//
+// Trees, whose nodes make more rows than a decode's: up to four mma.sync tiles where all tiles' keys together are few, for
+// the tensor-memory kernel's start alone takes longer then. 64 rows (8 nodes, 8 heads): on one kv head and 512 keys 9.8 us against 13.2,
+// 8192 keys 11.6 / 14.8, on eight heads and 2048 keys 13.4 / 14.3 (65,000 keys of all tiles), 64 x 512 keys 13.8 / 15.7
+// (131,000), but 8 x 8192 keys 23.3 / 19.0 (262,000); 128 rows on 8 x 2048 keys 17.4 / 15.9. Lists, 64 heads: 8 nodes of
+// 1024 keys 11.9 / 16.3 (33,000), 16 of them 14.7 / 16.8, 32 17.2 / 17.3 (132,000), 128 of 256 keys 20.7 / 13.9 (135,000), 152 of 120 15.3 / 9.9 (78,000, but two rounds of tiles).
+constexpr int kTreeRows = 64, kTreeKeys = 1024, kTreeEntries = 512;  // the latter two per SM
 Choice choose(const AttnArgs& a) {
     const int64_t rows = shared_rows(a), times = (a.n_sel ? a.T : (int64_t)a.B) * a.kv_heads;
-    if (rows <= (a.n_sel ? 16 : 32)) return {false, times * ((rows + 15) / 16), 3};
+    const int64_t few = times * ((rows + 15) / 16), keys = a.n_sel ? a.n_sel + a.max_q_len : a.max_seq_len_k;
+    const int64_t sms = device_sm_count();
+    const bool small = few <= 2 * sms && few * keys <= (a.n_sel ? kTreeEntries : kTreeKeys) * sms;
+    if (rows <= (a.n_sel ? 16 : 32) || (a.tree && rows <= kTreeRows && small)) return {false, few, 3};
     return {true, times * ((rows + 127) / 128), 2};
 }
 
@@ -707,6 +717,8 @@ int64_t attn_plan(AttnArgs& a, int64_t bytes) {
             want = least(64, least(4 * slots / units, keys / 1024));
             if (units * want < slots + slots / 2) want = least(64, least(slots / units, keys / one_round_keys));
         }
+        // a small tree's step of up to 512 keys stays whole: 9.9 us against 9.7 in two, and the join's launch costs the host 2
+        if (a.tree && !choice.tile && keys <= 512) want = 1;
         if (want < 1) want = 1;
     }
     const int64_t fits = per_split > 0 ? bytes / per_split : 1;
