@@ -48,7 +48,7 @@ struct SmemT {
     static constexpr int kKey = kOff + 2 * kKeysT * 8;      // [2][128] scale bytes of the listed keys
     static constexpr int kRange = kKey + 2 * kKeysT * 4;    // [2][4] their ranges, a word per warp
     static constexpr int kBar = kRange + 32;
-    static constexpr int kBytes = kBar + 64 + 1024;         // 1024: alignment of the operand tiles
+    static constexpr int kBytes = kBar + 80 + 1024;         // 1024: alignment of the operand tiles
     static_assert(kK + kRowsT * kOutRow<D> <= kBar, "results are staged from K's tile on");
 };
 
@@ -74,6 +74,8 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + S::kBar);
     uint64_t *q_full = bars, *k_full = bars + 1, *v_full = bars + 2, *s_full = bars + 3, *p_full = bars + 4,
              *o_done = bars + 5, *drain = bars + 6;
+    // [2], steps in turn: a helper may be done with steps 0 and 1 before the other has done step 0
+    [[maybe_unused]] uint64_t* look_full = bars + 8;
     int* nan_key = reinterpret_cast<int*>(bars + 7);  // lowest key whose V held a NaN code that was taken out
     float4* scales = reinterpret_cast<float4*>(sm + S::kScale);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -118,6 +120,8 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
         tc::mbar_init(p_full, (rows + 31) / 32);  // a warp without rows takes no part
         tc::mbar_init(o_done, 1);
         tc::mbar_init(drain, 1);
+        tc::mbar_init(look_full, 2);
+        tc::mbar_init(look_full + 1, 2);
         *nan_key = INT32_MAX;
         tc::fence_mbar_init();
     }
@@ -138,6 +142,45 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
     const int n = k1 > k0 ? (k1 - k0 + kKeysT - 1) / kKeysT : 0;
     bool ok = true;
     [[maybe_unused]] const int front = s.len - s.nq;  // keys in front of the tree
+    // A list's lookups: with up to 64 rows by the softmax warps that have none.
+    const bool helped = kSel && rows <= 64;
+    int64_t* offs = reinterpret_cast<int64_t*>(sm + S::kOff);
+    uint32_t* key_scales = reinterpret_cast<uint32_t*>(sm + S::kKey);
+    uint32_t* ranges = reinterpret_cast<uint32_t*>(sm + S::kRange);
+    const int P = a.page_size, lp = P == 128 ? 7 : 6;
+    const uint8_t* pool = a.pool + (int64_t)head * kv_head_bytes(P, D);
+    const int32_t* pt = a.page_table + (int64_t)b * a.pt_stride;
+    const int vis_sel = kSel ? (int)visible_keys(s.len, s.nq, tok0 - s.t0, a.causal) : 0;
+    // Entry i of step j, and whether what it holds counts.
+    auto load_entry = [&](int j, int i) -> int32_t {
+        const int e = k0 + j * kKeysT + i;
+        if constexpr (kTree) {  // the nodes that the row sees come behind its list
+            const int node = e - a.n_sel;
+            if (node >= 0)
+                return e < k1 && tree_window(a.tree + tok0 * a.tree_stride, a.tree_words, s.nq, node) & 1 ? front + node : -1;
+        }
+        return e < k1 ? a.sel[tok0 * a.sel_stride + e] : -1;
+    };
+    auto counts = [&](int j, int i, int32_t ent) -> bool {
+        const int end = kTree && k0 + j * kKeysT + i < a.n_sel ? front : vis_sel;
+        return ent >= 0 && ent < end;
+    };
+    // The ranges of a warp's scale bytes (of those that count), into words `at` of the step's four: largest K, smallest K,
+    // largest V, smallest V.
+    auto ranges_of = [&](uint32_t lo_scale, uint32_t hi_scale) -> uint32_t {
+        uint32_t k_hi = 0, k_lo = 255, v_hi = 0, v_lo = 255;
+        // a key that does not count makes the range too wide
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t two = i ? hi_scale : lo_scale, ek = scale_byte(two), ev = scale_byte(two >> 8);
+            k_hi = max(k_hi, two ? ek : 255u);
+            k_lo = min(k_lo, two ? ek : 0u);
+            v_hi = max(v_hi, two ? ev : 255u);
+            v_lo = min(v_lo, two ? ev : 0u);
+        }
+        return __reduce_max_sync(kFull, k_hi) | __reduce_min_sync(kFull, k_lo) << 8 | __reduce_max_sync(kFull, v_hi) << 16 |
+               __reduce_min_sync(kFull, v_lo) << 24;
+    };
 
     if (warp < 4) {
         // ---- softmax: this thread's row --------------------------------------------------------------
@@ -301,6 +344,69 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
             tc::tmem_st_wait();
             tc::tc_fence_before();
         };
+        // A list's lookups by the warps of rows 64 .. 127 where there are none: for each step the places of its keys' rows and
+        // the scale bytes, two entries a thread. In the converters they were half of a round's chain of instructions (a step
+        // of 7500 cycles; the products and the softmax take 4800). Step j + 2's places lie where step j's were.
+        if constexpr (kSel) {
+            if (helped && warp >= 2) {
+                const int ht = tid - 64;
+                int32_t ent[2], pg[2];
+                int64_t at[2], at_n[2];
+                uint32_t two[2], two_n[2];
+                bool bad = false;
+                auto look = [&](int j) {  // pages of step j, whose entries are there
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) pg[i] = j < n && counts(j, ht + 64 * i, ent[i]) ? pt[ent[i] >> lp] : -1;
+                };
+                auto place = [&](int j) {  // places and scales of step j, whose pages are there
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const bool seen = j < n && counts(j, ht + 64 * i, ent[i]), in = (uint32_t)pg[i] < (uint64_t)a.num_pages;
+                        bad |= seen && !in;
+                        at_n[i] = -1;
+                        two_n[i] = 0;
+                        if (seen && in) {
+                            const int tok = ent[i] & (P - 1);
+                            at_n[i] = (int64_t)pg[i] * a.page_stride;
+                            two_n[i] = *reinterpret_cast<const uint16_t*>(pool + at_n[i] + 2ll * P * D + 2 * (tok / kKvBlock)) | 65536u;
+                            at_n[i] += (int64_t)tok * 2 * D;
+                        }
+                    }
+                };
+                auto entries = [&](int j) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) ent[i] = j < n ? load_entry(j, ht + 64 * i) : -1;
+                };
+                entries(0);
+                look(0);
+                place(0);
+                entries(1);
+                look(1);
+#pragma unroll 1
+                for (int j = 0; j < n; ++j) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        at[i] = at_n[i];
+                        two[i] = two_n[i];
+                    }
+                    if (j >= 2) ok = warp_wait<kNsConv>(v_full, j & 1);
+                    if (!ok) break;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        offs[(j & 1) * kKeysT + ht + 64 * i] = at[i];
+                        key_scales[(j & 1) * kKeysT + ht + 64 * i] = two[i];
+                    }
+                    const uint32_t r = ranges_of(two[0], two[1]);
+                    if (lane < 2) ranges[(j & 1) * 4 + (warp & 1) + 2 * lane] = r;
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(look_full + (j & 1));
+                    place(j + 1);
+                    entries(j + 2);
+                    look(j + 2);
+                }
+                if (bad) report(a.dev_status, IDX_STATUS_BAD_PAGE);
+            }
+        }
         // Warp 0 issues the MMAs: it has nothing else to do meanwhile.
         const uint32_t base = tc::smem_u32(sm);
         // Round j: O += P V of step j and S of step j + 1, then the softmax of step j + 1.
@@ -357,12 +463,6 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
         using C = ConvShare<D>;
         const C my(ct);
         constexpr int kPieces = C::kPieces;
-        const int P = a.page_size, lp = P == 128 ? 7 : 6;
-        const int64_t hb = kv_head_bytes(P, D);
-        const uint8_t* pool = a.pool + (int64_t)head * hb;
-        const int32_t* pt = a.page_table + (int64_t)b * a.pt_stride;
-        int64_t* offs = reinterpret_cast<int64_t*>(sm + S::kOff);
-        const int vis_sel = kSel ? (int)visible_keys(s.len, s.nq, tok0 - s.t0, a.causal) : 0;
         // keys that the tile's first row does not see though another does begin here
         const int vis_first = kSel ? 0 : kTree ? front : (int)visible_keys(s.len, s.nq, row0 / G, a.causal);
         uint4 rk[kPieces], rv[8];
@@ -375,22 +475,9 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
         int32_t page[2] = {-1, -1};                     // the second: keys 64 .. of the step
         const uint8_t* rows_at[2] = {nullptr, nullptr};  // key 0 of the step, seen from either half
         int keys = 0;                                    // of the step
-        auto load_entry = [&](int j) -> int32_t {
-            const int e = k0 + j * kKeysT + ct;
-            if constexpr (kTree) {  // the nodes that the row sees come behind its list
-                const int node = e - a.n_sel;
-                if (node >= 0)
-                    return e < k1 && tree_window(a.tree + tok0 * a.tree_stride, a.tree_words, s.nq, node) & 1 ? front + node : -1;
-            }
-            return e < k1 ? a.sel[tok0 * a.sel_stride + e] : -1;
-        };
-        auto counts = [&](int j) -> bool {  // this thread's entry of step j
-            const int end = kTree && k0 + j * kKeysT + ct < a.n_sel ? front : vis_sel;
-            return ent >= 0 && ent < end;
-        };
         auto lookup = [&](int j) {
             if constexpr (kSel) {
-                page[0] = counts(j) ? pt[ent >> lp] : -1;
+                page[0] = counts(j, ct, ent) ? pt[ent >> lp] : -1;
             } else {
                 const int kt = k0 + j * kKeysT;
                 page[0] = kt < k1 ? pt[kt >> lp] : -1;
@@ -417,7 +504,7 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
         auto place = [&](int j) {
             my_scale = 0;
             if constexpr (kSel) {
-                const bool seen = counts(j), in = (uint32_t)page[0] < (uint64_t)a.num_pages;
+                const bool seen = counts(j, ct, ent), in = (uint32_t)page[0] < (uint64_t)a.num_pages;
                 int64_t at = -1;
                 bad |= seen && !in;
                 if (seen && in) {
@@ -487,17 +574,12 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
         // A list's keys have scales of their own. Where a step's lie within 2^15 of one another and every key
         // counts, they are folded into the fp16 operands (exact: a code is at least 2^-9, fp16
         // reaches 2^-24) and the softmax sees one scale pair; otherwise it takes a pair per key.
-        uint32_t* key_scales = reinterpret_cast<uint32_t*>(sm + S::kKey);
-        uint32_t* ranges = reinterpret_cast<uint32_t*>(sm + S::kRange);
         int k_top = 0, v_top = 0;  // largest scale bytes of the step
         bool fold = false;
         auto publish = [&](int j) {  // before the barrier
-            const uint32_t ek = scale_byte(my_scale), ev = scale_byte(my_scale >> 8);
-            const bool in = my_scale != 0;
-            const uint32_t k_hi = __reduce_max_sync(kFull, in ? ek : 255u), k_lo = __reduce_min_sync(kFull, in ? ek : 0u);
-            const uint32_t v_hi = __reduce_max_sync(kFull, in ? ev : 255u), v_lo = __reduce_min_sync(kFull, in ? ev : 0u);
+            const uint32_t r = ranges_of(my_scale, my_scale);
             key_scales[(j & 1) * kKeysT + ct] = my_scale;
-            if (lane == 0) ranges[(j & 1) * 4 + cw] = k_hi | k_lo << 8 | v_hi << 16 | v_lo << 24;
+            if (lane == 0) ranges[(j & 1) * 4 + cw] = r;
         };
         auto collect = [&](int j) {  // behind it
             const uint4 r = *reinterpret_cast<const uint4*>(ranges + (j & 1) * 4);
@@ -505,13 +587,13 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
             const uint32_t lo = __vminu4(__vminu4(r.x, r.y), __vminu4(r.z, r.w));
             k_top = hi & 255;
             v_top = hi >> 16 & 255;
-            // a key that does not count makes the range too wide
             fold = k_top - (int)(lo >> 8 & 255) <= 15 && v_top - (int)(lo >> 24) <= 15;
         };
         auto down = [&](int by) -> uint32_t {  // 2^-by as fp16 bits, by in 0 .. 15
             return by < 15 ? (uint32_t)(15 - by) << 10 : 0x0200u;
         };
         auto write_k = [&](int j) {
+            if (helped) my_scale = key_scales[(j & 1) * kKeysT + ct];
             const float ev = v_exponent(my_scale);
             const float4 sc = my_scale ? make_float4(k_scale(my_scale), ev, ex2(-ev), 1.0f)
                                        : make_float4(1.0f, neg_inf(), 0.0f, 1.0f);
@@ -569,38 +651,49 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
         };
 
         if (n > 0) {
-            if constexpr (kSel) {
-                ent = load_entry(0);
-                ent_n = load_entry(1);
+            if (!helped) {
+                if constexpr (kSel) {
+                    ent = load_entry(0, ct);
+                    ent_n = load_entry(1, ct);
+                }
+                lookup(0);
+                for (int j = 1; j < kFar; ++j) {
+                    far_lookup(j);
+                    send_for(j);
+                }
+                far_lookup(kFar);
             }
-            lookup(0);
-            for (int j = 1; j < kFar; ++j) {
-                far_lookup(j);
-                send_for(j);
-            }
-            far_lookup(kFar);
             // Round j: K of step j + 1 to shared memory (where step j's product has read), loads of step
             // j + 2's K; V of step j + 1 (where O += P V has read), loads of step j + 2's V.
 #pragma unroll 1
             for (int j = -2; j + 1 < n; ++j) {
                 if (j >= 0) ok = warp_wait<kNsConv>(s_full, j & 1) && ok;
                 if constexpr (kSel) {
-                    if (j >= -1) publish(j + 1);
-                    ok = conv_all(ok);  // leave together: place() has a barrier
+                    if (!helped) {
+                        if (j >= -1) publish(j + 1);
+                        ok = conv_all(ok);  // leave together: place() has a barrier
+                    }
                     if (j >= -1) collect(j + 1);
                 }
                 if (!ok) break;
                 if (j >= -1) write_k(j + 1);
                 if (j + 2 < n) {
-                    send_for(j + 2 + kFar);
-                    far_lookup(j + 3 + kFar);
-                    place(j + 2);
-                    load_k(j + 2);
-                    if constexpr (kSel) {
-                        ent = ent_n;
-                        ent_n = load_entry(j + 4);
+                    if (helped) {
+                        ok = warp_wait<kNsConv>(look_full + (j & 1), (j + 2) >> 1 & 1);
+                        if (!ok) break;
+                    } else {
+                        send_for(j + 2 + kFar);
+                        far_lookup(j + 3 + kFar);
+                        place(j + 2);
                     }
-                    lookup(j + 3);
+                    load_k(j + 2);
+                    if (!helped) {
+                        if constexpr (kSel) {
+                            ent = ent_n;
+                            ent_n = load_entry(j + 4, ct);
+                        }
+                        lookup(j + 3);
+                    }
                 }
                 if (j >= 0) ok = warp_wait<kNsConv>(o_done, j & 1) && ok;
                 if (j >= -1) write_v(j + 1);

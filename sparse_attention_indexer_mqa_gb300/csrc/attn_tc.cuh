@@ -109,6 +109,13 @@ __device__ __forceinline__ float write_q_rows(uint8_t* tile, const uint16_t* src
     const unsigned exist = __ballot_sync(kFull, real);
     const uint32_t lo = (uint32_t)reinterpret_cast<uintptr_t>(src), hi = (uint32_t)(reinterpret_cast<uintptr_t>(src) >> 32);
     float mine = 0.0f;
+    if (!exist) {  // the other form of the loop below, for warps that have something else to do
+#pragma unroll 1
+        for (int r = sub; r < 32; r += kAtOnce)
+            *reinterpret_cast<uint4*>(tile + dims_sub<D>(i) * (kRowsT * 128) + (first + r) * 128 +
+                                      ((dims_chunk<D>(i) ^ ((first + r) & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+        return mine;
+    }
 #pragma unroll 1
     for (int s0 = 0; s0 < kLanes; s0 += kBatch) {
         uint4 w[kBatch];

@@ -150,6 +150,29 @@ def test_tree_split(torch, Bn, Hq, Hkv, D, nq, k):
     a.check(sel)
 
 
+@pytest.mark.parametrize("D,k,heads", [(128, 300, 64), (64, 1030, 48), (128, 140, 128)])
+def test_many_lists_at_once(torch, Bn, D, k, heads):
+    """Thousands of units of the tensor-memory kernel, whose lookups and products run side by side on every SM, against 16
+    heads at a time, which take the other kernel. Either is within its own bound of the exact result, about 2^-10 of the
+    weighted codes; rows of 300 keys add up to less than 64."""
+    a = Tree(torch, [5000, 3000], [1000, 900], heads, 1, D, 64, torch.float16, k, fan=1)
+    g = torch.Generator(device="cuda").manual_seed(k)
+    sel = torch.randint(0, 2000, (a.T, k), generator=g, device="cuda", dtype=torch.int32)
+    sel[:, ::7] = torch.randint(-5, 9000, sel[:, ::7].shape, generator=g, device="cuda", dtype=torch.int32)
+    a.call(Bn, sel, a.workspace(Bn, k))
+    out, lse = a.out.clone(), a.lse.clone()
+    a.call(Bn, sel, a.workspace(Bn, k))
+    assert torch.equal(out, a.out) and torch.equal(lse, a.lse)
+    q = a.q
+    for h in range(0, heads, 16):
+        a.q, a.Hq = q[:, h:h + 16], 16
+        a.out, a.lse = torch.zeros_like(a.q), torch.zeros(a.T, 16, device="cuda")
+        a.call(Bn, sel)
+        assert int(a.status) == 0
+        assert float((a.lse - lse[:, h:h + 16]).abs().max()) < 1e-4
+        assert float((a.out.float() - out[:, h:h + 16].float()).abs().max()) < 64 * 2.0 ** -9
+
+
 @pytest.mark.parametrize("Hq,nq,D", [(4, 6, 128), (8, 40, 64), (64, 5, 128), (2, 140, 128), (2, 9, 64)])
 @pytest.mark.parametrize("long", [False, True])
 def test_tree_nan_codes(torch, Bn, Hq, nq, D, long):
