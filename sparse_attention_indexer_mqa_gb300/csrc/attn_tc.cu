@@ -370,6 +370,11 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
                             at_n[i] = (int64_t)pg[i] * a.page_stride;
                             two_n[i] = *reinterpret_cast<const uint16_t*>(pool + at_n[i] + 2ll * P * D + 2 * (tok / kKvBlock)) | 65536u;
                             at_n[i] += (int64_t)tok * 2 * D;
+                            if constexpr (kTree) {  // read by few units, as a dense tree's keys are: see send_for
+#pragma unroll
+                                for (int line = 0; line < 2 * D; line += 128)
+                                    asm volatile("prefetch.global.L2 [%0];" ::"l"(pool + at_n[i] + line));
+                            }
                         }
                     }
                 };
