@@ -159,11 +159,12 @@ def _load_torch():
     return torch
 
 
-def _stream(stream):
+def _stream(stream, dev=None):
+    """The stream's handle; dev: the current device, where the caller knows it."""
     if stream is None:
         torch = _torch or _load_torch()
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(torch.cuda.current_device() if dev is None else dev)
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -387,7 +388,7 @@ def idx_step_meta(ctx_lens, q_lens, page_table, page_size, max_seq_len_k, free_p
         ctx_lens.data_ptr(), q_lens.data_ptr(), B, page_table.data_ptr(), width, page_size, max_seq_len_k,
         free_pages.data_ptr(), free_pages.numel(), free_span.data_ptr(), num_pages, cu_seqlens_q.data_ptr(),
         seq_lens_k.data_ptr(), positions.data_ptr(), slot_mapping.data_ptr(), T, free_next.data_ptr(),
-        _status(fn, dev_status, dev), _stream(stream))
+        _status(fn, dev_status, dev), _stream(stream, dev))
     if st:
         _check(fn, st)
 
@@ -435,7 +436,7 @@ def idx_kv_store(k, v, slot_mapping, pool, num_pages, page_size, page_stride, de
     _pool_bytes(fn, pool, num_pages, page_stride, H * (2 * page_size * D + 16), dev)
     st = (_lib or load()).idx_kv_store(
         k.data_ptr(), v.data_ptr(), ft, n, H, D, kr, kh, vr, vh, slot_mapping.data_ptr(), pool.data_ptr(), num_pages,
-        page_size, page_stride, _status(fn, dev_status, dev), _stream(stream))
+        page_size, page_stride, _status(fn, dev_status, dev), _stream(stream, dev))
     if st:
         _check(fn, st)
 
@@ -501,7 +502,7 @@ def _attention(fn, q, pool, num_pages, page_size, page_stride, kv_heads, page_ta
     front = (q.data_ptr(), ft, T, H, kv_heads, D, qr, qh, pool.data_ptr(), num_pages, page_size, page_stride,
              page_table.data_ptr(), width, seq_lens_k.data_ptr(), cu_seqlens_q.data_ptr(), B)
     back = (max_q_len, max_seq_len_k, sel_p, sel_stride, n_sel, softmax_scale, out.data_ptr(), orow, oh, lse_p, ws_p, wsb,
-            _status(fn, dev_status, dev), _stream(stream))
+            _status(fn, dev_status, dev), _stream(stream, dev))
     if causal is not None:
         st = (_lib or load()).idx_attn_paged(*front, 1 if causal else 0, *back)
     else:
@@ -589,7 +590,7 @@ def idx_draft_verify(target_probs, draft_probs, tokens, parents, coins, last_coi
     st = (_lib or load()).idx_draft_verify(
         target_probs.data_ptr(), draft_p, ft, ts, ds, T, V, tokens.data_ptr(), parents.data_ptr(), coins.data_ptr(),
         last_coins.data_ptr(), cu_seqlens_q.data_ptr(), B, max_q_len, path.shape[1], path.data_ptr(), n_path.data_ptr(),
-        out_tokens.data_ptr(), _status(fn, dev_status, dev), _stream(stream))
+        out_tokens.data_ptr(), _status(fn, dev_status, dev), _stream(stream, dev))
     if st:
         _check(fn, st)
 
@@ -630,7 +631,7 @@ def idx_kv_compact(path, n_path, seq_lens_k, cu_seqlens_q, page_table, pool, num
     _layers_bytes(fn, pool, num_pages, page_stride, kv_heads * (2 * page_size * head_dim + 16), layers, layer_stride, dev)
     st = (_lib or load()).idx_kv_compact(
         *lists, pool.data_ptr(), kv_heads, head_dim, layers, layer_stride, num_pages, page_size, page_stride,
-        None if new_lens is None else new_lens.data_ptr(), _status(fn, dev_status, dev), _stream(stream))
+        None if new_lens is None else new_lens.data_ptr(), _status(fn, dev_status, dev), _stream(stream, dev))
     if st:
         _check(fn, st)
 
@@ -643,7 +644,7 @@ def idx_k_compact(path, n_path, seq_lens_k, cu_seqlens_q, page_table, dtype, poo
     _layers_bytes(fn, pool, num_pages, page_stride, (132 if dtype == IDX_FP8 else 68) * page_size, layers, layer_stride, dev)
     st = (_lib or load()).idx_k_compact(
         *lists, dtype, pool.data_ptr(), layers, layer_stride, num_pages, page_size, page_stride,
-        None if new_lens is None else new_lens.data_ptr(), _status(fn, dev_status, dev), _stream(stream))
+        None if new_lens is None else new_lens.data_ptr(), _status(fn, dev_status, dev), _stream(stream, dev))
     if st:
         _check(fn, st)
 
@@ -670,7 +671,7 @@ def idx_pages_update(parent, keep, page_table, lens, page_size, new_table, new_l
         parent.data_ptr(), keep.data_ptr(), n, page_table.data_ptr(), width, lens.data_ptr(), B, page_size,
         new_table.data_ptr(), new_width, new_lens.data_ptr(), shares.data_ptr(), new_shares.data_ptr(), pages,
         free_pages.data_ptr(), free_pages.numel(), free_span.data_ptr(), new_free.data_ptr(), new_free.numel(),
-        new_span.data_ptr(), copies.data_ptr(), _status(fn, dev_status, dev), _stream(stream))
+        new_span.data_ptr(), copies.data_ptr(), _status(fn, dev_status, dev), _stream(stream, dev))
     if st:
         _check(fn, st)
 
@@ -686,6 +687,6 @@ def idx_pages_copy(copies, pool, num_pages, page_bytes, page_stride, layers=1, l
     _layers_bytes(fn, pool, num_pages, page_stride, page_bytes, layers, layer_stride, dev)
     st = (_lib or load()).idx_pages_copy(
         copies.data_ptr(), n, pool.data_ptr(), layers, layer_stride, num_pages, page_bytes, page_stride,
-        _status(fn, dev_status, dev), _stream(stream))
+        _status(fn, dev_status, dev), _stream(stream, dev))
     if st:
         _check(fn, st)

@@ -1,5 +1,5 @@
-// attn.cu -- attention over the 8-bit paged KV cache for few query rows per kv head (decode), the join of a
-// split key axis, and the choice between this kernel and the tensor-memory one (attn_tc.cu).
+// attn.cu -- attention over the 8-bit paged KV cache for few query rows per kv head (decode, small trees of drafted
+// tokens), the join of a split key axis, and the choice between this kernel and the tensor-memory one (attn_tc.cu).
 //
 // A unit is up to 16 query rows of one kv head (the rows of its group of heads, token after
 // token) against a range of keys. Its four warps take 32 keys in turn, each with a running softmax
@@ -635,24 +635,27 @@ int64_t shared_rows(const AttnArgs& a) { return a.n_sel ? a.group : (int64_t)a.m
 // one sequence: 10.1 us against 14.8; 64 x 8192 keys: 59 against 58), more the tensor-memory one (64 heads, 64 x 8192
 // keys: 62 against 93). Lists, whose keys are gathered for each tile: up to one (4096 queries x 1024 keys, 16 heads:
 // 207 us against 380; 32 heads in two tiles 413 against 389).
+//
+// Trees, whose nodes make more rows than a decode's: up to four mma.sync tiles where all tiles' keys together are few, for
+// the tensor-memory kernel's start alone takes longer then. 64 rows (8 nodes, 8 heads): on one kv head and 512 keys 9.8 us
+// against 13.2, 8192 keys 11.6 / 14.8, on eight heads and 2048 keys 13.4 / 14.3 (65,000 keys of all tiles), 64 x 512 keys
+// 13.8 / 15.7 (131,000), but 8 x 8192 keys 23.3 / 19.0 (262,000); 128 rows on 8 x 2048 keys 17.4 / 15.9. Lists, 64 heads: 8
+// nodes of 1024 keys 11.9 / 16.3 (33,000), 16 of them 14.7 / 16.8, 32 17.2 / 17.3 (132,000), 128 of 256 keys 20.7 / 13.9
+// (135,000), 152 of 120 15.3 / 9.9 (78,000, but in more than one round of CTAs).
 struct Choice {
     bool tile;
     int64_t units;
     int per_sm;  // resident CTAs
 };
-//
-// Trees, whose nodes make more rows than a decode's: up to four mma.sync tiles where all tiles' keys together are few, for
-// the tensor-memory kernel's start alone takes longer then. 64 rows (8 nodes, 8 heads): on one kv head and 512 keys 9.8 us against 13.2,
-// 8192 keys 11.6 / 14.8, on eight heads and 2048 keys 13.4 / 14.3 (65,000 keys of all tiles), 64 x 512 keys 13.8 / 15.7
-// (131,000), but 8 x 8192 keys 23.3 / 19.0 (262,000); 128 rows on 8 x 2048 keys 17.4 / 15.9. Lists, 64 heads: 8 nodes of
-// 1024 keys 11.9 / 16.3 (33,000), 16 of them 14.7 / 16.8, 32 17.2 / 17.3 (132,000), 128 of 256 keys 20.7 / 13.9 (135,000), 152 of 120 15.3 / 9.9 (78,000, but two rounds of tiles).
 constexpr int kTreeRows = 64, kTreeKeys = 1024, kTreeEntries = 512;  // the latter two per SM
 Choice choose(const AttnArgs& a) {
     const int64_t rows = shared_rows(a), times = (a.n_sel ? a.T : (int64_t)a.B) * a.kv_heads;
     const int64_t few = times * ((rows + 15) / 16), keys = a.n_sel ? a.n_sel + a.max_q_len : a.max_seq_len_k;
-    const int64_t sms = device_sm_count();
-    const bool small = few <= 2 * sms && few * keys <= (a.n_sel ? kTreeEntries : kTreeKeys) * sms;
-    if (rows <= (a.n_sel ? 16 : 32) || (a.tree && rows <= kTreeRows && small)) return {false, few, 3};
+    if (rows <= (a.n_sel ? 16 : 32)) return {false, few, 3};
+    if (a.tree && rows <= kTreeRows) {
+        const int64_t sms = device_sm_count();
+        if (few <= 2 * sms && few * keys <= (a.n_sel ? kTreeEntries : kTreeKeys) * sms) return {false, few, 3};
+    }
     return {true, times * ((rows + 127) / 128), 2};
 }
 

@@ -1,5 +1,5 @@
 // attn_tc.cu -- attention over the 8-bit paged KV cache for many query rows per kv head (prefill, chunks,
-// large groups of heads) on the tensor cores with tensor-memory accumulators.
+// large groups of heads, trees of drafted tokens) on the tensor cores with tensor-memory accumulators.
 //
 // A unit is a tile of 128 query rows of one kv head (token-major: row = token * group + head of the
 // group; with a list of keys, the group's heads of one token) against a range of keys, 128 at a
@@ -19,7 +19,7 @@
 // (tensor memory 2 x 256 columns, shared memory 2 x 107 KB): one's products run under the other's
 // softmax.
 //
-// What bounds it. That prompt takes 609 us, 903 TFLOP/s of its visible pairs (47 % of a large bf16 product's measured
+// What bounds it. That prompt takes 588 us, 935 TFLOP/s of its visible pairs (47 % of a large bf16 product's measured
 // rate). Eight MMAs of 128 x 128 x 16 take 736 cycles (both operands in shared memory) or 679
 // (P in tensor memory) with nothing else on the SM, so a step needs 1415 cycles of the tensor pipe;
 // a CTA's step takes 4400: S 740, softmax 1950, O += P V 700, and 200 to 500 from each to
@@ -27,8 +27,17 @@
 // an N = 64 MMA takes as long as an N = 128 one: 600 us, and 548 with lists, which were at 443 then),
 // with K's and V's converters apart (645, 518); two tiles to a CTA that share converted K and V (698, and
 // 685 with the tiles' MMAs in turn); the softmax in one pass over S with P kept in registers
-// (665). With lists (4096 queries x 1024 keys, 64 heads over 1: 450 us) half of a tile's rows are
-// empty and a unit is only eight steps long; the order of the keys hardly matters (447 in order, 453 at random).
+// (665). With lists (4096 queries x 1024 keys, 64 heads over 1: 386 us) half of a tile's rows are
+// empty and a unit is only eight steps long; the order of the keys hardly matters (447 in order, 453 at random, when the
+// converters still looked the keys up).
+//
+// Trees. 64 requests of 16 nodes on 8176 keys, 64 heads over 8, are 512 units of 128 rows and 65 steps: 338 us, where the cache
+// (1.1 GB) takes 164 at the copy rate and the products 139. Each key is read by one unit, from memory: 391 us until it was sent for
+// into L2 (send_for), 346 until q and the results moved in whole lines. 304 CTAs fit, so the units take 1.7 rounds and two are
+// paid for; a step is 4800 cycles (S 850, softmax 2100, O += P V 900, waits 950) and 5500 with two CTAs on the SM, whose
+// shared-memory port is then about three quarters busy (operands written and read, tensor pipe 35 %, ALU 38 %: profiles). Lists of
+// 1024 keys and 8 nodes for 64 requests: 80 us, 23 at the copy rate; nine steps a unit and two rounds, a converter's step of
+// 5000 cycles, half of it folding scales into operands.
 #include "attn_tc.cuh"
 
 namespace idx {

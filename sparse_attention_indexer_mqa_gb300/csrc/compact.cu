@@ -8,6 +8,11 @@
 // that its tokens come from (its own too where it keeps tokens in front of the tree), and codes from blocks of a smaller one shift
 // down by the difference: a power of two, so exact but for codes that become subnormal.
 // Indexer's cache: scales belong to tokens, the bytes move as they are.
+//
+// A warp per request, head and layer (a lane has 16 bytes of two or four tokens): the chains of loads, lengths, path, page
+// table, scales, rows, are what it takes, and there are many of them. In replayed graphs 64 requests of up to 6 tokens in 8 layers
+// of 8 heads (4.8 MB moved) take 6.6 us, 64 of up to 9 in one layer of the indexer's cache 3.9, about 1 of it for the kernel that
+// orders new_lens; a call from the host takes 10.
 #include <cuda_fp16.h>
 
 #include "common.cuh"

@@ -7,8 +7,15 @@
 //   3. numbers the fresh pages (a prefix sum over the rows) and writes the rows; what a replaced page or a refused row
 //      held is taken back;
 //   4. collects the pages whose count fell below zero, in page order, behind what is left of the free list.
-// The steps depend on one another through counts that any row may change, so they are phases of one cluster of eight
-// CTAs with its barrier between them (counts are whole numbers: the order of the atomics does not show).
+// The steps depend on one another through counts that any row may change, so they are phases of one cluster with its
+// barrier between them (counts are whole numbers: the order of the atomics does not show). A present row's first heir
+// keeps its holders, so rows that merely go on change no count.
+//
+// Measured in replayed graphs: 64 rows of up to 64 pages, 6000 pages 10.8 us, 1024 rows of up to 250 pages that fork, shrink and
+// end, 200,000 pages 23.4 us (3.1 MB; 63.6 with every holder counted twice, one load at a time and two passes over the pages). Both
+// are chains of latencies: five barriers of 1100 to 1500 cycles, and between them two to four dependent loads, eight in flight a
+// thread. Launches in place of barriers would cost more, and the host 2 us each. Copies of pages: 54 us for 43 pages of 262 KB in 16
+// layers, 6.7 TB/s read and written, the measured copy rate.
 #include <cooperative_groups.h>
 
 #include "common.cuh"
@@ -48,7 +55,8 @@ __device__ __forceinline__ int cta_sum(int v, int* warp_sums, int& total) {
 // Dynamic shared memory: three words per next row (heirs and fresh pages take turns, heirs being one per present row), then a
 // bitmap of kSegment pages.
 constexpr int kSegment = 131072;
-constexpr int64_t kMany = 100000;  // table entries and pages from which a wide cluster is taken
+constexpr int64_t kMany = 100000;  // table entries and pages from which a wide cluster is taken (23.4 us against 33.3 above; 64 rows
+                                   // 10.8 with eight CTAs, 11.0 with sixteen)
 inline size_t pages_smem(int32_t n_out, int32_t B) {
     return (2 * (size_t)n_out + (size_t)(n_out > B ? n_out : B)) * sizeof(int32_t) + kSegment / 8;
 }

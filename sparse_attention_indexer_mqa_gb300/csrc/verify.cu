@@ -9,14 +9,22 @@
 // running sum passes r times the row's sum. The last rejection's pass has left the sums that the search starts from.
 //
 // Sums. The draw looks for a border among a vocabulary's running sums, and with 2^17 of them an error of 2^-24 in each
-// would move one draw in a hundred. fp64 has a 64th of fp32's rate here (a few scalar operations of it in every warp
-// were most of a small call's time), so weights, sums and what is compared with them are pairs of fp32: a value and what its
-// rounding lost, by error-free sums and products, about 2^-46 of the sum.
+// would move one draw in a hundred. fp64 has a 64th of fp32's rate here, so weights, sums and what is compared with them
+// are pairs of fp32: a value and what its rounding lost, by error-free sums and products, about 2^-46 of the sum.
 //
 // A cluster of up to eight CTAs per request: the row is cut into a slice for each, a slice into the CTA's warps' parts. All
 // threads follow the walk by themselves; a pass ends with one cluster barrier, behind which every CTA adds up the
 // slices' sums in the same order. What the walk asks of each node (its parent, token, number and the two
-// probabilities) is fetched for 1024 nodes at once, so that a step between passes is no chain of loads.
+// probabilities) is fetched for 256 nodes at once, so that a step between passes is no chain of loads. The CTA whose slice holds
+// the draw's border searches the part of the warp that holds it with all its threads.
+//
+// Measured in replayed graphs. 64 trees of 32 nodes, 131072 tokens, fp32: 28.6 us. One pass for each (67 MB) is 9.9 us at the copy
+// rate and takes 6 to 9 us here, but a request of three or four passes, each behind the decision that the one before allows,
+// sets the end; a pass of few requests is bound by its SMs' issue (16 instructions an entry of p and q, 10 of p alone) and by the
+// loads' latency, four vectors of either row a thread. Without a drafter, one pass: 14.9 us. One chain of 4 drafts,
+// 49999 tokens, bf16: 7.8 us: launch, three dependent loads, the pass with its barriers, the search; a call from the
+// host takes 10. Before: a CTA per request, sums in fp64 907; a cluster 68; no fp64 (its few scalar operations in every warp
+// were half of it) and the search by a whole CTA 36; no test per vector 30.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -32,7 +40,7 @@ namespace idx {
 
 namespace {
 
-constexpr int kThreadsV = 512, kWarpsV = kThreadsV / 32, kCtasMost = 8;
+constexpr int kThreadsV = 256, kWarpsV = kThreadsV / 32, kCtasMost = 8;
 constexpr int kNodes = kThreadsV;  // nodes that are staged at once
 constexpr int kAhead = 4;          // vectors of either row that a thread has on their way
 
@@ -167,7 +175,7 @@ __device__ __forceinline__ void weigh(const Pair& cut, uint32_t gone, const floa
 }
 
 template <typename T, bool kDrafter>
-__global__ void __launch_bounds__(kThreadsV, 2) draft_verify_kernel(const VerifyArgs a) {
+__global__ void __launch_bounds__(kThreadsV, 4) draft_verify_kernel(const VerifyArgs a) {
     constexpr int kVec = Row<T>::kVec;
     // without a drafter: a bit for each token of the CTA's slice that was rejected, from the slice's first vector on
     extern __shared__ uint32_t gone[];
@@ -524,9 +532,10 @@ cudaError_t launch_form(const VerifyArgs& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     const int sms = device_sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
-    // two CTAs fit on an SM: as many to a request as there is room for
+    // Four CTAs fit on an SM: as many to a request as there is room for. (64 requests: 28.6 us; 512 threads, two to an SM
+    // 29.6, 1024, one to an SM 48; a single small request 7.8, 8.4 and 9.5.)
     int ctas = kCtasMost;
-    while (ctas > 1 && (int64_t)a.B * ctas > 2 * sms) ctas /= 2;
+    while (ctas > 1 && (int64_t)a.B * ctas > 4 * sms) ctas /= 2;
     const int64_t slice = (((a.V + 2 * kVec - 2) / kVec + ctas - 1) / ctas) * kVec;  // as if no row were aligned
     const size_t smem = kDrafter ? 0 : (size_t)(slice + 31) / 32 * 4;
     return launch_cluster(kernel, dim3((unsigned)(a.B * ctas)), dim3(kThreadsV), ctas, smem, st, a);
