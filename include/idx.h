@@ -566,7 +566,8 @@ int idx_attn_tree(const void* q, int32_t ftype, int64_t T, int32_t q_heads, int3
  * Outputs: n_path int32 [B]: accepted nodes, node 0 among them (0 for a sequence without rows); path int32 [B][max_path]:
  *   those nodes, increasing; out_tokens int32 [B][max_path]: the tokens of path[1] .. and then the drawn one, n_path of
  *   them. -1 behind. A sequence whose rows break their bounds (as in idx_attn_paged) gets n_path 0 and sets IDX_STATUS_BAD_LEN.
- * V <= 2^20 (IDX_EUNSUPPORTED above). Reads the rows of the nodes that the walk stands on, no others.
+ * V <= 2^20 (IDX_EUNSUPPORTED above). Reads the rows of the nodes that the walk stands on,
+ * and of other nodes at most single entries: that of a child's token in its parent's row.
  */
 int idx_draft_verify(const void* target_probs, const void* draft_probs, int32_t ptype,
                      int64_t target_stride, int64_t draft_stride, int64_t T, int32_t V,

@@ -149,7 +149,7 @@ __global__ void step_meta_kernel(const MetaArgs a, int rows_per_cta) {
     }
 }
 
-// Behind the metadata: returns when they are visible. The library's kernels read lengths and page tables before they
+// Behind the metadata, and behind other kernels that write lengths or tables: returns when they are visible. The library's kernels read lengths and page tables before they
 // wait for the kernel in front of them, and a kernel launched with programmatic serialization may start as
 // soon as the CTAs of that one have ended. In front of them is this one, whose CTA ends behind its wait: whatever
 // is launched next, eagerly, captured or replayed, starts when the metadata are there. It is resident while the

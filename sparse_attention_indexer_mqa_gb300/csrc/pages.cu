@@ -14,7 +14,7 @@
 // Measured in replayed graphs: 64 rows of up to 64 pages, 6000 pages 10.8 us, 1024 rows of up to 250 pages that fork, shrink and
 // end, 200,000 pages 23.4 us (3.1 MB; 63.6 with every holder counted twice, one load at a time and two passes over the pages). Both
 // are chains of latencies: five barriers of 1100 to 1500 cycles, and between them two to four dependent loads, eight in flight a
-// thread. Launches in place of barriers would cost more, and the host 2 us each. Copies of pages: 54 us for 43 pages of 262 KB in 16
+// thread. Copies of pages: 54 us for 43 pages of 262 KB in 16
 // layers, 6.7 TB/s read and written, the measured copy rate.
 #include <cooperative_groups.h>
 

@@ -9,7 +9,7 @@
 // running sum passes r times the row's sum. The last rejection's pass has left the sums that the search starts from.
 //
 // Sums. The draw looks for a border among a vocabulary's running sums, and with 2^17 of them an error of 2^-24 in each
-// would move one draw in a hundred. fp64 has a 64th of fp32's rate here, so weights, sums and what is compared with them
+// could move up to one draw in a hundred. fp64 has a 64th of fp32's rate here, so weights, sums and what is compared with them
 // are pairs of fp32: a value and what its rounding lost, by error-free sums and products, about 2^-46 of the sum.
 //
 // A cluster of up to eight CTAs per request: the row is cut into a slice for each, a slice into the CTA's warps' parts. All
@@ -18,13 +18,13 @@
 // probabilities) is fetched for 256 nodes at once, so that a step between passes is no chain of loads. The CTA whose slice holds
 // the draw's border searches the part of the warp that holds it with all its threads.
 //
-// Measured in replayed graphs. 64 trees of 32 nodes, 131072 tokens, fp32: 28.6 us. One pass for each (67 MB) is 9.9 us at the copy
-// rate and takes 6 to 9 us here, but a request of three or four passes, each behind the decision that the one before allows,
-// sets the end; a pass of few requests is bound by its SMs' issue (16 instructions an entry of p and q, 10 of p alone) and by the
-// loads' latency, four vectors of either row a thread. Without a drafter, one pass: 14.9 us. One chain of 4 drafts,
-// 49999 tokens, bf16: 7.8 us: launch, three dependent loads, the pass with its barriers, the search; a call from the
-// host takes 10. Before: a CTA per request, sums in fp64 907; a cluster 68; no fp64 (its few scalar operations in every warp
-// were half of it) and the search by a whole CTA 36; no test per vector 30.
+// Measured. 64 trees of 32 nodes, 131072 tokens, fp32: 28.1 us in a replayed graph, whose rows (67 MB) stay in L2; 34 among
+// other calls, 40 with L2 flushed and events included. One pass for each is 9.9 us at the copy rate, but a request of three or
+// four passes, each behind the decision that the one before allows, sets the end; a pass of few requests is bound by the
+// loads' latency, four vectors of either row a thread, and the barriers. One chain of 4 drafts,
+// 49999 tokens, bf16: 7.9 us in a graph: launch, three dependent loads, the pass with its barriers, the search; a call from the
+// host takes 10. Before: a CTA per request, sums in fp64 907; a cluster 68; batched loads and the search
+// by a whole CTA 53; no fp64 36; no test per vector 30.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
