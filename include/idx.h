@@ -568,6 +568,7 @@ int idx_attn_tree(const void* q, int32_t ftype, int64_t T, int32_t q_heads, int3
  *   them. -1 behind. A sequence whose rows break their bounds (as in idx_attn_paged) gets n_path 0 and sets IDX_STATUS_BAD_LEN.
  * V <= 2^20 (IDX_EUNSUPPORTED above). Reads the rows of the nodes that the walk stands on,
  * and of other nodes at most single entries: that of a child's token in its parent's row.
+ * The outputs may not overlap the inputs or one another (IDX_EINVAL).
  */
 int idx_draft_verify(const void* target_probs, const void* draft_probs, int32_t ptype,
                      int64_t target_stride, int64_t draft_stride, int64_t T, int32_t V,
@@ -592,8 +593,8 @@ int idx_draft_verify(const void* target_probs, const void* draft_probs, int32_t 
  *   negative, above pt_stride * page_size, or whose n_path is negative or above max_path or its rows is left alone too and sets
  *   IDX_STATUS_BAD_LEN; one whose path does not increase or leaves the tree IDX_STATUS_BAD_VALUE (new length: seq_lens_k, at
  *   least 0). A token whose page, or whose destination's, is outside the pool does not move (IDX_STATUS_BAD_PAGE).
- * Sequences may share pages in front of their trees only (idx_pages_update keeps it so). new_lens may not be one of the
- *   inputs. layers <= 65535.
+ * Sequences may share pages in front of their trees only (idx_pages_update keeps it so). new_lens may not overlap the
+ *   inputs (IDX_EINVAL), and the lists may not lie in pages. layers <= 65535; with layers 0 nothing is done, new_lens is not written.
  */
 int idx_kv_compact(const int32_t* path, int32_t max_path, const int32_t* n_path,
                    const int32_t* seq_lens_k, const int32_t* cu_seqlens_q, int32_t B,
@@ -629,7 +630,7 @@ int idx_k_compact(const int32_t* path, int32_t max_path, const int32_t* n_path,
  *   and becomes an empty row, and what it would have held is released. A page id outside [0, num_pages) is passed on but not counted
  *   (IDX_STATUS_BAD_PAGE); a page released more often than it was held becomes free once (IDX_STATUS_BAD_PAGE); a
  *   free_span outside [0, free_cap] is taken as empty (IDX_STATUS_BAD_PAGE).
- * B, n_out <= 16384, num_pages <= 2^30 (IDX_EUNSUPPORTED above). Outputs may not be inputs (but new_shares may be shares) nor one another. What
+ * B, n_out <= 16384, num_pages <= 2^30 (IDX_EUNSUPPORTED above). Outputs may not overlap inputs (but new_shares may be shares) nor one another (IDX_EINVAL). What
  *   follows on the stream starts when the outputs are visible.
  */
 int idx_pages_update(const int32_t* parent, const int32_t* keep, int32_t n_out,

@@ -302,3 +302,37 @@ def test_hand_worked_pages():
     assert t == [[5, 6], [5, 2], [5, -1]] and lens == [100, 100, 64]
     assert shares == [0, 0, 0, 0, 0, 2, 0, 0, 0, 0] and copies == [[-1, -1], [6, 2], [-1, -1]]
     assert free[:3] == [3, 7, 8] and span == [0, 3] and status == 0
+
+
+# ------------------------------------------------------------------------------ arrays that overlap in part
+
+@pytest.mark.parametrize("kw", [
+    dict(path=36), dict(path=28), dict(path=84), dict(n=84), dict(n=104), dict(out=100), dict(out=60, mp=2), dict(out=1148),
+    dict(n=2172), dict(path=16384, B=1 << 30, mp=1 << 30, n=1 << 60, out=1 << 61),
+])
+def test_verify_refuses_partial_overlap(lib, kw):
+    """Addresses that are nobody's first one: a word of an output inside an input (path in parents, tokens or lengths, out in coins,
+    the last probability of either side), of an output inside another, and sizes whose product passes 64 bits."""
+    assert _verify(lib, **kw) == -1
+
+
+@pytest.mark.parametrize("kw", [dict(nl=20), dict(nl=28), dict(nl=68), dict(nl=84), dict(B=3, n=128, sl=144, cu=160, pt=192, nl=152),
+                                dict(B=2, n=128, sl=144, cu=160, pt=192, nl=140)])
+def test_compact_refuses_partial_overlap(lib, kw):
+    """new_lens inside the path, the row bounds, the table or the lengths, and running into them from in front."""
+    assert _kv(lib, **kw) == -1
+    assert _k(lib, **kw) == -1
+
+
+_APART = dict(par=4096, keep=4112, pt=4128, lens=4160, nt=4224, nl=4256, sh=4352, ns=4416, fp=4480, fs=4544, nf=4608, nsp=4672,
+              cp=4736)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(nl=4100), dict(nl=4108), dict(nt=4120), dict(nt=4132), dict(cp=4164), dict(nl=4156), dict(ns=4356), dict(ns=4324),
+    dict(nf=4484), dict(nsp=4548), dict(nsp=4540), dict(nf=4420), dict(cp=4228), dict(nsp=4740),
+])
+def test_pages_update_refuses_partial_overlap(lib, kw):
+    """A word of an output inside parent, keep, table, lengths, counts (new counts are the counts as a whole or apart from them),
+    free pages or their span, and of one output inside another."""
+    assert _pages(lib, **{**_APART, **kw}) == -1
