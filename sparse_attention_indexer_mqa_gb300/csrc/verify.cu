@@ -334,9 +334,10 @@ __global__ void __launch_bounds__(kThreadsV, 4) draft_verify_kernel(const Verify
             fast(std::integral_constant<int, kLessCutQ>{});
         const bool again = bits >= 0x7f800000u;  // this thread's once more
         if (again) s[0] = s[1] = s[2] = s[3] = zero;
-        // what the row's ends cut, or all of it where p and q are not aligned alike
+        // What the row's ends cut, or all of it where p and q are not aligned alike, and once more what this thread has thrown
+        // away: a vector from f0 on is the same thread's as above; the only one that can lie in front of f0 is k0.
 #pragma unroll 1
-        for (int k = k0 + lane; k < k1; k += 32) {
+        for (int k = k0 < f0 && lane == 31 ? k0 : f0 + lane; k < k1; k += 32) {
             if (!again && k >= f0 && k < f1) {
                 k += (f1 - 1 - k) / 32 * 32;
                 continue;

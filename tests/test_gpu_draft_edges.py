@@ -1,0 +1,67 @@
+"""Verification on the GPU with entries that are no probabilities, or unusual ones, anywhere in rows of any alignment."""
+import math
+
+import pytest
+
+from test_gpu_attn import Bn, torch  # noqa: F401  (fixtures)
+from test_gpu_draft import check_verify, walk_inputs
+
+pytestmark = pytest.mark.gpu
+
+NONE = (-0.25, math.nan, math.inf, -math.inf, -2.0 ** -14)  # count as 0 and are reported
+UNUSUAL = (-0.0, 2.5, 2.0, 100.0)                           # are what they are
+
+
+def plant_entries(w, values, places):
+    """In every row of sequence b the value b stands for, at the places; never in the tokens that its nodes name."""
+    for b, (t0, t1) in enumerate(zip(w["cu"], w["cu"][1:])):
+        named = set(w["tokens"][t0:t1])
+        at = [x for x in places if x not in named]
+        for x in (w["target"], w["draft"]):
+            if x is not None:
+                x[t0:t1, at] = values[b % len(values)]
+
+
+def aligned_elsewhere(torch, x, shift):
+    """x with rows of an odd distance that begin `shift` elements behind a 16-byte boundary."""
+    T, V = x.shape
+    wide = torch.full((T, V + (V + 1) % 2), 0.5, dtype=x.dtype, device="cuda")
+    flat = torch.full((wide.numel() + 16,), 0.5, dtype=x.dtype, device="cuda")
+    y = flat[shift:shift + wide.numel()].view(wide.shape)[:, :V]
+    y.copy_(x.cuda())
+    return y
+
+
+@pytest.mark.parametrize("V", [4099, 50001, 131073])
+@pytest.mark.parametrize("dt", ["float32", "bfloat16", "float16"])
+@pytest.mark.parametrize("drafter", [False, True])
+@pytest.mark.parametrize("values,bad", [(NONE, True), (UNUSUAL, False)])
+def test_verify_unusual_entries(torch, Bn, V, dt, drafter, values, bad):
+    """Odd row lengths, three nodes to a sequence: rows of every alignment. Coins near 1 reject."""
+    w = walk_inputs(torch, [3] * 10, V, getattr(torch, dt), 2, V, drafter)
+    clean = {k: None if w[k] is None else w[k].clone() for k in ("target", "draft")}
+    w["coins"] = [0.99 if t % 2 else 0.6 for t in range(30)]
+    for places in ([20], [V // 2, V // 2 + 41], [V - 3, V - 1000], [0, V - 1], [5, V // 3, V // 5 * 4]):
+        w.update({k: None if x is None else x.clone() for k, x in clean.items()})
+        plant_entries(w, values, places)
+        check_verify(torch, Bn, w, 3, Bn.IDX_STATUS_BAD_VALUE if bad else 0)
+
+
+@pytest.mark.parametrize("dt,shifts", [("float32", range(4)), ("bfloat16", (0, 1, 5, 7))])
+@pytest.mark.parametrize("drafter", [False, True])
+def test_verify_one_bad_entry(torch, Bn, dt, shifts, drafter):
+    """One sequence, one entry: it is reported wherever it lies, and the sums count every other entry once. The drafter's
+    rows are aligned like the target's, and unlike them."""
+    V = 4099
+    for shift in shifts:
+        for other in (shift, shift + 1):
+            for at in (0, 3, 20, 130, 517, 1024, 2050, 4000, 4098):
+                w = walk_inputs(torch, [2], V, getattr(torch, dt), 1, at, drafter)
+                w["coins"] = [1.0, 1.0]  # a rejection wherever q > p
+                w["target"][:, at] = math.nan
+                w["target"] = aligned_elsewhere(torch, w["target"], shift)
+                if drafter:
+                    w["draft"] = aligned_elsewhere(torch, w["draft"], other)
+                for last in (0.9, 0.1):
+                    w["last"] = [last]
+                    check_verify(torch, Bn, w, 2, Bn.IDX_STATUS_BAD_VALUE)
