@@ -1,4 +1,5 @@
-"""Verification on the GPU with entries that are no probabilities, or unusual ones, anywhere in rows of any alignment."""
+"""The drafting step's operators on the GPU where their inputs are unusual: verification with entries that are no probabilities,
+or large ones, anywhere in rows of any alignment; page copies with passed-over pairs."""
 import math
 
 import pytest
@@ -65,3 +66,30 @@ def test_verify_one_bad_entry(torch, Bn, dt, shifts, drafter):
                 for last in (0.9, 0.1):
                     w["last"] = [last]
                     check_verify(torch, Bn, w, 2, Bn.IDX_STATUS_BAD_VALUE)
+
+
+# ------------------------------------------------------------------------------ page copies
+
+@pytest.mark.parametrize("n,layers,page,every", [(64, 16, 8 * 32784, 3), (65, 2, 4352, 1), (7, 1, 16, 2), (1, 3, 8208, 0)])
+@pytest.mark.parametrize("seed", range(4))
+def test_pages_copy_with_passed_over_pairs(torch, Bn, n, layers, page, every, seed):
+    """Pairs that are passed over leave every page alone, the pool's first and last too, which other pairs write or
+    read: equal to copies made one pair after the other."""
+    g = torch.Generator().manual_seed(seed)
+    pages = 2 * n + 3
+    others = (torch.randperm(pages - 2, generator=g) + 1)[:2 * n].tolist()
+    pairs = [[others[2 * i], others[2 * i + 1]] for i in range(n)]
+    pairs[0][seed & 1] = pages - 1              # the last page read, or written
+    pairs[-1][1 - (seed & 1)] = 0               # the first page the other way round
+    for i in range(n):
+        if every and i % (every + 1) == every:
+            pairs[i][seed % 2] = -1 - i
+    pool = torch.randint(0, 256, (layers, pages, page), generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda", dtype=torch.uint8)
+    want = pool.clone()
+    for src, dst in pairs:
+        if src >= 0 and dst >= 0:
+            want[:, dst] = pool[:, src]
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    Bn.idx_pages_copy(torch.tensor(pairs, dtype=torch.int32, device="cuda"), pool, pages, page, page, layers=layers,
+                      layer_stride=pool.stride(0), dev_status=st)
+    assert int(st) == 0 and torch.equal(pool, want)
