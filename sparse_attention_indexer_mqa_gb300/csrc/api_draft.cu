@@ -150,7 +150,8 @@ int idx_pages_update(const int32_t* parent, const int32_t* keep, int32_t n_out, 
     if (page_size != 64 && page_size != 128) return IDX_EUNSUPPORTED;
     if (n_out > idx::kPagesMaxRows || B > idx::kPagesMaxRows || num_pages > (1 << 30)) return IDX_EUNSUPPORTED;
     if (new_free_cap < num_pages) return IDX_EINVAL;  // every page may become free
-    if (!free_span || !new_span || (free_cap > 0 && !free_pages) || (num_pages > 0 && (!shares || !new_shares || !new_free)))
+    if (new_free_cap > 0 && !new_free) return IDX_EINVAL;  // without pages too: what is left of the free list goes there
+    if (!free_span || !new_span || (free_cap > 0 && !free_pages) || (num_pages > 0 && (!shares || !new_shares)))
         return IDX_EINVAL;
     if (B > 0 && (!lens || (pt_stride > 0 && !page_table))) return IDX_EINVAL;
     if (n_out > 0 && (!parent || !keep || !new_lens || !copies || (new_stride > 0 && !new_table))) return IDX_EINVAL;

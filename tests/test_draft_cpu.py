@@ -336,3 +336,18 @@ def test_pages_update_refuses_partial_overlap(lib, kw):
     """A word of an output inside parent, keep, table, lengths, counts (new counts are the counts as a whole or apart from them),
     free pages or their span, and of one output inside another."""
     assert _pages(lib, **{**_APART, **kw}) == -1
+
+
+# ------------------------------------------------------------------------------ free lists without pages of their own
+
+@pytest.mark.parametrize("kw", [dict(nf=None), dict(nf=None, nfc=1), dict(nf=None, no=0, B=0)])
+def test_pages_update_refuses_a_free_list_without_memory(lib, kw):
+    """No page is counted, yet what is left of free_pages is passed on to new_free."""
+    assert _pages(lib, **{**_APART, "np": 0, "sh": None, "ns": None, **kw}) == -1
+
+
+def test_pages_update_without_any_list_reaches_the_launch(calls):
+    """Empty tensors have null pointers: the binding hands them on with length 0."""
+    pages(shares=z(0), new_shares=z(0), free=z(0), new_free=z(0))
+    args = calls[0][1]
+    assert args[13] == 0 and args[15] == 0 and args[18] == 0
