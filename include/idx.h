@@ -568,7 +568,7 @@ int idx_attn_tree(const void* q, int32_t ftype, int64_t T, int32_t q_heads, int3
  *   them. -1 behind. A sequence whose rows break their bounds (as in idx_attn_paged) gets n_path 0 and sets IDX_STATUS_BAD_LEN.
  * V <= 2^20 (IDX_EUNSUPPORTED above). Reads the rows of the nodes that the walk stands on,
  * and of other nodes at most single entries: that of a child's token in its parent's row.
- * The outputs may not overlap the inputs or one another (IDX_EINVAL).
+ * The outputs may not overlap the inputs (what lies between two rows belongs to them) or one another (IDX_EINVAL).
  */
 int idx_draft_verify(const void* target_probs, const void* draft_probs, int32_t ptype,
                      int64_t target_stride, int64_t draft_stride, int64_t T, int32_t V,

@@ -13,16 +13,16 @@ bool layers_apart(int32_t layers, int64_t layer_stride, int64_t num_pages, int64
     return layer_stride >= whole || (layer_stride >= page_bytes && (__int128)(layers - 1) * layer_stride + page_bytes <= page_stride);
 }
 
-// An array of the caller's, in 4-byte words; NULL or empty arrays overlap nothing.
-struct Words {
+// An array of the caller's, in bytes; NULL or empty arrays overlap nothing.
+struct Bytes {
     const void* at;
     __int128 n;
 };
-Words words(const void* p, int64_t rows, int64_t width = 1) { return {p, (__int128)rows * width}; }
-bool overlap(const Words& x, const Words& y) {
+Bytes words(const void* p, int64_t rows, int64_t width = 1) { return {p, 4 * ((__int128)rows * width)}; }  // of 4 bytes each
+bool overlap(const Bytes& x, const Bytes& y) {
     if (!x.at || !y.at || x.n <= 0 || y.n <= 0) return false;
     const __int128 a = (__int128)reinterpret_cast<uintptr_t>(x.at), b = (__int128)reinterpret_cast<uintptr_t>(y.at);
-    return a < b + 4 * y.n && b < a + 4 * x.n;
+    return a < b + y.n && b < a + x.n;
 }
 
 // what both caches' compaction asks of its lists
@@ -41,9 +41,9 @@ int check_compact(const int32_t* path, int32_t max_path, const int32_t* n_path, 
         !aligned(page_table, 4) || !aligned(new_lens, 4))
         return IDX_EINVAL;
     // warps that have tested the lists read them again while another writes the lengths
-    const Words in[] = {words(path, B, max_path), words(n_path, B), words(seq_lens_k, B), words(cu_seqlens_q, B + 1ll),
+    const Bytes in[] = {words(path, B, max_path), words(n_path, B), words(seq_lens_k, B), words(cu_seqlens_q, B + 1ll),
                         words(page_table, B, pt_stride)};
-    for (const Words& x : in)
+    for (const Bytes& x : in)
         if (overlap(x, words(new_lens, B))) return IDX_EINVAL;
     return IDX_OK;
 }
@@ -78,13 +78,13 @@ int idx_draft_verify(const void* target_probs, const void* draft_probs, int32_t 
     }
     // a request's CTAs follow the walk each for itself: what they read stays as it is
     auto rows = [&](const void* p, int64_t stride) {
-        return Words{p, T > 0 ? (((__int128)(T - 1) * stride + V) * (int)size + 3) / 4 : 0};
+        return Bytes{p, T > 0 ? ((__int128)(T - 1) * stride + V) * (int)size : 0};
     };
-    const Words reads[] = {rows(target_probs, target_stride), rows(draft_probs, draft_stride), words(tokens, T), words(parents, T),
+    const Bytes reads[] = {rows(target_probs, target_stride), rows(draft_probs, draft_stride), words(tokens, T), words(parents, T),
                            words(coins, T), words(last_coins, B), words(cu_seqlens_q, B + 1ll)};
-    const Words writes[] = {words(path, B, max_path), words(n_path, B), words(out_tokens, B, max_path)};
+    const Bytes writes[] = {words(path, B, max_path), words(n_path, B), words(out_tokens, B, max_path)};
     for (int i = 0; i < 3; ++i) {
-        for (const Words& x : reads)
+        for (const Bytes& x : reads)
             if (overlap(x, writes[i])) return IDX_EINVAL;
         for (int j = 0; j < i; ++j)
             if (overlap(writes[j], writes[i])) return IDX_EINVAL;
@@ -167,12 +167,12 @@ int idx_pages_update(const int32_t* parent, const int32_t* keep, int32_t n_out, 
             if (out[i] && out[i] == out[j]) return IDX_EINVAL;
     }
     // the phases read the lists again that the first one has tested; only new_shares may be shares, and then as a whole
-    const Words reads[] = {words(parent, n_out), words(keep, n_out), words(page_table, B, pt_stride), words(lens, B),
+    const Bytes reads[] = {words(parent, n_out), words(keep, n_out), words(page_table, B, pt_stride), words(lens, B),
                            words(free_pages, free_cap), words(free_span, 2), words(shares, new_shares == shares ? 0 : num_pages)};
-    const Words writes[] = {words(new_table, n_out, new_stride), words(new_lens, n_out), words(new_free, new_free_cap),
+    const Bytes writes[] = {words(new_table, n_out, new_stride), words(new_lens, n_out), words(new_free, new_free_cap),
                             words(new_span, 2), words(copies, n_out, 2), words(new_shares, num_pages)};
     for (int i = 0; i < 6; ++i) {
-        for (const Words& x : reads)
+        for (const Bytes& x : reads)
             if (overlap(x, writes[i])) return IDX_EINVAL;
         for (int j = 0; j < i; ++j)
             if (overlap(writes[j], writes[i])) return IDX_EINVAL;

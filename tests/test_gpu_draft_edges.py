@@ -68,6 +68,29 @@ def test_verify_one_bad_entry(torch, Bn, dt, shifts, drafter):
                     check_verify(torch, Bn, w, 2, Bn.IDX_STATUS_BAD_VALUE)
 
 
+@pytest.mark.parametrize("dt", ["bfloat16", "float16"])
+@pytest.mark.parametrize("V", [7, 4098, 4099])
+def test_verify_outputs_right_behind_16_bit_rows(torch, Bn, dt, V):
+    """Probabilities that begin and end inside a 4-byte word, and a result that begins with the next byte."""
+    w = walk_inputs(torch, [1], V, getattr(torch, dt), 1, V, False)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    memory = torch.zeros(V + 64, dtype=getattr(torch, dt), device="cuda")
+    first = V % 2                          # ends on a whole word
+    row = memory[first:first + V].view(1, V)
+    row.copy_(w["target"].cuda())
+    path = memory[first + V:first + V + 4].view(torch.int32).view(1, 2)
+    assert path.data_ptr() == row.data_ptr() + 2 * V
+    n_path, out, st = torch.zeros(1, **i32), torch.zeros(1, 2, **i32), torch.zeros(1, **i32)
+    args = [torch.zeros(1, **i32), torch.zeros(1, **i32), torch.zeros(1, device="cuda"), torch.tensor(w["last"], dtype=torch.float32, device="cuda"),
+            torch.tensor([0, 1], **i32), 1]
+    Bn.idx_draft_verify(row, None, *args, path, n_path, out, dev_status=st)
+    want = check_verify(torch, Bn, w, 2)
+    assert [path.tolist(), n_path.tolist(), out.tolist()] == list(want) and int(st) == 0
+    path = memory[first + V - 2:first + V + 2].view(torch.int32).view(1, 2)  # from the row's last word on
+    with pytest.raises(Bn.IdxError):
+        Bn.idx_draft_verify(row, None, *args, path, n_path, out)
+
+
 # ------------------------------------------------------------------------------ page copies
 
 @pytest.mark.parametrize("n,layers,page,every", [(64, 16, 8 * 32784, 3), (65, 2, 4352, 1), (7, 1, 16, 2), (1, 3, 8208, 0)])
