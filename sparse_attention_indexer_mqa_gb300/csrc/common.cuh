@@ -140,19 +140,6 @@ inline cudaError_t allow_smem(std::atomic<uint64_t>& done, Kernel* kernel, int b
     return e;
 }
 
-// Lets a kernel run in clusters of more than eight CTAs, once per device.
-template <typename Kernel>
-inline cudaError_t allow_wide_cluster(std::atomic<uint64_t>& done, Kernel* kernel) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-    return e;
-}
-
 // ---- paged cache layout (see idx.h) ------------------------------------------------------
 // MXFP4: byte offset in a page of 16-byte chunk c (scale block c) of in-page token s.
 __device__ __forceinline__ int mx_chunk_off(int P, int s, int c) {

@@ -20,6 +20,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "pages_plan.h"
 
 namespace cg = cooperative_groups;
 
@@ -27,7 +28,7 @@ namespace idx {
 
 namespace {
 
-constexpr int kCtas = 8, kCtasMost = 16, kThreadsP = 1024, kWarpsP = kThreadsP / 32;
+constexpr int kThreadsP = 1024, kWarpsP = kThreadsP / 32;
 
 // Exclusive sum over the CTA of one value per thread, and the total.
 __device__ __forceinline__ int cta_sum(int v, int* warp_sums, int& total) {
@@ -55,8 +56,6 @@ __device__ __forceinline__ int cta_sum(int v, int* warp_sums, int& total) {
 // Dynamic shared memory: three words per next row (heirs and fresh pages take turns, heirs being one per present row), then a
 // bitmap of kSegment pages.
 constexpr int kSegment = 131072;
-constexpr int64_t kMany = 100000;  // table entries and pages from which a wide cluster is taken (23.4 us against 33.3 above; 64 rows
-                                   // 10.8 with eight CTAs, 11.0 with sixteen)
 inline size_t pages_smem(int32_t n_out, int32_t B) {
     return (2 * (size_t)n_out + (size_t)(n_out > B ? n_out : B)) * sizeof(int32_t) + kSegment / 8;
 }
@@ -304,20 +303,45 @@ __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const CopyArgs
         if (at + i * kCopyThreads < n) to[at + i * kCopyThreads] = w[i];
 }
 
+// Clusters of kCtasMost CTAs that the current device takes at once, with all the shared memory that a call may ask for. Asked
+// once per device (64 at most are remembered).
+int wide_clusters() {
+    static std::atomic<uint64_t> known{0}, fit{0};
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (known.load(std::memory_order_acquire) & bit) return (fit.load(std::memory_order_relaxed) & bit) != 0;
+    cudaError_t e = cudaFuncSetAttribute(pages_update_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) {
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = kCtasMost;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(kCtasMost);
+        cfg.blockDim = dim3(kThreadsP);
+        cfg.dynamicSmemBytes = pages_smem(kPagesMaxRows, kPagesMaxRows);
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&n, pages_update_kernel, &cfg);
+    }
+    if (e != cudaSuccess) {
+        cudaGetLastError();  // the narrow cluster is launched all the same
+        n = 0;
+    }
+    if (n > 0) fit.fetch_or(bit, std::memory_order_relaxed);
+    known.fetch_or(bit, std::memory_order_release);
+    return n;
+}
+
 }  // namespace
 
 cudaError_t launch_pages_update(const PagesArgs& a, cudaStream_t st) {
     static std::atomic<uint64_t> allowed{0};
     cudaError_t e = allow_smem(allowed, pages_update_kernel, (int)pages_smem(kPagesMaxRows, kPagesMaxRows));
     if (e != cudaSuccess) return e;
-    // Eight CTAs, sixteen (more than every GPU has to offer, so it is asked for) where there is much to go through.
     const int64_t entries = (int64_t)a.B * a.pt_stride + (int64_t)a.n_out * a.new_stride + a.num_pages;
-    const int ctas = entries > kMany ? kCtasMost : kCtas;
-    if (ctas > kCtas) {
-        static std::atomic<uint64_t> wide{0};
-        e = allow_wide_cluster(wide, pages_update_kernel);
-        if (e != cudaSuccess) return e;
-    }
+    const int ctas = pages_ctas(entries, wide_clusters);
     e = launch_cluster(pages_update_kernel, dim3(ctas), dim3(kThreadsP), ctas, pages_smem(a.n_out, a.B), st, a);
     return e == cudaSuccess ? launch_done(st) : e;  // the library's kernels read lengths and tables before they wait
 }

@@ -2,6 +2,8 @@
 GPU is needed), what the binding refuses and hands on, and the plain forms that the GPU tests compare with."""
 import ctypes as C
 import math
+import os
+import subprocess
 
 import pytest
 import torch
@@ -351,3 +353,28 @@ def test_pages_update_without_any_list_reaches_the_launch(calls):
     pages(shares=z(0), new_shares=z(0), free=z(0), new_free=z(0))
     args = calls[0][1]
     assert args[13] == 0 and args[15] == 0 and args[18] == 0
+
+
+# ------------------------------------------------------------------------------ a device without room for a wide cluster
+
+def test_pages_update_takes_a_narrow_cluster_where_no_wide_one_fits(tmp_path):
+    """The choice, compiled for the host with fakes of the device's answer: some room, none, and a query that failed."""
+    csrc = os.path.join(os.path.dirname(Bn.__file__), "csrc")
+    main = tmp_path / "plan.cpp"
+    main.write_text(r"""
+#include <stdio.h>
+#include "pages_plan.h"
+int main() {
+    const int64_t entries[] = {0, 1, idx::kMany, idx::kMany + 1, int64_t(1) << 40};
+    const int fits[] = {-1, 0, 1, 9};
+    for (int64_t n : entries)
+        for (int f : fits) {
+            int asked = 0;
+            const int ctas = idx::pages_ctas(n, [&] { ++asked; return f; });
+            printf("%d %d ", ctas, asked);
+        }
+}
+""")
+    subprocess.run(["g++", "-std=c++17", "-I" + csrc, str(main), "-o", str(tmp_path / "plan")], check=True)
+    got = [int(x) for x in subprocess.run([str(tmp_path / "plan")], check=True, capture_output=True, text=True).stdout.split()]
+    assert got == [8, 0] * 12 + [8, 1, 8, 1, 16, 1, 16, 1] * 2

@@ -1,9 +1,12 @@
 """The drafting step's operators on the GPU where their inputs are unusual: verification with entries that are no probabilities,
 or large ones, anywhere in rows of any alignment; page copies with passed-over pairs."""
 import math
+import subprocess
+import sys
 
 import pytest
 
+from conftest import ROOT
 from test_gpu_attn import Bn, torch  # noqa: F401  (fixtures)
 from test_gpu_draft import check_verify, walk_inputs
 
@@ -116,3 +119,41 @@ def test_pages_copy_with_passed_over_pairs(torch, Bn, n, layers, page, every, se
     Bn.idx_pages_copy(torch.tensor(pairs, dtype=torch.int32, device="cuda"), pool, pages, page, page, layers=layers,
                       layer_stride=pool.stride(0), dev_status=st)
     assert int(st) == 0 and torch.equal(pool, want)
+
+
+# ------------------------------------------------------------------------------ page rows
+
+FIRST_CALL = r"""
+import torch
+from sparse_attention_indexer_mqa_gb300 import binding as Bn
+i32 = dict(dtype=torch.int32, device="cuda")
+pages, B, width = 120000, 200, 100  # enough for a wide cluster
+table = torch.arange(B * width, **i32).view(B, width)
+lens, parent = torch.full((B,), 64 * width, **i32), torch.arange(B, **i32)
+keep = torch.full((B,), 64 * width // 2, **i32)
+shares, span = torch.zeros(pages, **i32), torch.tensor([0, pages - B * width], **i32)
+free = torch.arange(B * width, pages, **i32)
+new_table, new_lens, new_free = torch.full((B, width), -9, **i32), torch.zeros(B, **i32), torch.full((pages,), -9, **i32)
+new_span, copies, st = torch.zeros(2, **i32), torch.zeros(B, 2, **i32), torch.zeros(1, **i32)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    Bn.idx_pages_update(parent, keep, table, lens, 64, new_table, new_lens, shares, shares, free, span, new_free, new_span, copies,
+                        dev_status=st)
+for _ in range(2):
+    new_free.fill_(-9)
+    g.replay()
+    torch.cuda.synchronize()
+    half = width // 2
+    assert int(st) == 0 and bool((new_table[:, :half] == table[:, :half]).all()) and bool((new_table[:, half:] == -9).all())
+    assert new_lens.tolist() == keep.tolist() and not bool(shares.any()) and bool((copies == -1).all())
+    back = table[:, half:].reshape(-1)
+    assert new_span.tolist() == [0, pages - B * half]
+    assert torch.equal(new_free[:pages - B * half], torch.cat([free, back]))
+print("fine")
+"""
+
+
+def test_first_wide_update_of_a_process_is_captured(torch):
+    """What the device has room for is asked inside the capture."""
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.split() == ["fine"], r.stderr[-2000:]
