@@ -174,8 +174,8 @@ __global__ void __launch_bounds__(kThreadsT, 2) attn_tile_kernel(const AttnArgs 
         const int end = kTree && k0 + j * kKeysT + i < a.n_sel ? front : vis_sel;
         return ent >= 0 && ent < end;
     };
-    // The ranges of a warp's scale bytes (of those that count), into words `at` of the step's four: largest K, smallest K,
-    // largest V, smallest V.
+    // The ranges of the scale bytes that a warp's lanes give (two each), a byte each from the lowest on: largest K, smallest K,
+    // largest V, smallest V. The caller puts the word among the step's four.
     auto ranges_of = [&](uint32_t lo_scale, uint32_t hi_scale) -> uint32_t {
         uint32_t k_hi = 0, k_lo = 255, v_hi = 0, v_lo = 255;
         // a key that does not count makes the range too wide

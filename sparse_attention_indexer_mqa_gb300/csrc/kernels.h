@@ -268,7 +268,7 @@ cudaError_t launch_kv_compact(const CompactArgs& a, cudaStream_t st);
 cudaError_t launch_k_compact(const CompactArgs& a, cudaStream_t st);
 
 // Next rows of a page table out of the present ones (idx_pages_update), copies of pages (idx_pages_copy).
-constexpr int32_t kPagesMaxRows = 16384;  // 8 bytes each in shared memory
+constexpr int32_t kPagesMaxRows = 16384;  // 12 bytes each in shared memory, beside a bitmap of 16 KB (pages.cu)
 struct PagesArgs {
     const int32_t* parent;
     const int32_t* keep;

@@ -56,9 +56,11 @@ __device__ __forceinline__ int cta_sum(int v, int* warp_sums, int& total) {
 // Dynamic shared memory: three words per next row (heirs and fresh pages take turns, heirs being one per present row), then a
 // bitmap of kSegment pages.
 constexpr int kSegment = 131072;
-inline size_t pages_smem(int32_t n_out, int32_t B) {
+constexpr size_t pages_smem(int32_t n_out, int32_t B) {
     return (2 * (size_t)n_out + (size_t)(n_out > B ? n_out : B)) * sizeof(int32_t) + kSegment / 8;
 }
+static_assert(pages_smem(kPagesMaxRows, kPagesMaxRows) + (32 + kCtasMost) * sizeof(int32_t) <= 227 * 1024,
+              "with the kernel's static arrays within a CTA's shared memory");
 
 // put(j, get(j)) for j = first, first + step, .. below end, kBatch loads at a time in flight.
 constexpr int kBatch = 8;
