@@ -720,8 +720,10 @@ int64_t attn_plan(AttnArgs& a, int64_t bytes) {
             want = least(64, least(4 * slots / units, keys / 1024));
             if (units * want < slots + slots / 2) want = least(64, least(slots / units, keys / one_round_keys));
         }
-        // a small tree's step of up to 512 keys stays whole: 9.9 us against 9.7 in two, and the join's launch costs the host 2
-        if (a.tree && !choice.tile && keys <= 512) want = 1;
+        // A small tree's step is cut from 768 keys on, where both parts are shorter than it by three steps of 128: the join's launch
+        // costs the host 2 to 3 us. Whole / in two, replayed: 512 keys 10.1 / 9.7 us (D = 64: 6.2 / 7.1, listed 9.9 / 9.1), 640
+        // 10.8 / 9.9 (6.9 / 7.5, 11.2 / 10.6), 768 12.0 / 9.4 (7.4 / 7.1, 12.5 / 9.2); a call among others 12.5 / 15.2 at 640.
+        if (a.tree && !choice.tile && keys < 768) want = 1;
         if (want < 1) want = 1;
     }
     const int64_t fits = per_split > 0 ? bytes / per_split : 1;

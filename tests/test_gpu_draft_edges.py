@@ -8,7 +8,7 @@ import pytest
 
 from conftest import ROOT
 from test_gpu_attn import Bn, torch  # noqa: F401  (fixtures)
-from test_gpu_draft import check_verify, walk_inputs
+from test_gpu_draft import Tree, check_verify, walk_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -92,6 +92,29 @@ def test_verify_outputs_right_behind_16_bit_rows(torch, Bn, dt, V):
     path = memory[first + V - 2:first + V + 2].view(torch.int32).view(1, 2)  # from the row's last word on
     with pytest.raises(Bn.IdxError):
         Bn.idx_draft_verify(row, None, *args, path, n_path, out)
+
+
+# ------------------------------------------------------------------------------ small trees
+
+@pytest.mark.parametrize("D,Hq,Hkv", [(128, 8, 1), (64, 16, 2)])
+@pytest.mark.parametrize("listed", [False, True])
+def test_small_trees_near_one_length_are_cut_alike(torch, Bn, D, Hq, Hkv, listed):
+    """No length of a step is an exception among its neighbours: whole below 768 keys, in parts from there on."""
+    def wanted(keys):
+        n = 8
+        return Bn.idx_attn_tree_workspace_bytes(n, Hq, Hkv, D, 1, n, 5000 if listed else keys, keys - n if listed else 0)
+    sizes = [256, 384, 511, 512, 513, 520, 600, 640, 766, 767]
+    assert [wanted(k) for k in sizes] == [0] * len(sizes)
+    assert min(wanted(k) for k in (768, 769, 1024, 1536)) > 0
+
+
+@pytest.mark.parametrize("keys", [513, 640, 767, 768, 900])
+@pytest.mark.parametrize("D,Hq,Hkv,k", [(128, 8, 1, 0), (64, 16, 2, 0), (128, 8, 1, 1), (64, 8, 1, 1)])
+def test_small_trees_of_several_steps(torch, Bn, keys, D, Hq, Hkv, k):
+    a = Tree(torch, [keys + 300 if k else keys, 70], [8, 3], Hq, Hkv, D, 64, torch.bfloat16, seed=keys)
+    sel = a.lists(keys - 8, keys).cuda() if k else None
+    a.call(Bn, sel, a.workspace(Bn, keys - 8 if k else 0))
+    a.check(sel)
 
 
 # ------------------------------------------------------------------------------ page copies
