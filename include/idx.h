@@ -525,6 +525,10 @@ int idx_attn_paged(const void* q, int32_t ftype, int64_t T, int32_t q_heads, int
  *   With a list (sel_idx, n_sel entries a row, as in idx_attn_paged) a row attends the listed keys in front of the tree
  *     and the nodes that its mask shows, which are not listed: entries that are negative or front and above are
  *     ignored. The scorers and the top-k give such lists when they are called with causal = 0 and the lengths in front of the tree.
+ *     So a node's ancestors come on top of its n_sel keys, where a sparse layer that takes one token at a time lets them
+ *     compete for the same k: beyond k keys in front the two attend unlike sets, and their probabilities differ. idx_draft_verify
+ *     then emits what a target with this rule would draw. The other rule's result for a row comes from a list and a mask that
+ *     together hold its k best of both; the library has no scorer of nodes under a mask that would choose them.
  *   max_q_len (after min with T) <= 1024 (IDX_EUNSUPPORTED above).
  * All else, the arithmetic and the treatment of bad lengths, pages and NaN codes too, as in idx_attn_paged; the
  * workspace's size by idx_attn_tree_workspace_bytes.
@@ -544,8 +548,8 @@ int idx_attn_tree(const void* q, int32_t ftype, int64_t T, int32_t q_heads, int3
                   size_t workspace_bytes, int32_t* dev_status, cudaStream_t stream);
 
 /*
- * Verification of drafted tokens against the target's probabilities, from given random numbers, so that
- * what is emitted is distributed as if the target had drawn every token itself.
+ * Verification of drafted tokens against the target's probabilities, from given random numbers, so that what is
+ * emitted is distributed as if every token had been drawn from the given rows of target_probs.
  * Sequence b's rows t = cu_seqlens_q[b] .. are the nodes of its tree: node 0 is its last accepted token, and
  *   tokens[t], parents[t] (int32 [T]) are node t - cu_seqlens_q[b]'s drafted token and the node that it follows, a lower
  *   one (a node whose parent is not lower is never reached). A chain is a tree.
