@@ -526,8 +526,8 @@ int idx_attn_paged(const void* q, int32_t ftype, int64_t T, int32_t q_heads, int
  *     and the nodes that its mask shows, which are not listed: entries that are negative or front and above are
  *     ignored. The scorers and the top-k give such lists when they are called with causal = 0 and the lengths in front of the tree.
  *     So a node's ancestors come on top of its n_sel keys, where a sparse layer that takes one token at a time lets them
- *     compete for the same k: beyond k keys in front the two attend unlike sets, and their probabilities differ. idx_draft_verify
- *     then emits what a target with this rule would draw. The other rule's result for a row comes from a list and a mask that
+ *     compete for the same k: where those and the keys in front are more than k, the two attend unlike sets and their
+ *     probabilities differ. idx_draft_verify then emits what a target with this rule would draw. The other rule's result for a row comes from a list and a mask that
  *     together hold its k best of both; the library has no scorer of nodes under a mask that would choose them.
  *   max_q_len (after min with T) <= 1024 (IDX_EUNSUPPORTED above).
  * All else, the arithmetic and the treatment of bad lengths, pages and NaN codes too, as in idx_attn_paged; the
@@ -571,7 +571,8 @@ int idx_attn_tree(const void* q, int32_t ftype, int64_t T, int32_t q_heads, int3
  *   those nodes, increasing; out_tokens int32 [B][max_path]: the tokens of path[1] .. and then the drawn one, n_path of
  *   them. -1 behind. A sequence whose rows break their bounds (as in idx_attn_paged) gets n_path 0 and sets IDX_STATUS_BAD_LEN.
  * V <= 2^20 (IDX_EUNSUPPORTED above). Reads the rows of the nodes that the walk stands on,
- * and of other nodes at most single entries: that of a child's token in its parent's row.
+ * and of other nodes at most single entries: that of a child's token in its parent's row. Rows may lie anywhere;
+ * a rejection takes twice as long and more where the two sides' rows are not at the same place within 16 bytes.
  * The outputs may not overlap the inputs (what lies between two rows belongs to them) or one another (IDX_EINVAL).
  */
 int idx_draft_verify(const void* target_probs, const void* draft_probs, int32_t ptype,

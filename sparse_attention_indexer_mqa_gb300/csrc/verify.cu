@@ -24,7 +24,10 @@
 // loads' latency, four vectors of either row a thread, and the barriers. One chain of 4 drafts,
 // 49999 tokens, bf16: 7.9 us in a graph: launch, three dependent loads, the pass with its barriers, the search; a call from the
 // host takes 10. Before: a CTA per request, sums in fp64 907; a cluster 68; batched loads and the search
-// by a whole CTA 53; no fp64 36; no test per vector 30.
+// by a whole CTA 53; no fp64 36; no test per vector 30. 16-bit probabilities take as long (bf16 28.8, fp16 27.3): passes in turn, not
+// bytes. Rows that begin at other places within 16 bytes for the two sides (a padded vocabulary on one side) have q's entries
+// fetched one by one: 68 us for those 64 trees in fp32, 60 in bf16; a chain of 4 drafts, 50000 tokens, 15.2 against 10.2. An odd
+// vocabulary, rows of every alignment but alike on both sides: 37 in fp32, 40 in bf16.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
