@@ -6,9 +6,10 @@ import sys
 
 import pytest
 
+import draft_ref as dr
 from conftest import ROOT
 from test_gpu_attn import Bn, torch  # noqa: F401  (fixtures)
-from test_gpu_draft import Tree, check_verify, walk_inputs
+from test_gpu_draft import Tree, check_verify, run_verify, walk_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -69,6 +70,27 @@ def test_verify_one_bad_entry(torch, Bn, dt, shifts, drafter):
                 for last in (0.9, 0.1):
                     w["last"] = [last]
                     check_verify(torch, Bn, w, 2, Bn.IDX_STATUS_BAD_VALUE)
+
+
+@pytest.mark.parametrize("B,V,dt", [(100, 70001, "float32"), (200, 70001, "bfloat16"), (310, 1 << 20, "float32"), (310, (1 << 20) - 1, "float16")])
+def test_verify_many_requests_reject_without_drafter(torch, Bn, B, V, dt):
+    """Four, two and one CTA to a request, whose slice's rejected tokens are marked, up to the whole largest vocabulary. One row
+    of probabilities for all nodes."""
+    g = torch.Generator().manual_seed(B)
+    p = (torch.randn(1, V, generator=g) * 3).softmax(-1).to(getattr(torch, dt))
+    heavy = p[0].float().topk(40).indices.tolist()
+    tokens = []
+    for b in range(B):  # heavy ones, which the draw shows if they stay, and the ends
+        pick = torch.randperm(40, generator=g)[:3].tolist()
+        tokens += [0, heavy[pick[0]], heavy[pick[1]], heavy[pick[2]], (0, V - 1, V // 2)[b % 3]]
+    T = 5 * B
+    w = dict(target=p.expand(T, V), draft=None, tokens=tokens, parents=[-1, 0, 0, 0, 0] * B, coins=[0.9999] * T,
+             last=torch.rand(B, generator=g).tolist(), cu=[5 * b for b in range(B + 1)])
+    dev = dict(w, target=p.cuda().expand(T, V))
+    f32 = lambda x: torch.tensor(x, dtype=torch.float32).tolist()  # noqa: E731
+    want = dr.verify(w["target"], None, tokens, w["parents"], f32(w["coins"]), f32(w["last"]), w["cu"], 3)
+    assert min(want[3]) > 2.0 ** -40
+    assert list(run_verify(torch, Bn, dev, 3)) == list(want[:3])
 
 
 @pytest.mark.parametrize("dt", ["bfloat16", "float16"])
